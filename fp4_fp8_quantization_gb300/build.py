@@ -14,7 +14,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoeq.so")
-SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "layout.cu", "route.cu"]
+SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "layout.cu", "route.cu", "gate.cu", "rows.cu",
+           "fp8_block.cu", "gemm_fp8_block.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-fmad=false", "-Xcompiler", "-fPIC",

@@ -566,4 +566,232 @@ moeq_status moeq_grouped_matmul_swiglu_mx(
     return cuda_status(moeq::launch_gemm(ga, stream));
 }
 
+// ------------------------------------------------ router, rows, FP8 blocks
+
+static bool dtype_ok(int dt) { return dt == MOEQ_BF16 || dt == MOEQ_FP16 || dt == MOEQ_FP32; }
+static int64_t dtype_size(int dt) { return dt == MOEQ_FP32 ? 4 : 2; }
+
+static moeq_status gate_args_ok(moeq_dtype dt, const void *logits, int64_t stride,
+                                int64_t num_tokens, int32_t num_experts, int32_t top_k) {
+    if (!dtype_ok(dt) || num_tokens < 0 || num_experts < 1 || top_k < 1 || top_k > num_experts ||
+        stride < num_experts)
+        return MOEQ_ERR_INVALID_ARG;
+    if (num_experts > moeq::kRouteMaxExperts || top_k > moeq::kTopkRowsMax ||
+        num_tokens >= ((int64_t)1 << 31) / top_k)
+        return MOEQ_ERR_UNSUPPORTED;
+    if (num_tokens > 0 && (!logits || !aligned16(logits))) return MOEQ_ERR_INVALID_ARG;
+    return MOEQ_OK;
+}
+
+moeq_status moeq_gate_topk(moeq_dtype dtype, const void *logits, int64_t logit_stride,
+                           int64_t num_tokens, int32_t num_experts, int32_t top_k,
+                           int32_t normalize, float scale, int32_t *topk_ids, float *weights,
+                           moeq_stream_t stream) {
+    const moeq_status st =
+        gate_args_ok(dtype, logits, logit_stride, num_tokens, num_experts, top_k);
+    if (st != MOEQ_OK) return st;
+    if (num_tokens == 0) return MOEQ_OK;
+    if (!topk_ids || !weights || !aligned16(topk_ids) || !aligned16(weights))
+        return MOEQ_ERR_INVALID_ARG;
+    moeq::GateArgs a = {};
+    a.dtype = dtype;
+    a.logits = logits;
+    a.stride = logit_stride;
+    a.num_tokens = num_tokens;
+    a.num_experts = num_experts;
+    a.top_k = top_k;
+    a.normalize = normalize != 0;
+    a.scale = scale;
+    a.ids = topk_ids;
+    a.weights = weights;
+    return cuda_status(moeq::launch_gate(a, stream));
+}
+
+moeq_status moeq_gate_topk_grad(moeq_dtype dtype, const void *logits, int64_t logit_stride,
+                                int64_t num_tokens, int32_t num_experts, int32_t top_k,
+                                int32_t normalize, float scale, const int32_t *topk_ids,
+                                const float *d_weights, void *d_logits, moeq_stream_t stream) {
+    const moeq_status st =
+        gate_args_ok(dtype, logits, logit_stride, num_tokens, num_experts, top_k);
+    if (st != MOEQ_OK) return st;
+    if (num_tokens == 0) return MOEQ_OK;
+    if (!topk_ids || !d_weights || !d_logits || !aligned16(topk_ids) || !aligned16(d_weights) ||
+        !aligned16(d_logits))
+        return MOEQ_ERR_INVALID_ARG;
+    uint32_t *err = device_error_ptr();
+    if (!err) return cuda_status(cudaErrorInvalidDevice);
+    moeq::GateArgs a = {};
+    a.dtype = dtype;
+    a.logits = logits;
+    a.stride = logit_stride;
+    a.num_tokens = num_tokens;
+    a.num_experts = num_experts;
+    a.top_k = top_k;
+    a.normalize = normalize != 0;
+    a.scale = scale;
+    a.ids = const_cast<int32_t *>(topk_ids);
+    a.d_weights = d_weights;
+    a.d_logits = d_logits;
+    a.err = err;
+    return cuda_status(moeq::launch_gate(a, stream));
+}
+
+// Common checks of the calls between tokens and their rows.
+static moeq_status rows_args_ok(moeq_dtype dt, int64_t token_stride, int64_t num_tokens,
+                                int64_t hidden, const int32_t *dst, int32_t top_k,
+                                const float *weights, int64_t total_rows) {
+    if (!dtype_ok(dt) || num_tokens < 0 || hidden <= 0 || top_k < 1 || total_rows < 0 ||
+        token_stride < hidden || hidden * dtype_size(dt) % 16 || token_stride * dtype_size(dt) % 16)
+        return MOEQ_ERR_INVALID_ARG;
+    if (top_k > moeq::kTopkRowsMax || num_tokens >= ((int64_t)1 << 31) / top_k ||
+        total_rows >= (int64_t)1 << 31 || hidden >= (int64_t)1 << 24)
+        return MOEQ_ERR_UNSUPPORTED;
+    if (num_tokens > 0 && (!dst || !aligned16(dst) || !aligned16(weights)))
+        return MOEQ_ERR_INVALID_ARG;
+    return MOEQ_OK;
+}
+
+static moeq_status rows_call(bool spread, moeq_dtype dtype, const void *token_in,
+                             int64_t token_stride, void *token_out, const void *rows_in,
+                             void *rows_out, int64_t num_tokens, int64_t hidden,
+                             const int32_t *dst, int32_t top_k, const float *weights,
+                             float *d_weights, int64_t total_rows, moeq_stream_t stream) {
+    const moeq_status st = rows_args_ok(dtype, token_stride, num_tokens, hidden, dst, top_k,
+                                        weights, total_rows);
+    if (st != MOEQ_OK) return st;
+    if (num_tokens == 0) return MOEQ_OK;
+    // the token side is always there; the row side may have no rows
+    const void *tok = spread ? token_in : token_out, *rows = spread ? rows_out : rows_in;
+    if (!tok || !aligned16(tok) || !aligned16(rows) || (total_rows > 0 && !rows))
+        return MOEQ_ERR_INVALID_ARG;
+    if (d_weights) {
+        const void *other = spread ? rows_in : token_in;
+        const bool needed = !spread || total_rows > 0;
+        if (!aligned16(d_weights) || !aligned16(other) || (needed && !other))
+            return MOEQ_ERR_INVALID_ARG;
+    }
+    uint32_t *err = device_error_ptr();
+    if (!err) return cuda_status(cudaErrorInvalidDevice);
+    const moeq::RowsArgs a{(int)dtype, spread, token_in, token_stride, token_out, rows_in, rows_out,
+                           dst, weights, d_weights, num_tokens, total_rows, hidden, top_k, err};
+    return cuda_status(moeq::launch_topk_rows(a, stream));
+}
+
+moeq_status moeq_permute_topk(moeq_dtype dtype, const void *tokens, int64_t token_stride,
+                              int64_t num_tokens, int64_t hidden, const int32_t *dst_info,
+                              int32_t top_k, const float *weights, void *rows, int64_t total_rows,
+                              moeq_stream_t stream) {
+    return rows_call(true, dtype, tokens, token_stride, nullptr, nullptr, rows, num_tokens, hidden,
+                     dst_info, top_k, weights, nullptr, total_rows, stream);
+}
+
+moeq_status moeq_permute_topk_grad(moeq_dtype dtype, const void *d_rows, int64_t total_rows,
+                                   int64_t num_tokens, int64_t hidden, const int32_t *dst_info,
+                                   int32_t top_k, const float *weights, void *d_tokens,
+                                   const void *tokens, int64_t token_stride, float *d_weights,
+                                   moeq_stream_t stream) {
+    return rows_call(false, dtype, tokens, tokens ? token_stride : hidden, d_tokens, d_rows, nullptr,
+                     num_tokens, hidden, dst_info, top_k, weights, d_weights, total_rows, stream);
+}
+
+moeq_status moeq_combine_topk(moeq_dtype dtype, const void *rows, int64_t total_rows,
+                              int64_t num_tokens, int64_t hidden, const int32_t *dst_info,
+                              int32_t top_k, const float *weights, void *out,
+                              moeq_stream_t stream) {
+    return rows_call(false, dtype, nullptr, hidden, out, rows, nullptr, num_tokens, hidden, dst_info,
+                     top_k, weights, nullptr, total_rows, stream);
+}
+
+moeq_status moeq_combine_topk_grad(moeq_dtype dtype, const void *d_out, int64_t d_out_stride,
+                                   int64_t num_tokens, int64_t hidden, const int32_t *dst_info,
+                                   int32_t top_k, const float *weights, void *d_rows,
+                                   int64_t total_rows, const void *rows, float *d_weights,
+                                   moeq_stream_t stream) {
+    return rows_call(true, dtype, d_out, d_out_stride, nullptr, rows, d_rows, num_tokens, hidden,
+                     dst_info, top_k, weights, d_weights, total_rows, stream);
+}
+
+static moeq_status fp8_block_call(const void *in, int64_t stride, int64_t rows, int64_t K,
+                                  const int32_t *dst, int32_t top_k, int64_t out_rows, bool swiglu,
+                                  uint8_t *out, float *scales, moeq_stream_t stream) {
+    if (rows < 0 || K <= 0 || K % 16 || stride < (swiglu ? 2 * K : K) || stride % 8 || out_rows < 0)
+        return MOEQ_ERR_INVALID_ARG;
+    if (rows >= ((int64_t)1 << 31) / top_k || K >= (int64_t)1 << 31 || out_rows >= (int64_t)1 << 31)
+        return MOEQ_ERR_UNSUPPORTED;
+    if (rows == 0) return MOEQ_OK;
+    if (!in || !aligned16(in) || !aligned16(out) || !aligned16(scales) || (dst && !aligned16(dst)))
+        return MOEQ_ERR_INVALID_ARG;
+    if (out_rows > 0 && (!out || !scales)) return MOEQ_ERR_INVALID_ARG;
+    uint32_t *err = device_error_ptr();
+    if (!err) return cuda_status(cudaErrorInvalidDevice);
+    const moeq::Fp8BlockArgs a{in, stride, rows, K, dst, top_k, out_rows, swiglu, out, scales, err};
+    return cuda_status(moeq::launch_fp8_block(a, stream));
+}
+
+moeq_status moeq_quantize_fp8_block(const void *in, int64_t in_row_stride, int64_t rows, int64_t K,
+                                    uint8_t *out, float *scales, moeq_stream_t stream) {
+    return fp8_block_call(in, in_row_stride, rows, K, nullptr, 1, rows, false, out, scales, stream);
+}
+
+moeq_status moeq_quantize_fp8_block_topk(const void *tokens, int64_t token_stride,
+                                         int64_t num_tokens, int64_t K, const int32_t *dst_info,
+                                         int32_t top_k, uint8_t *out, float *scales,
+                                         int64_t total_rows, moeq_stream_t stream) {
+    if (top_k < 1) return MOEQ_ERR_INVALID_ARG;
+    if (top_k > moeq::kTopkRowsMax) return MOEQ_ERR_UNSUPPORTED;
+    if (num_tokens > 0 && !dst_info) return MOEQ_ERR_INVALID_ARG;
+    return fp8_block_call(tokens, token_stride, num_tokens, K, dst_info, top_k, total_rows, false,
+                          out, scales, stream);
+}
+
+moeq_status moeq_swiglu_quantize_fp8_block(const void *y, int64_t rows, int64_t I, uint8_t *out,
+                                           float *scales, moeq_stream_t stream) {
+    return fp8_block_call(y, 2 * I, rows, I, nullptr, 1, rows, true, out, scales, stream);
+}
+
+moeq_status moeq_quantize_fp8_block_weight(const void *w, int64_t num_experts, int64_t N, int64_t K,
+                                           uint8_t *out, float *scales, moeq_stream_t stream) {
+    if (num_experts < 0 || N < 0 || K <= 0 || K % 16) return MOEQ_ERR_INVALID_ARG;
+    // the launch grid holds one CTA per 128 x 128 block
+    if (num_experts > 65535 || (N + 127) / 128 > 65535 || K >= (int64_t)1 << 31)
+        return MOEQ_ERR_UNSUPPORTED;
+    if (num_experts == 0 || N == 0) return MOEQ_OK;
+    if (!w || !out || !scales || !aligned16(w) || !aligned16(out) || !aligned16(scales))
+        return MOEQ_ERR_INVALID_ARG;
+    return cuda_status(moeq::launch_fp8_block_weight(w, num_experts, N, K, out, scales, stream));
+}
+
+moeq_status moeq_grouped_matmul_fp8_block(void *c, const uint8_t *a, const uint8_t *b,
+                                          const float *a_scales, const float *b_scales,
+                                          const uint32_t *a_offsets, const int32_t *expert_ids,
+                                          int64_t total_tokens, int64_t N, int64_t K,
+                                          int32_t num_experts, int32_t max_tokens_per_expert,
+                                          int32_t num_active_experts, moeq_stream_t stream) {
+    (void)max_tokens_per_expert;
+    if (!groups_ok(a_offsets, expert_ids, num_experts, num_active_experts))
+        return MOEQ_ERR_INVALID_ARG;
+    if (total_tokens < 0 || N <= 0 || K <= 0 || K % 16 || N % 8) return MOEQ_ERR_INVALID_ARG;
+    if (total_tokens >= (int64_t)1 << 31 || N >= (int64_t)1 << 31 || K >= (int64_t)1 << 31 ||
+        num_active_experts > moeq::kMaxGroups)
+        return MOEQ_ERR_UNSUPPORTED;
+    if (!b || !b_scales || !aligned16(b) || !aligned16(b_scales)) return MOEQ_ERR_INVALID_ARG;
+    if (num_active_experts == 0 || total_tokens == 0) return MOEQ_OK;
+    if (!c || !a || !a_scales || !aligned16(c) || !aligned16(a) || !aligned16(a_scales))
+        return MOEQ_ERR_INVALID_ARG;
+    uint32_t *err = device_error_ptr();
+    if (!err) return cuda_status(cudaErrorInvalidDevice);
+    moeq::GemmBlockArgs ga = {};
+    ga.groups = make_groups(a_offsets, nullptr, expert_ids, num_active_experts, num_experts,
+                            total_tokens, 0);
+    ga.N = N;
+    ga.K = K;
+    ga.a = a;
+    ga.b = b;
+    ga.a_scales = a_scales;
+    ga.b_scales = b_scales;
+    ga.c = c;
+    ga.err = err;
+    return cuda_status(moeq::launch_gemm_fp8_block(ga, stream));
+}
+
 }  // extern "C"

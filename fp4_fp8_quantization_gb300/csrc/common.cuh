@@ -858,4 +858,61 @@ __device__ __forceinline__ void st_global_v4(void *p, uint32_t a, uint32_t b, ui
                  : "memory");
 }
 
+// ------------------------------------- shared staging and tensor stores
+
+__device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z,
+                                             uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z),
+                 "r"(w)
+                 : "memory");
+}
+
+// TMA tensor store of a shared-memory box (bulk async-group of this thread)
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     map),
+                 "r"(src), "r"(x), "r"(y)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// the thread's bulk stores have read their shared memory / have completed
+__device__ __forceinline__ void bulk_wait_read_all() {
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() {
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+
+// ------------------------------------------------------ GEMM tile ids
+// A tile id of a grouped GEMM -> (group, m-block, n-block), n fastest;
+// prefix[g] is the number of tiles before group g.
+struct Tile {
+    int g, mb, nb;
+};
+
+__device__ __forceinline__ Tile decode_tile(const uint32_t *prefix, int G, uint32_t t, int NB) {
+    int lo = 0, hi = G;
+    while (hi - lo > 1) {
+        int mid = (lo + hi) >> 1;
+        if (prefix[mid] <= t) lo = mid; else hi = mid;
+    }
+    uint32_t local = t - prefix[lo];
+    Tile r;
+    r.g = lo;
+    r.mb = (int)(local / (uint32_t)NB);
+    r.nb = (int)(local % (uint32_t)NB);
+    return r;
+}
+
 }  // namespace moeq

@@ -1,0 +1,173 @@
+// FP8 (E4M3) quantization with one fp32 scale for each block of 128: 1 x 128
+// blocks of rows (activations: plain rows, tokens copied to their routed
+// rows, SwiGLU of a gate/up tensor) and 128 x 128 blocks of weights.
+//
+//   s = max(amax / 448, 2^-126),  r = 1 / s,  q = E4M3(x * r)
+//
+// each step one fp32 operation, round to nearest even, saturating.  The floor
+// keeps r finite; an all-zero block has the floor as its scale.  A NaN does
+// not enter amax and stays a NaN code of its own element; an infinity makes
+// its block's scale infinite and itself a NaN code.
+//
+// All are streaming kernels, bound by memory: 2 bytes read and 1 written per
+// element (1 per choice for routed tokens, each token read and quantized
+// once; 4 read for SwiGLU).
+#include "common.cuh"
+#include "launch.h"
+
+namespace moeq {
+
+namespace {
+
+constexpr int kBlk = 128;
+constexpr int kWarps = 4;
+
+__device__ __forceinline__ float block_scale(float amax) {
+    return fmaxf(__fdiv_rn(amax, 448.0f), __uint_as_float(0x00800000u));
+}
+
+// fmaxf drops a NaN operand, so a NaN never becomes the amax.
+__device__ __forceinline__ float amax8(const float (&x)[8]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+    return m;
+}
+
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float r) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(x[i], r);
+    return make_uint2(e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16),
+                      e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16));
+}
+
+__device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+struct BlockParams {
+    const uint16_t *in;
+    int64_t stride, rows, K;
+    const int32_t *dst;  // null: row t goes to row t
+    int top_k;
+    int64_t out_rows;
+    uint8_t *out;
+    float *scales;
+    uint32_t *err;
+};
+
+// One warp per row; 16 lanes hold a block, 8 elements each.
+template <bool SWIGLU>
+__global__ void __launch_bounds__(kWarps * 32) fp8_block_kernel(BlockParams p) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (t >= p.rows) return;
+    const int64_t KB = (p.K + kBlk - 1) / kBlk;
+    for (int64_t k0 = 0; k0 < p.K; k0 += 256) {
+        const int64_t k = k0 + lane * 8;
+        float x[8] = {};
+        if (k < p.K) {
+            if constexpr (SWIGLU) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(p.in + t * p.stride + 2 * k);
+                const uint4 a = src[0], b = src[1];
+                const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {  // gate in the low half, up in the high
+                    const F2 h = swiglu2(
+                        __uint_as_float(w[i] << 16), __uint_as_float(w[i + 1] << 16),
+                        __uint_as_float(w[i] & 0xFFFF0000u), __uint_as_float(w[i + 1] & 0xFFFF0000u));
+                    x[i] = f2_lo(h);
+                    x[i + 1] = f2_hi(h);
+                }
+            } else {
+                unpack8(*reinterpret_cast<const uint4 *>(p.in + t * p.stride + k), x);
+            }
+        }
+        float m = amax8(x);
+#pragma unroll
+        for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        const float s = block_scale(m);
+        const uint2 q = codes8(x, __fdiv_rn(1.0f, s));
+        if (k >= p.K) continue;
+        for (int j = 0; j < (p.dst ? p.top_k : 1); ++j) {
+            int64_t r = t;
+            if (p.dst) {
+                r = __ldg(p.dst + t * p.top_k + j);
+                if (r < 0 || r >= p.out_rows) {
+                    if (r != -1 && k == 0) set_error(p.err, MOEQ_DEVERR_BAD_INDEX);
+                    continue;
+                }
+            }
+            *reinterpret_cast<uint2 *>(p.out + r * p.K + k) = q;
+            if ((lane & 15) == 0) p.scales[r * KB + k / kBlk] = s;
+        }
+    }
+}
+
+// One CTA per 128 x 128 weight block (grid: K blocks, N blocks, experts): 16
+// threads hold a row's 128 columns, 16 rows at a time.
+__global__ void __launch_bounds__(256) fp8_block_weight_kernel(const uint16_t *w, int64_t N,
+                                                               int64_t K, uint8_t *out,
+                                                               float *scales) {
+    pdl_wait();
+    pdl_trigger();
+    __shared__ float part[8];
+    const int64_t e = blockIdx.z, n0 = (int64_t)blockIdx.y * kBlk;
+    const int64_t k = (int64_t)blockIdx.x * kBlk + (threadIdx.x & 15) * 8;
+    uint4 u[8];
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t n = n0 + i * 16 + (threadIdx.x >> 4);
+        u[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (n < N && k < K) u[i] = *reinterpret_cast<const uint4 *>(w + (e * N + n) * K + k);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float x[8];
+        unpack8(u[i], x);
+        m = fmaxf(m, amax8(x));
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, part[i]);
+    const float s = block_scale(m), r = __fdiv_rn(1.0f, s);
+    if (threadIdx.x == 0) scales[(e * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x] = s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t n = n0 + i * 16 + (threadIdx.x >> 4);
+        float x[8];
+        unpack8(u[i], x);
+        if (n < N && k < K) *reinterpret_cast<uint2 *>(out + (e * N + n) * K + k) = codes8(x, r);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_block(const Fp8BlockArgs &a, cudaStream_t s) {
+    const BlockParams p{static_cast<const uint16_t *>(a.in), a.stride, a.rows, a.K, a.dst,
+                        a.top_k, a.out_rows, a.out, a.scales, a.err};
+    const unsigned blocks = (unsigned)((a.rows + kWarps - 1) / kWarps);
+    return launch_pdl(a.swiglu ? fp8_block_kernel<true> : fp8_block_kernel<false>, blocks,
+                      kWarps * 32, 0, s, p);
+}
+
+cudaError_t launch_fp8_block_weight(const void *w, int64_t E, int64_t N, int64_t K, uint8_t *out,
+                                    float *scales, cudaStream_t s) {
+    const dim3 grid((unsigned)((K + kBlk - 1) / kBlk), (unsigned)((N + kBlk - 1) / kBlk), (unsigned)E);
+    return launch_pdl(fp8_block_weight_kernel, grid, 256, 0, s, static_cast<const uint16_t *>(w), N,
+                      K, out, scales);
+}
+
+}  // namespace moeq

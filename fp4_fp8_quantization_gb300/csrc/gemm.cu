@@ -45,6 +45,7 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "tensormap.h"
 
 // Scale-load warp (1) or scale loads issued by the A/B producer (0).
 #ifndef MOEQ_SF_LOADER
@@ -178,24 +179,6 @@ struct Params {
     uint32_t *err;
 };
 
-struct Tile {
-    int g, mb, nb;
-};
-
-__device__ __forceinline__ Tile decode_tile(const uint32_t *prefix, int G, uint32_t t, int NB) {
-    int lo = 0, hi = G;
-    while (hi - lo > 1) {
-        int mid = (lo + hi) >> 1;
-        if (prefix[mid] <= t) lo = mid; else hi = mid;
-    }
-    uint32_t local = t - prefix[lo];
-    Tile r;
-    r.g = lo;
-    r.mb = (int)(local / (uint32_t)NB);
-    r.nb = (int)(local % (uint32_t)NB);
-    return r;
-}
-
 // Tiles of group g (0 when the group is empty or its offsets / expert id /
 // scale rows are unusable; those errors are reported by CTA 0 only).
 template <class C, int EPI>
@@ -221,41 +204,6 @@ __device__ __forceinline__ uint32_t group_tiles(const Params &p, int g, int NB, 
     }
     // a CTA pair takes two consecutive m-blocks of the group
     return ((rows + C::BM - 1) / C::BM + C::PAIR - 1) / C::PAIR * (uint32_t)NB;
-}
-
-__device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z,
-                                             uint32_t w) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z),
-                 "r"(w)
-                 : "memory");
-}
-
-// TMA tensor store of a shared-memory box (bulk async-group of this thread)
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t src, int x, int y) {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                     map),
-                 "r"(src), "r"(x), "r"(y)
-                 : "memory");
-}
-__device__ __forceinline__ void bulk_commit() {
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-// the thread's bulk stores have read their shared memory / have completed
-__device__ __forceinline__ void bulk_wait_read_all() {
-    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-__device__ __forceinline__ void bulk_wait_all() {
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
-
-
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(a)
-                 : "memory");
-    return v;
 }
 
 // Epilogue of one 32-column accumulator chunk of this thread's row.
@@ -1028,39 +976,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
 // ------------------------------------------------------------------ host
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    // looked up once (thread-safe static initialisation)
-    static const EncodeTiledFn fn = []() -> EncodeTiledFn {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
-                                             cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            return reinterpret_cast<EncodeTiledFn>(ptr);
-        return nullptr;
-    }();
-    return fn;
-}
-
-// uint8 tensor map with 128-byte swizzled boxes of box_rows x 128 bytes.
-bool make_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims,
-              const cuuint64_t *strides, cuuint32_t box_rows) {
-    EncodeTiledFn enc = encode_fn();
-    if (!enc) return false;
-    cuuint32_t box[3] = {128, box_rows, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void *>(base),
-                     dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
-
 // uint8 tensor map over `bytes` bytes viewed as rows of 256 bytes (no
 // swizzle), boxes of box_rows rows: the scale buffers, whose 512-byte atoms
 // are two such rows.
@@ -1094,18 +1009,6 @@ bool make_sfb_map(CUtensorMap *m, const void *base, int64_t row_blocks, int64_t 
                      box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
-}
-
-int sm_count() {
-    static std::atomic<int> cache[kMaxDevices];
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= kMaxDevices) dev = 0;
-    return cached_per_device(cache, dev, [dev]() {
-        int n = 0;
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        return n > 0 ? n : 1;
-    });
 }
 
 template <int KIND, int EPI, int BN, int STAGES, int ACC_BUFS, int EPI_WARPS, int SF_WARPS = 1,

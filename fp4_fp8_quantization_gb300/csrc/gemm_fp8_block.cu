@@ -1,0 +1,439 @@
+// Grouped FP8 GEMM with a scale for each block of 128 of the reduction:
+//
+//   c[t, n] = bf16( sum_kb (sa[t, kb] sb[e, n / 128, kb]) P_kb[t, n] ),
+//   P_kb[t, n] = sum over k in block kb of a[t, k] b[e, n, k]
+//
+// The tensor cores can only apply power-of-two block scales, so P_kb (fp32,
+// in tensor memory) is scaled outside: the warps that would be an epilogue
+// run along the whole reduction.  Per K block of 128, one 128-byte swizzle
+// row per operand row:
+//  * warp 0 (one thread) loads the A and B tiles by TMA into a ring of
+//    stages (columns past K and rows past N arrive as zeros);
+//  * warp 1 (one thread) issues the block's four MMAs into one of NBUF
+//    tensor-memory accumulators, overwriting it;
+//  * the other warps read it (one row per thread, COLS_W columns per warp)
+//    and add it, times the row's and column block's scales, to sums that stay
+//    in registers for the whole tile.  A warp's columns lie in one 128-column
+//    block, so the factor is one number per thread and K block: the pass is
+//    one paired fused multiply-add per two elements.
+// Persistent CTAs, one per SM, walk the tiles of all groups (n fastest).
+// Every wait is bounded and sets the device error word instead of hanging.
+#include <cstring>
+
+#include "common.cuh"
+#include "launch.h"
+#include "tensormap.h"
+
+namespace moeq {
+
+namespace {
+
+template <int BN_, int STAGES_, int SUM_WARPS_>
+struct BlockCfg {
+    static constexpr int BM = 128, BN = BN_, STAGES = STAGES_, SUM_WARPS = SUM_WARPS_;
+    static constexpr int BK = 128;
+    static constexpr int NBUF = 512 / BN < 4 ? 512 / BN : 4;   // accumulators
+    static constexpr int TMEM_COLS = NBUF * BN;
+    static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int COLS_W = BN / (SUM_WARPS / 4), CHUNKS_W = COLS_W / 32;
+    static constexpr int SUM_WARP0 = 4;  // warps 0 and 1 work, 2 and 3 fill their warpgroup
+    static constexpr int THREADS = 32 * (SUM_WARP0 + SUM_WARPS);
+    // 128 sums per thread do not fit the 168 registers that 384 threads leave
+    // each: the control warpgroup gives up registers to the two sum warpgroups
+    // (setmaxnreg redistributes exactly the registers the block is launched
+    // with; the host checks the compiled count before launching)
+    static constexpr bool NREG = COLS_W == 128;
+    static constexpr int LAUNCH_REGS = 65536 / THREADS / 8 * 8;
+    static constexpr int NREG_CTRL = 72;
+    static constexpr int NREG_SUM =
+        NREG ? (THREADS * LAUNCH_REGS - 32 * SUM_WARP0 * NREG_CTRL) / (32 * SUM_WARPS) / 8 * 8 : 0;
+    static constexpr int BUF_BYTES = 2048;  // staging of a 32 x 32 bf16 chunk per warp
+    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SUM_WARPS * BUF_BYTES + 1024;
+    static_assert(SMEM_BYTES + 4 * (kMaxGroups + 1) + 512 <= 227 * 1024, "shared memory per CTA");
+    static_assert(!NREG || (NREG_SUM >= LAUNCH_REGS && NREG_SUM <= 248 &&
+                            32 * SUM_WARP0 * NREG_CTRL + 32 * SUM_WARPS * NREG_SUM <=
+                                THREADS * LAUNCH_REGS),
+                  "register split by warpgroups");
+    static_assert(COLS_W % 32 == 0 && 128 % COLS_W == 0, "a warp's columns share one scale");
+};
+
+struct BlockGemmParams {
+    const uint32_t *offsets;
+    const int32_t *expert_ids;
+    int num_groups, num_experts;
+    int64_t total_rows;
+    int N, K;
+    const float *a_scales, *b_scales;
+    uint16_t *c;
+    uint32_t *err;
+};
+
+// Waits for the thread's tensor-memory loads; r is written by them.
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+// Scales 4 q .. 4 q + 3 of a row of kb (0 past its end): 16 bytes at once
+// where every row is aligned for it.
+__device__ __forceinline__ float4 load_scales4(const float *row, int q, int kb) {
+    if ((kb & 3) == 0) return __ldg(reinterpret_cast<const float4 *>(row) + q);
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = 4 * q + i < kb ? __ldg(row + 4 * q + i) : 0.0f;
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1)
+    gemm_fp8_block_kernel(const __grid_constant__ CUtensorMap tmA,
+                          const __grid_constant__ CUtensorMap tmB,
+                          const __grid_constant__ CUtensorMap tmC, const BlockGemmParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full_bar[C::STAGES], empty_bar[C::STAGES];
+    __shared__ uint64_t tfull_bar[C::NBUF], tempty_bar[C::NBUF];
+    __shared__ uint64_t drain_bar;
+    __shared__ uint32_t tmem_slot, stages_done;
+    __shared__ int abort_flag;
+    __shared__ uint32_t prefix[kMaxGroups + 1];
+
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int G = p.num_groups;
+    const int NB = (p.N + C::BN - 1) / C::BN;
+    const int KB = (p.K + C::BK - 1) / C::BK;
+    volatile int *abort_v = &abort_flag;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&full_bar[s], 1);
+            mbar_init(&empty_bar[s], 1);
+        }
+        for (int b = 0; b < C::NBUF; ++b) {
+            mbar_init(&tfull_bar[b], 1);
+            mbar_init(&tempty_bar[b], C::SUM_WARPS);
+        }
+        mbar_init(&drain_bar, 1);
+        abort_flag = 0;
+        stages_done = 0;
+        prefix[0] = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmB);
+        prefetch_tensormap(&tmC);
+    }
+    // everything above touches only shared memory and the kernel parameters
+    pdl_wait();
+    if (warp == 1) {
+        tmem_alloc(&tmem_slot, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    // tiles of each group; an unusable group has none and is reported once
+    for (int g = threadIdx.x; g < G; g += blockDim.x) {
+        const uint32_t r0 = __ldg(p.offsets + g), r1 = __ldg(p.offsets + g + 1);
+        const int e = __ldg(p.expert_ids + g);
+        uint32_t n = 0;
+        if (r1 < r0 || (int64_t)r1 > p.total_rows) {
+            if (blockIdx.x == 0) set_error(p.err, MOEQ_DEVERR_BAD_OFFSETS);
+        } else if (e < 0 || e >= p.num_experts) {
+            if (blockIdx.x == 0) set_error(p.err, MOEQ_DEVERR_BAD_EXPERT);
+        } else {
+            n = (r1 - r0 + C::BM - 1) / C::BM * (uint32_t)NB;
+        }
+        prefix[g + 1] = n;
+    }
+    __syncthreads();
+    if (warp == 0) {  // inclusive prefix over prefix[1..G]
+        uint32_t carry = 0;
+        for (int base = 0; base < G; base += 32) {
+            const int g = base + lane;
+            uint32_t v = g < G ? prefix[g + 1] : 0u;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t t = __shfl_up_sync(0xFFFFFFFFu, v, o);
+                if (lane >= o) v += t;
+            }
+            if (g < G) prefix[g + 1] = carry + v;
+            carry += __shfl_sync(0xFFFFFFFFu, v, 31);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t total = prefix[G];
+    const uint32_t tmem = tmem_slot;
+
+    if (warp < C::SUM_WARP0) {
+    if constexpr (C::NREG) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::NREG_CTRL));
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t pol = policy_evict_last();
+            int stage = 0;
+            uint32_t phase = 0, issued = 0;
+            bool ok = true;
+            for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
+                const Tile tl = decode_tile(prefix, G, t, NB);
+                const int e = __ldg(p.expert_ids + tl.g);
+                const int row0 = (int)__ldg(p.offsets + tl.g) + tl.mb * C::BM;
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_v, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *sa = smem + stage * C::STAGE_BYTES;
+                    mbar_arrive_expect_tx(&full_bar[stage], C::STAGE_BYTES);
+                    tma_load_2d(sa, &tmA, &full_bar[stage], kb * C::BK, row0, pol);
+                    tma_load_3d(sa + C::A_BYTES, &tmB, &full_bar[stage], kb * C::BK,
+                                tl.nb * C::BN, e, pol);
+                    ++issued;
+                    if (++stage == C::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            stages_done = issued;
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, bphase = 0;
+            bool ok = true;
+            for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!mbar_wait(&tempty_bar[buf], bphase ^ 1u, abort_v, p.err) ||
+                        !mbar_wait(&full_bar[stage], phase, abort_v, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(smem + stage * C::STAGE_BYTES);
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_f8f6f4(tmem + buf * C::BN, sdesc_sw128(sa + ks * 32),
+                                   sdesc_sw128(sa + C::A_BYTES + ks * 32),
+                                   idesc_f8_e4m3(C::BM, C::BN), ks ? 1u : 0u);
+                    tc_commit(&empty_bar[stage]);
+                    tc_commit(&tfull_bar[buf]);
+                    if (++stage == C::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    if (++buf == C::NBUF) {
+                        buf = 0;
+                        bphase ^= 1u;
+                    }
+                }
+            }
+            // every tcgen05 operation issued here completes before TMEM is freed
+            tc_commit(&drain_bar);
+            mbar_drain(&drain_bar, 0);
+        }
+    }
+    } else {
+        if constexpr (C::NREG)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::NREG_SUM));
+        const int quad = warp & 3;               // TMEM lanes 32 quad .. 32 quad + 31
+        const int cgrp = (warp - C::SUM_WARP0) >> 2;        // columns COLS_W cgrp ...
+        const uint32_t toff = ((uint32_t)(quad * 32) << 16) + cgrp * C::COLS_W;
+        const uint32_t sbuf = smem_u32(smem + C::STAGES * C::STAGE_BYTES) + (warp - C::SUM_WARP0) * C::BUF_BYTES;
+        const int NBLK = (p.N + 127) / 128;
+        int buf = 0;
+        uint32_t bphase = 0;
+        bool ok = true;
+        for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
+            const Tile tl = decode_tile(prefix, G, t, NB);
+            const int e = __ldg(p.expert_ids + tl.g);
+            const uint32_t r0 = __ldg(p.offsets + tl.g);
+            const int left = (int)(__ldg(p.offsets + tl.g + 1) - r0) - (tl.mb * C::BM + quad * 32);
+            const int nvalid = left <= 0 ? 0 : (left >= 32 ? 32 : left);  // this warp's rows
+            const int64_t row = (int64_t)r0 + tl.mb * C::BM + quad * 32 + lane;
+            const int ncol0 = tl.nb * C::BN + cgrp * C::COLS_W;
+            const bool work = nvalid > 0 && ncol0 < p.N;
+            // a row past the group's end takes the last row's scales (its sums are dropped)
+            const float *sa = p.a_scales + (lane < nvalid ? row : row - lane + max(nvalid - 1, 0)) * KB;
+            const float *sb = p.b_scales + ((int64_t)e * NBLK + min(ncol0 / 128, NBLK - 1)) * KB;
+            F2 acc[C::COLS_W / 2];
+#pragma unroll
+            for (int i = 0; i < C::COLS_W / 2; ++i) acc[i] = f2(0.0f, 0.0f);
+            float4 a4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b4 = a4, an = a4, bn = a4;
+            if (work) {
+                an = load_scales4(sa, 0, KB);
+                bn = load_scales4(sb, 0, KB);
+            }
+#pragma unroll 1
+            for (int kb = 0; kb < KB; ++kb) {
+                const int j = kb & 3;
+                if (j == 0) {
+                    a4 = an;
+                    b4 = bn;
+                    if (work && kb + 4 < KB) {
+                        an = load_scales4(sa, (kb >> 2) + 1, KB);
+                        bn = load_scales4(sb, (kb >> 2) + 1, KB);
+                    }
+                }
+                const float av = j == 0 ? a4.x : j == 1 ? a4.y : j == 2 ? a4.z : a4.w;
+                const float bv = j == 0 ? b4.x : j == 1 ? b4.y : j == 2 ? b4.z : b4.w;
+                const float s = __fmul_rn(av, bv);
+                const F2 s2 = f2(s, s);
+                if (!mbar_wait(&tfull_bar[buf], bphase, abort_v, p.err)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (work) {
+#pragma unroll
+                    for (int ch = 0; ch < C::CHUNKS_W; ++ch) {
+                        uint32_t r[32];
+                        tmem_ld32(tmem + buf * C::BN + toff + ch * 32, r);
+                        tmem_ld_wait32(r);
+                        if (ch == C::CHUNKS_W - 1) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&tempty_bar[buf]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            acc[ch * 16 + i] =
+                                fma2(f2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), s2,
+                                     acc[ch * 16 + i]);
+                    }
+                } else {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&tempty_bar[buf]);
+                }
+                if (++buf == C::NBUF) {
+                    buf = 0;
+                    bphase ^= 1u;
+                }
+            }
+            if (!ok || !work) continue;
+            // bf16 out through the warp's 32 x 32 staging buffer (64-byte rows
+            // whose 16-byte pieces are XOR-swizzled by row pair, the tensor
+            // map's 64-byte swizzle): one tensor store where all 32 rows lie in
+            // the group, else the group's rows by four lanes each
+#pragma unroll
+            for (int ch = 0; ch < C::CHUNKS_W; ++ch) {
+                const int nc = ncol0 + ch * 32;
+                if (nc >= p.N) break;
+                if (lane == 0) bulk_wait_read_all();
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const F2 v = acc[ch * 16 + j * 4 + i];
+                        w[i] = f32_to_bf16_bits(f2_lo(v)) | (f32_to_bf16_bits(f2_hi(v)) << 16);
+                    }
+                    st_shared_v4(sbuf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), w[0], w[1], w[2],
+                                 w[3]);
+                }
+                if (nvalid == 32) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&tmC, sbuf, nc, (int)(row - lane));
+                        bulk_commit();
+                    }
+                } else {
+                    __syncwarp();
+                    const int k = lane & 3, n = nc + k * 8;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int rr = (lane >> 2) + 8 * i;
+                        const uint4 v = ld_shared_v4(sbuf + rr * 64 + ((k ^ ((rr >> 1) & 3)) << 4));
+                        if (rr < nvalid && n < p.N &&
+                            store_ok(row - lane + rr < p.total_rows && n + 8 <= p.N, p.err))
+                            st_global_v4(p.c + (row - lane + rr) * p.N + n, v.x, v.y, v.z, v.w);
+                    }
+                }
+            }
+        }
+        if (lane == 0) bulk_wait_all();
+    }
+
+    pdl_trigger();
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        // every issued copy lands before the CTA leaves, after an abort too
+        const uint32_t v = stages_done;
+        for (uint32_t s = 0; s < (uint32_t)C::STAGES; ++s) {
+            const uint32_t n = v / C::STAGES + (s < v % C::STAGES ? 1u : 0u);
+            if (n) mbar_drain(&full_bar[s], (n - 1) & 1u);
+        }
+    }
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+template <int BN, int STAGES, int SUM_WARPS>
+cudaError_t run_block_gemm(const GemmBlockArgs &a, cudaStream_t s) {
+    using C = BlockCfg<BN, STAGES, SUM_WARPS>;
+    const int64_t T = a.groups.total_rows;
+    CUtensorMap tA, tB, tC;
+    cuuint64_t da[2] = {(cuuint64_t)a.K, (cuuint64_t)T};
+    cuuint64_t sa[1] = {(cuuint64_t)a.K};
+    cuuint64_t db[3] = {(cuuint64_t)a.K, (cuuint64_t)a.N, (cuuint64_t)a.groups.num_experts};
+    cuuint64_t sb[2] = {(cuuint64_t)a.K, (cuuint64_t)(a.K * a.N)};
+    if (!make_map(&tA, a.a, 2, da, sa, C::BM)) return cudaErrorInvalidValue;
+    if (!make_map(&tB, a.b, 3, db, sb, BN)) return cudaErrorInvalidValue;
+    // bf16 output, boxes of 32 rows x 32 columns in the staging buffer's swizzle
+    cuuint64_t dc[2] = {(cuuint64_t)a.N, (cuuint64_t)T};
+    cuuint64_t sc[1] = {(cuuint64_t)a.N * 2};
+    cuuint32_t bc[2] = {32, 32}, ec[2] = {1, 1};
+    if (encode_fn()(&tC, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.c, dc, sc, bc, ec,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    const BlockGemmParams p{a.groups.row_offsets, a.groups.expert_ids, a.groups.num_groups,
+                            a.groups.num_experts, T, (int)a.N, (int)a.K, a.a_scales, a.b_scales,
+                            static_cast<uint16_t *>(a.c), a.err};
+    auto kern = gemm_fp8_block_kernel<C>;
+    static std::atomic<int> attr_done[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    cudaError_t attr_err = cudaSuccess;
+    cached_per_device(attr_done, dev, [&]() {
+        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        C::SMEM_BYTES);
+        if (attr_err == cudaSuccess && C::NREG) {
+            // the register split assumes THREADS x LAUNCH_REGS registers: refuse
+            // to launch a build that differs
+            cudaFuncAttributes fa;
+            attr_err = cudaFuncGetAttributes(&fa, kern);
+            if (attr_err == cudaSuccess && fa.numRegs != C::LAUNCH_REGS)
+                attr_err = cudaErrorInvalidConfiguration;
+        }
+        return attr_err == cudaSuccess ? 1 : 0;
+    });
+    if (attr_err != cudaSuccess) return attr_err;
+    // upper bound of the tiles the offsets can give
+    const int64_t tiles = (T / C::BM + a.groups.num_groups) * ((a.N + BN - 1) / BN);
+    const unsigned grid = (unsigned)(tiles < sm_count() ? tiles : sm_count());
+    return launch_pdl(kern, grid, C::THREADS, C::SMEM_BYTES, s, tA, tB, tC, p);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_fp8_block(const GemmBlockArgs &a, cudaStream_t s) {
+    return run_block_gemm<256, 4, 8>(a, s);
+}
+
+}  // namespace moeq

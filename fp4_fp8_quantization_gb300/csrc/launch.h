@@ -123,6 +123,69 @@ struct GemmArgs {
 // Returns cudaErrorNotSupported for shapes without a built kernel.
 cudaError_t launch_gemm(const GemmArgs &a, cudaStream_t s);
 
+// Grouped FP8 GEMM with 1 x 128 activation and 128 x 128 weight scales.
+struct GemmBlockArgs {
+    GroupArgs groups;
+    int64_t N, K;
+    const uint8_t *a, *b;
+    const float *a_scales, *b_scales;
+    void *c;
+    uint32_t *err;
+};
+cudaError_t launch_gemm_fp8_block(const GemmBlockArgs &a, cudaStream_t s);
+
+// Tokens to rows (spread) or rows to tokens, and the dots of the weights'
+// gradient where d_weights is given.  Sizes and strides in elements.
+struct RowsArgs {
+    int dtype;
+    bool spread;
+    const void *token_in;
+    int64_t token_stride;
+    void *token_out;
+    const void *rows_in;
+    void *rows_out;
+    const int32_t *dst;
+    const float *weights;
+    float *d_weights;
+    int64_t num_tokens, total_rows, hidden;
+    int32_t top_k;
+    uint32_t *err;
+};
+cudaError_t launch_topk_rows(const RowsArgs &a, cudaStream_t s);
+constexpr int kTopkRowsMax = 32;  // top_k of the router and the row calls
+
+// The router (d_logits null) or its gradient.
+struct GateArgs {
+    int dtype;
+    const void *logits;
+    int64_t stride, num_tokens;
+    int32_t num_experts, top_k;
+    int normalize;
+    float scale;
+    int32_t *ids;
+    float *weights;
+    const float *d_weights;
+    void *d_logits;
+    uint32_t *err;
+};
+cudaError_t launch_gate(const GateArgs &a, cudaStream_t s);
+
+// 1 x 128 block quantization of rows, routed tokens (dst) or SwiGLU rows.
+struct Fp8BlockArgs {
+    const void *in;
+    int64_t stride, rows, K;
+    const int32_t *dst;
+    int32_t top_k;
+    int64_t out_rows;
+    bool swiglu;
+    uint8_t *out;
+    float *scales;
+    uint32_t *err;
+};
+cudaError_t launch_fp8_block(const Fp8BlockArgs &a, cudaStream_t s);
+cudaError_t launch_fp8_block_weight(const void *w, int64_t E, int64_t N, int64_t K, uint8_t *out,
+                                    float *scales, cudaStream_t s);
+
 // Maximum number of groups the GEMM scheduler accepts.
 constexpr int kMaxGroups = 1024;
 

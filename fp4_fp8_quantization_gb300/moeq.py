@@ -19,6 +19,7 @@ _LIB_PATH = os.environ.get("MOEQ_LIB") or os.path.join(
     os.path.dirname(os.path.abspath(__file__)), "libmoeq.so")
 _lib = None
 
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # moeq_dtype
 FORMATS = {"nvfp4": 0, "mxfp4": 1, "mxfp8": 2}
 STATUS = {0: "MOEQ_OK", 1: "MOEQ_ERR_INVALID_ARG", 2: "MOEQ_ERR_UNSUPPORTED",
           3: "MOEQ_ERR_CUDA", 4: "MOEQ_ERR_DEVICE"}
@@ -26,6 +27,7 @@ DEVERR_BAD_OFFSETS, DEVERR_BAD_EXPERT, DEVERR_SCALE_ROWS, DEVERR_TIMEOUT, DEVERR
 DEVERR_BOUNDS = 32   # debug builds only: a store outside its buffer was skipped
 
 _P, _I64, _I32, _U32P = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.POINTER(ctypes.c_uint32)
+_F = ctypes.c_float
 _SIGNATURES = {
     "moeq_grouped_amax_scale": [_P, _I64, _I64, _I64, _P, _P, _P, _I32, _I32, _P],
     "moeq_grouped_quantize": [_I32, _P, _I64, _I64, _I64, _P, _P, _I64, _P, _P, _P, _P,
@@ -56,6 +58,18 @@ _SIGNATURES = {
     "moeq_grouped_amax_scale_topk": [_P, _I64, _I64, _I64, _P, _I32, _P, _I32, _P],
     "moeq_dispatch_mxfp4": [_P, _I64, _I64, _I64, _P, _I32, _I32, _P, _P, _I64, _P, _P, _P, _P,
                             _P, _I32, _P],
+    "moeq_gate_topk": [_I32, _P, _I64, _I64, _I32, _I32, _I32, _F, _P, _P, _P],
+    "moeq_gate_topk_grad": [_I32, _P, _I64, _I64, _I32, _I32, _I32, _F, _P, _P, _P, _P],
+    "moeq_permute_topk": [_I32, _P, _I64, _I64, _I64, _P, _I32, _P, _P, _I64, _P],
+    "moeq_permute_topk_grad": [_I32, _P, _I64, _I64, _I64, _P, _I32, _P, _P, _P, _I64, _P, _P],
+    "moeq_combine_topk": [_I32, _P, _I64, _I64, _I64, _P, _I32, _P, _P, _P],
+    "moeq_combine_topk_grad": [_I32, _P, _I64, _I64, _I64, _P, _I32, _P, _P, _I64, _P, _P, _P],
+    "moeq_quantize_fp8_block": [_P, _I64, _I64, _I64, _P, _P, _P],
+    "moeq_quantize_fp8_block_topk": [_P, _I64, _I64, _I64, _P, _I32, _P, _P, _I64, _P],
+    "moeq_swiglu_quantize_fp8_block": [_P, _I64, _I64, _P, _P, _P],
+    "moeq_quantize_fp8_block_weight": [_P, _I64, _I64, _I64, _P, _P, _P],
+    "moeq_grouped_matmul_fp8_block": [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32,
+                                      _I32, _P],
     "moeq_get_device_error": [_P, _U32P],
     "moeq_clear_device_error": [_P],
     "moeq_last_cuda_error": [],
@@ -366,6 +380,205 @@ def grouped_matmul_swiglu_mx(fmt, c_q, c_sf, a, a_sf, b, b_sf, expert_scales, a_
           _ptr(expert_scales, torch.float32), _ptr(a_offsets, _U32),
           _ptr(a_scales_offsets, _U32), _ptr(expert_ids, torch.int32), a.shape[0],
           scale_rows_total, I, K, b.shape[0], max_tokens_per_expert, G, _stream(stream))
+
+
+def _rows_of(t, name, shape=None, dtype=None):
+    """Pointer of a 2-D CUDA tensor with unit column stride (rows may be
+    strided) of one of DTYPES, or of dtype, and of the given shape."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.dtype not in DTYPES if dtype is None else t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype or tuple(DTYPES)}")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape or '2-D'}")
+    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: must have unit column stride")
+    return t.data_ptr()
+
+
+def _row_stride(t):
+    # a single row has no stride to speak of
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _shaped(t, shape, dtype, name):
+    """Pointer of a contiguous CUDA tensor of this shape and dtype (or None)."""
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return _ptr(t, dtype, name)
+
+
+def _given(t, name):
+    if t is None:
+        raise ValueError(f"{name}: required")
+    return t
+
+
+def _choices(dst_info, num_tokens):
+    if dst_info.dim() != 2 or dst_info.shape[0] != num_tokens or dst_info.shape[1] < 1:
+        raise ValueError("dst_info: expected [num_tokens, top_k]")
+    return dst_info.shape[1]
+
+
+def gate_topk(logits, topk_ids, weights, normalize=True, scale=1.0, stream=None):
+    """The router: topk_ids (int32 [num_tokens, top_k], out) are the largest
+    logits of each token (ties to the lowest index) and weights (fp32, out)
+    their softmax weights times scale, over the chosen (normalize) or over all
+    experts.  logits bf16 / fp16 / fp32 [num_tokens, num_experts], -inf for a
+    masked expert; a token with too few others gets id -1 and weight 0."""
+    p = _rows_of(logits, "logits")
+    T, E = logits.shape
+    k = _choices(topk_ids, T)
+    _call("moeq_gate_topk", DTYPES[logits.dtype], p, _row_stride(logits), T, E, k, bool(normalize),
+          scale, _ptr(topk_ids, torch.int32, "topk_ids"),
+          _shaped(_given(weights, "weights"), (T, k), torch.float32, "weights"), _stream(stream))
+
+
+def gate_topk_grad(logits, topk_ids, d_weights, d_logits, normalize=True, scale=1.0, stream=None):
+    """Gradient of gate_topk's weights: d_logits (out, the logits' dtype,
+    contiguous) from d_weights fp32 [num_tokens, top_k] and the logits and
+    topk_ids of the forward call."""
+    p = _rows_of(logits, "logits")
+    T, E = logits.shape
+    k = _choices(topk_ids, T)
+    _call("moeq_gate_topk_grad", DTYPES[logits.dtype], p, _row_stride(logits), T, E, k,
+          bool(normalize), scale, _ptr(topk_ids, torch.int32, "topk_ids"),
+          _shaped(_given(d_weights, "d_weights"), (T, k), torch.float32, "d_weights"),
+          _shaped(_given(d_logits, "d_logits"), (T, E), logits.dtype, "d_logits"), _stream(stream))
+
+
+def permute_topk(tokens, dst_info, rows, weights=None, stream=None):
+    """Tokens to their experts' rows: rows[dst_info[t, j]] = weights[t, j] *
+    tokens[t] (weights fp32 [num_tokens, top_k], or None: copies).  tokens
+    bf16 / fp16 / fp32 [num_tokens, hidden]; dst_info int32 [num_tokens,
+    top_k] from route_topk; rows (out) of the tokens' dtype [rows, hidden]."""
+    p = _rows_of(tokens, "tokens")
+    T, H = tokens.shape
+    k = _choices(dst_info, T)
+    _call("moeq_permute_topk", DTYPES[tokens.dtype], p, _row_stride(tokens), T, H,
+          _ptr(dst_info, torch.int32, "dst_info"), k,
+          _shaped(weights, (T, k), torch.float32, "weights"),
+          _shaped(_given(rows, "rows"), (rows.shape[0], H), tokens.dtype, "rows"), rows.shape[0],
+          _stream(stream))
+
+
+def permute_topk_grad(d_rows, dst_info, d_tokens, weights=None, tokens=None, d_weights=None,
+                      stream=None):
+    """Gradient of permute_topk: d_tokens[t] (out) = the sum over j of
+    weights[t, j] * d_rows[dst_info[t, j]]; with d_weights (out, fp32
+    [num_tokens, top_k]) also <tokens[t], d_rows[dst_info[t, j]]>."""
+    p = _rows_of(d_tokens, "d_tokens")
+    T, H = d_tokens.shape
+    k = _choices(dst_info, T)
+    if d_weights is not None:
+        _given(tokens, "tokens")
+    _call("moeq_permute_topk_grad", DTYPES[d_tokens.dtype],
+          _shaped(d_rows, (d_rows.shape[0], H), d_tokens.dtype, "d_rows"), d_rows.shape[0], T, H,
+          _ptr(dst_info, torch.int32, "dst_info"), k,
+          _shaped(weights, (T, k), torch.float32, "weights"),
+          _shaped(d_tokens, (T, H), d_tokens.dtype, "d_tokens"),
+          None if tokens is None else _rows_of(tokens, "tokens", (T, H), d_tokens.dtype),
+          H if tokens is None else _row_stride(tokens),
+          _shaped(d_weights, (T, k), torch.float32, "d_weights"), _stream(stream))
+
+
+def combine_topk(rows, dst_info, out, weights=None, stream=None):
+    """Rows back to their tokens: out[t] = the sum over j of weights[t, j] *
+    rows[dst_info[t, j]] (weights None: 1).  rows bf16 / fp16 / fp32 [rows,
+    hidden]; out of the same dtype [num_tokens, hidden]."""
+    p = _rows_of(out, "out")
+    T, H = out.shape
+    k = _choices(dst_info, T)
+    _call("moeq_combine_topk", DTYPES[out.dtype],
+          _shaped(rows, (rows.shape[0], H), out.dtype, "rows"), rows.shape[0], T, H,
+          _ptr(dst_info, torch.int32, "dst_info"), k,
+          _shaped(weights, (T, k), torch.float32, "weights"), _shaped(out, (T, H), out.dtype, "out"),
+          _stream(stream))
+
+
+def combine_topk_grad(d_out, dst_info, d_rows, weights=None, rows=None, d_weights=None,
+                      stream=None):
+    """Gradient of combine_topk: d_rows[dst_info[t, j]] (out) = weights[t, j]
+    * d_out[t]; with d_weights (out, fp32 [num_tokens, top_k]) also
+    <d_out[t], rows[dst_info[t, j]]>."""
+    p = _rows_of(d_out, "d_out")
+    T, H = d_out.shape
+    k = _choices(dst_info, T)
+    if d_weights is not None:
+        _given(rows, "rows")
+    n = d_rows.shape[0]
+    _call("moeq_combine_topk_grad", DTYPES[d_out.dtype], p, _row_stride(d_out), T, H,
+          _ptr(dst_info, torch.int32, "dst_info"), k,
+          _shaped(weights, (T, k), torch.float32, "weights"),
+          _shaped(d_rows, (n, H), d_out.dtype, "d_rows"), n,
+          _shaped(rows, (n, H), d_out.dtype, "rows"),
+          _shaped(d_weights, (T, k), torch.float32, "d_weights"), _stream(stream))
+
+
+def _blocks128(n):
+    return (n + 127) // 128
+
+
+def quantize_fp8_block(inp, out, scales, stream=None):
+    """E4M3 with one fp32 scale per 128 elements of a row: inp bf16 [rows, K]
+    -> out (uint8 / float8_e4m3fn [rows, K]), scales fp32 [rows, ceil(K / 128)]."""
+    p = _rows_of(inp, "inp", dtype=torch.bfloat16)
+    T, K = inp.shape
+    _call("moeq_quantize_fp8_block", p, _row_stride(inp), T, K,
+          _shaped(_given(out, "out"), (T, K), _U8, "out"),
+          _shaped(_given(scales, "scales"), (T, _blocks128(K)), torch.float32, "scales"),
+          _stream(stream))
+
+
+def quantize_fp8_block_topk(tokens, dst_info, out, scales, stream=None):
+    """quantize_fp8_block of routed tokens: rows dst_info[t, j] of out and
+    scales are token t's, each token read and quantized once."""
+    p = _rows_of(tokens, "tokens", dtype=torch.bfloat16)
+    T, K = tokens.shape
+    k = _choices(dst_info, T)
+    n = out.shape[0]
+    _call("moeq_quantize_fp8_block_topk", p, _row_stride(tokens), T, K,
+          _ptr(dst_info, torch.int32, "dst_info"), k, _shaped(out, (n, K), _U8, "out"),
+          _shaped(_given(scales, "scales"), (n, _blocks128(K)), torch.float32, "scales"), n,
+          _stream(stream))
+
+
+def swiglu_quantize_fp8_block(y, out, scales, stream=None):
+    """quantize_fp8_block of silu(gate) * up: y bf16 [rows, 2 I] with column
+    2j = gate_j, 2j + 1 = up_j; out [rows, I], scales [rows, ceil(I / 128)]."""
+    T, I = y.shape[0], y.shape[1] // 2
+    _call("moeq_swiglu_quantize_fp8_block", _shaped(y, (T, 2 * I), torch.bfloat16, "y"), T, I,
+          _shaped(_given(out, "out"), (T, I), _U8, "out"),
+          _shaped(_given(scales, "scales"), (T, _blocks128(I)), torch.float32, "scales"),
+          _stream(stream))
+
+
+def quantize_fp8_block_weight(w, out, scales, stream=None):
+    """Weights in E4M3 with one fp32 scale per 128 x 128 block: w bf16 [E, N,
+    K] -> out of that shape, scales fp32 [E, ceil(N / 128), ceil(K / 128)]."""
+    E, N, K = w.shape
+    _call("moeq_quantize_fp8_block_weight", _ptr(w, torch.bfloat16, "w"), E, N, K,
+          _shaped(_given(out, "out"), (E, N, K), _U8, "out"),
+          _shaped(_given(scales, "scales"), (E, _blocks128(N), _blocks128(K)), torch.float32,
+                  "scales"), _stream(stream))
+
+
+def grouped_matmul_fp8_block(c, a, b, a_scales, b_scales, a_offsets, expert_ids,
+                             max_tokens_per_expert=0, num_active_experts=None, stream=None):
+    """Grouped FP8 matmul with a scale for each block of 128: c bf16 [rows, N]
+    (out); a [rows, K] with a_scales [rows, ceil(K / 128)]; b [E, N, K] with
+    b_scales [E, ceil(N / 128), ceil(K / 128)]; group g is rows
+    [a_offsets[g], a_offsets[g + 1]) of expert expert_ids[g]."""
+    G = expert_ids.numel() if num_active_experts is None else num_active_experts
+    E, N, K = b.shape
+    T = a.shape[0]
+    _call("moeq_grouped_matmul_fp8_block", _shaped(_given(c, "c"), (T, N), torch.bfloat16, "c"),
+          _shaped(a, (T, K), _U8, "a"), _ptr(b, _U8, "b"),
+          _shaped(_given(a_scales, "a_scales"), (T, _blocks128(K)), torch.float32, "a_scales"),
+          _shaped(_given(b_scales, "b_scales"), (E, _blocks128(N), _blocks128(K)), torch.float32,
+                  "b_scales"),
+          _ptr(a_offsets, _U32, "a_offsets"), _ptr(expert_ids, torch.int32, "expert_ids"), T, N, K,
+          E, max_tokens_per_expert, G, _stream(stream))
 
 
 def get_device_error(stream=None):

@@ -82,6 +82,9 @@ typedef enum {
  *   MXFP8: E4M3 elements, 32-element blocks, E8M0 block scale. */
 typedef enum { MOEQ_NVFP4 = 0, MOEQ_MXFP4 = 1, MOEQ_MXFP8 = 2 } moeq_format;
 
+/* Element types of the router's logits and of tokens and rows. */
+typedef enum { MOEQ_BF16 = 0, MOEQ_FP16 = 1, MOEQ_FP32 = 2 } moeq_dtype;
+
 /* Device error word bits (sticky until moeq_clear_device_error). */
 #define MOEQ_DEVERR_BAD_OFFSETS 0x1u /* non-monotone or out-of-range offsets */
 #define MOEQ_DEVERR_BAD_EXPERT 0x2u  /* expert id outside [0, num_experts)   */
@@ -445,6 +448,131 @@ moeq_status moeq_dispatch_mxfp4(const void *tokens, int64_t token_stride, int64_
                                 int32_t *expert_ids, int32_t *src_info, int32_t *dst_info,
                                 uint32_t *scales_offsets, int32_t slot_rows,
                                 moeq_stream_t stream);
+
+/* ---- the router, tokens to rows and back (with gradients), FP8 with 128-blocks
+ *
+ * moeq_gate_topk: the top_k largest logits of each token, largest first, ties
+ * to the lowest index, and their softmax weights.  With x a token's logits,
+ * m = max x, i_r its choices:
+ *   normalize == 0:  w_r = scale * exp(x_{i_r} - m) / sum over all experts of exp(x - m)
+ *   normalize != 0:  w_r = scale * exp(x_{i_r} - m) / sum over the choices of exp(x - m)
+ * fp32 throughout, exp as in the library's SiLU.
+ *   logits      dtype [num_tokens, num_experts], row stride logit_stride elements.
+ *   topk_ids    int32 [num_tokens, top_k] (out);  weights fp32 [num_tokens, top_k] (out).
+ * A logit of -inf (a masked expert) or NaN is never chosen; a token with fewer
+ * than top_k others gets id -1 and weight 0 in the places left over, which
+ * moeq_route_topk drops (setting MOEQ_DEVERR_BAD_EXPERT).  A NaN or +inf logit
+ * makes the token's weights NaN.
+ * 1 <= top_k <= num_experts; num_experts <= 1024 and top_k <= 32 (else
+ * MOEQ_ERR_UNSUPPORTED). */
+moeq_status moeq_gate_topk(moeq_dtype dtype, const void *logits, int64_t logit_stride,
+                           int64_t num_tokens, int32_t num_experts, int32_t top_k,
+                           int32_t normalize, float scale, int32_t *topk_ids, float *weights,
+                           moeq_stream_t stream);
+
+/* Gradient of moeq_gate_topk's weights (the choice is taken as fixed): with p
+ * the softmax over all experts, q = w / scale and g_j = sum over r with
+ * i_r = j of scale * d_weights_r,
+ *   normalize == 0:  d_logits = p * (g - <p, g>)
+ *   normalize != 0:  d_logits_{i_r} = scale * q_r * (d_weights_r - <q, d_weights>), 0 elsewhere.
+ *   logits, topk_ids  as given to and returned by moeq_gate_topk (an id of -1 is skipped;
+ *               any other id outside the experts too, and sets MOEQ_DEVERR_BAD_EXPERT).
+ *   d_weights   fp32 [num_tokens, top_k];  d_logits dtype [num_tokens, num_experts] (out). */
+moeq_status moeq_gate_topk_grad(moeq_dtype dtype, const void *logits, int64_t logit_stride,
+                                int64_t num_tokens, int32_t num_experts, int32_t top_k,
+                                int32_t normalize, float scale, const int32_t *topk_ids,
+                                const float *d_weights, void *d_logits, moeq_stream_t stream);
+
+/* Tokens sorted by expert: rows[dst_info[t, j]] = weights[t, j] * tokens[t].
+ *   tokens    dtype [num_tokens, hidden], row stride token_stride elements.
+ *   dst_info  int32 [num_tokens, top_k] (from moeq_route_topk): the row of each choice,
+ *             -1 for a dropped one; any other value outside [0, total_rows) is skipped
+ *             and sets MOEQ_DEVERR_BAD_INDEX.
+ *   weights   fp32 [num_tokens, top_k], or NULL: the rows are copies.
+ *   rows      dtype [total_rows, hidden] (out); rows that no choice has are not written.
+ * Here and in the three calls below products and sums are fp32, rounded once when stored;
+ * sums over the choices run in their order (no atomics).  hidden * sizeof(dtype) and
+ * token_stride * sizeof(dtype) are multiples of 16; top_k <= 32, hidden < 2^24 (else
+ * MOEQ_ERR_UNSUPPORTED). */
+moeq_status moeq_permute_topk(moeq_dtype dtype, const void *tokens, int64_t token_stride,
+                              int64_t num_tokens, int64_t hidden, const int32_t *dst_info,
+                              int32_t top_k, const float *weights, void *rows, int64_t total_rows,
+                              moeq_stream_t stream);
+
+/* Gradient of moeq_permute_topk:
+ *   d_tokens[t] = sum over j of weights[t, j] * d_rows[dst_info[t, j]]   (weights NULL: 1)
+ *   d_weights[t, j] = <tokens[t], d_rows[dst_info[t, j]]>, 0 for a dropped choice.
+ * d_weights (fp32 [num_tokens, top_k]) may be NULL; tokens is read for it only. */
+moeq_status moeq_permute_topk_grad(moeq_dtype dtype, const void *d_rows, int64_t total_rows,
+                                   int64_t num_tokens, int64_t hidden, const int32_t *dst_info,
+                                   int32_t top_k, const float *weights, void *d_tokens,
+                                   const void *tokens, int64_t token_stride, float *d_weights,
+                                   moeq_stream_t stream);
+
+/* Rows back to their tokens: out[t] = sum over j of weights[t, j] * rows[dst_info[t, j]]
+ * (weights NULL: 1; dropped choices add nothing, a token with none is 0).
+ *   rows dtype [total_rows, hidden];  out dtype [num_tokens, hidden]. */
+moeq_status moeq_combine_topk(moeq_dtype dtype, const void *rows, int64_t total_rows,
+                              int64_t num_tokens, int64_t hidden, const int32_t *dst_info,
+                              int32_t top_k, const float *weights, void *out,
+                              moeq_stream_t stream);
+
+/* Gradient of moeq_combine_topk:
+ *   d_rows[dst_info[t, j]] = weights[t, j] * d_out[t]   (weights NULL: 1)
+ *   d_weights[t, j] = <d_out[t], rows[dst_info[t, j]]>, 0 for a dropped choice.
+ * d_out has row stride d_out_stride elements; d_rows must not overlap rows; d_weights may be
+ * NULL, rows is read for it only. */
+moeq_status moeq_combine_topk_grad(moeq_dtype dtype, const void *d_out, int64_t d_out_stride,
+                                   int64_t num_tokens, int64_t hidden, const int32_t *dst_info,
+                                   int32_t top_k, const float *weights, void *d_rows,
+                                   int64_t total_rows, const void *rows, float *d_weights,
+                                   moeq_stream_t stream);
+
+/* FP8 with one fp32 scale per block of 128 (the last block of a row may be
+ * shorter).  Per block: s = max(amax / 448, 2^-126), q = E4M3(x * (1 / s)), each
+ * step one fp32 operation, round to nearest even, saturating; q * s stands for x.
+ * A NaN stays a NaN code of its element alone; an infinity gives its block an
+ * infinite scale and itself a NaN code.  K % 16 == 0.
+ *   in      bf16 [rows, K], row stride in_row_stride elements (a multiple of 8).
+ *   out     E4M3 [rows, K];  scales fp32 [rows, ceil(K / 128)]. */
+moeq_status moeq_quantize_fp8_block(const void *in, int64_t in_row_stride, int64_t rows, int64_t K,
+                                    uint8_t *out, float *scales, moeq_stream_t stream);
+
+/* The same of routed tokens: row dst_info[t, j] of out and scales is token t's
+ * (each token read and quantized once).  dst_info, top_k and rows outside
+ * [0, total_rows) as in moeq_permute_topk. */
+moeq_status moeq_quantize_fp8_block_topk(const void *tokens, int64_t token_stride,
+                                         int64_t num_tokens, int64_t K, const int32_t *dst_info,
+                                         int32_t top_k, uint8_t *out, float *scales,
+                                         int64_t total_rows, moeq_stream_t stream);
+
+/* The same of h = silu(gate) * up (fp32, as in moeq_swiglu_quantize; not rounded
+ * in between): y bf16 [rows, 2 I], column 2j = gate_j, 2j+1 = up_j; out E4M3
+ * [rows, I]; scales fp32 [rows, ceil(I / 128)].  I % 16 == 0. */
+moeq_status moeq_swiglu_quantize_fp8_block(const void *y, int64_t rows, int64_t I, uint8_t *out,
+                                           float *scales, moeq_stream_t stream);
+
+/* The same of weights, one scale per 128 x 128 block: w bf16 [num_experts, N, K];
+ * out E4M3 of that shape; scales fp32 [num_experts, ceil(N / 128), ceil(K / 128)]. */
+moeq_status moeq_quantize_fp8_block_weight(const void *w, int64_t num_experts, int64_t N, int64_t K,
+                                           uint8_t *out, float *scales, moeq_stream_t stream);
+
+/* Grouped FP8 matmul with a scale for each block of 128:
+ *   c[t, n] = bf16( sum over kb of (a_scales[t, kb] * b_scales[e, n / 128, kb])
+ *                   * sum over k in block kb of a[t, k] * b[e, n, k] ),  e = expert_ids[g]
+ * the inner sums fp32 on the tensor cores, the outer one fp32 in the order of kb,
+ * rounded once.
+ *   c         bf16 [total_tokens, N]
+ *   a         E4M3 [total_tokens, K];  a_scales fp32 [total_tokens, ceil(K / 128)]
+ *   b         E4M3 [num_experts, N, K];  b_scales fp32 [num_experts, ceil(N / 128), ceil(K / 128)]
+ * K % 16 == 0, N % 8 == 0.  The activations' gradient is the same call on the
+ * transposed weights. */
+moeq_status moeq_grouped_matmul_fp8_block(void *c, const uint8_t *a, const uint8_t *b,
+                                          const float *a_scales, const float *b_scales,
+                                          const uint32_t *a_offsets, const int32_t *expert_ids,
+                                          int64_t total_tokens, int64_t N, int64_t K,
+                                          int32_t num_experts, int32_t max_tokens_per_expert,
+                                          int32_t num_active_experts, moeq_stream_t stream);
 
 /* Reads the sticky device error word of the current device (MOEQ_DEVERR_*
  * bits) after synchronising `stream`.  Returns MOEQ_ERR_DEVICE when any bit
