@@ -87,54 +87,138 @@ __device__ __forceinline__ int64_t row_of(const RowsParams &p, int64_t c, bool r
     return -1;
 }
 
-// One 16-byte piece of one token per thread: grid (pieces / threads, tokens).
-template <int DT>
-__global__ void __launch_bounds__(128) spread_kernel(RowsParams p) {
-    pdl_wait();
-    pdl_trigger();
-    const int64_t t = blockIdx.x;
-    const int64_t at = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * 16;
-    if (at >= p.row_bytes) return;
-    const uint4 u = *reinterpret_cast<const uint4 *>(p.token_in + t * p.token_stride + at);
-    Vec<DT> x;
-    x.from(u);
-    for (int j = 0; j < p.top_k; ++j) {
-        const int64_t c = t * p.top_k + j;
-        const int64_t r = row_of(p, c, at == 0);
-        if (r < 0) continue;
-        uint4 o = u;
-        if (p.w) {
-            const float w = __ldg(p.w + c);
-            Vec<DT> y;
+// The rows of choices j0 .. j0 + KC - 1 of token t (-1: none) and their
+// weights.
+template <int KC>
+struct Choices {
+    int64_t row[KC];  // byte offset of the row, < 0 without one
+    float w[KC];
+    __device__ __forceinline__ void load(const RowsParams &p, int64_t t, int j0, bool report) {
 #pragma unroll
-            for (int i = 0; i < Vec<DT>::N; ++i) y.v[i] = __fmul_rn(x.v[i], w);
-            o = y.pack();
+        for (int j = 0; j < KC; ++j) {
+            const int64_t c = t * p.top_k + j0 + j;
+            row[j] = -1;
+            w[j] = 1.0f;
+            if (j0 + j < p.top_k) {
+                const int64_t r = row_of(p, c, report);
+                row[j] = r < 0 ? -1 : r * p.row_bytes;
+                if (p.w) w[j] = __ldg(p.w + c);
+            }
         }
-        *reinterpret_cast<uint4 *>(p.rows_out + r * p.row_bytes + at) = o;
+    }
+};
+
+// The KC dot products of a CTA's threads, summed and stored in d_w.  Every
+// thread calls it; the order of the sum is fixed by the CTA's size.
+template <int KC>
+__device__ __forceinline__ void store_dots(const RowsParams &p, int64_t t, float (&s)[KC]) {
+    __shared__ float part[8][KC];
+#pragma unroll
+    for (int j = 0; j < KC; ++j)
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s[j] = __fadd_rn(s[j], __shfl_xor_sync(0xFFFFFFFFu, s[j], o));
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+        for (int j = 0; j < KC; ++j) part[threadIdx.x >> 5][j] = s[j];
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < p.top_k) {
+        float v = 0.0f;
+        for (int i = 0; i < (int)(blockDim.x >> 5); ++i) v = __fadd_rn(v, part[i][threadIdx.x]);
+        p.dw[t * p.top_k + threadIdx.x] = v;
     }
 }
 
-template <int DT>
-__global__ void __launch_bounds__(128) collect_kernel(RowsParams p) {
+// Token -> rows.  Without dots: one 16-byte piece of a token per thread, grid
+// (tokens, pieces / threads).  With dots (top_k <= KC): one CTA per token; the
+// rows that the dots read are loaded KC at a time, so that a token and its
+// rows are each touched once.
+template <int DT, int KC, bool DOTS>
+__global__ void __launch_bounds__(256) spread_kernel(RowsParams p) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t t = blockIdx.x;
+    int64_t at = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * 16;
+    float dot[KC] = {};
+    for (int j0 = 0; j0 < (DOTS ? KC : p.top_k); j0 += KC) {
+        Choices<KC> ch;
+        ch.load(p, t, j0, at == 0);
+        for (int64_t a = at; a < p.row_bytes; a += (int64_t)blockDim.x * 16) {
+            uint4 y[DOTS ? KC : 1];
+            if constexpr (DOTS) {
+#pragma unroll
+                for (int j = 0; j < KC; ++j)
+                    if (ch.row[j] >= 0) y[j] = ld_stream(p.rows_in + ch.row[j] + a);
+            }
+            const uint4 u = *reinterpret_cast<const uint4 *>(p.token_in + t * p.token_stride + a);
+            Vec<DT> x;
+            x.from(u);
+#pragma unroll
+            for (int j = 0; j < KC; ++j) {
+                if (ch.row[j] < 0) continue;
+                uint4 o = u;
+                if (p.w) {
+                    Vec<DT> v;
+#pragma unroll
+                    for (int i = 0; i < Vec<DT>::N; ++i) v.v[i] = __fmul_rn(x.v[i], ch.w[j]);
+                    o = v.pack();
+                }
+                if (store_ok(ch.row[j] + a < p.total_rows * p.row_bytes, p.err))
+                    *reinterpret_cast<uint4 *>(p.rows_out + ch.row[j] + a) = o;
+                if constexpr (DOTS) {
+                    Vec<DT> v;
+                    v.from(y[j]);
+#pragma unroll
+                    for (int i = 0; i < Vec<DT>::N; ++i) dot[j] = __fmaf_rn(x.v[i], v.v[i], dot[j]);
+                }
+            }
+            if (!DOTS) break;  // one piece per thread
+        }
+    }
+    if constexpr (DOTS) store_dots<KC>(p, t, dot);
+}
+
+// Rows -> token, in the same two forms; KC rows are in flight at a time.
+template <int DT, int KC, bool DOTS>
+__global__ void __launch_bounds__(256) collect_kernel(RowsParams p) {
     pdl_wait();
     pdl_trigger();
     const int64_t t = blockIdx.x;
     const int64_t at = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * 16;
-    if (at >= p.row_bytes) return;
-    Vec<DT> acc;
+    float dot[KC] = {};
+    Choices<KC> ch;
+    ch.load(p, t, 0, at == 0);
+    for (int64_t a = at; a < p.row_bytes; a += (int64_t)blockDim.x * 16) {
+        Vec<DT> acc, x;
 #pragma unroll
-    for (int i = 0; i < Vec<DT>::N; ++i) acc.v[i] = 0.0f;
-    for (int j = 0; j < p.top_k; ++j) {
-        const int64_t c = t * p.top_k + j;
-        const int64_t r = row_of(p, c, at == 0);
-        if (r < 0) continue;
-        const float w = p.w ? __ldg(p.w + c) : 1.0f;
-        Vec<DT> x;
-        x.from(*reinterpret_cast<const uint4 *>(p.rows_in + r * p.row_bytes + at));
+        for (int i = 0; i < Vec<DT>::N; ++i) acc.v[i] = 0.0f;
+        if constexpr (DOTS)
+            x.from(*reinterpret_cast<const uint4 *>(p.token_in + t * p.token_stride + a));
+        for (int j0 = 0;;) {
+            uint4 y[KC];
 #pragma unroll
-        for (int i = 0; i < Vec<DT>::N; ++i) acc.v[i] = __fmaf_rn(x.v[i], w, acc.v[i]);
+            for (int j = 0; j < KC; ++j)
+                if (ch.row[j] >= 0) y[j] = ld_stream(p.rows_in + ch.row[j] + a);
+#pragma unroll
+            for (int j = 0; j < KC; ++j) {
+                if (ch.row[j] < 0) continue;
+                Vec<DT> v;
+                v.from(y[j]);
+#pragma unroll
+                for (int i = 0; i < Vec<DT>::N; ++i) {
+                    acc.v[i] = __fmaf_rn(v.v[i], ch.w[j], acc.v[i]);
+                    if constexpr (DOTS) dot[j] = __fmaf_rn(x.v[i], v.v[i], dot[j]);
+                }
+            }
+            j0 += KC;
+            if (DOTS || j0 >= p.top_k) break;
+            ch.load(p, t, j0, at == 0);
+        }
+        if (store_ok(t < p.num_tokens, p.err))
+            *reinterpret_cast<uint4 *>(p.token_out + t * p.row_bytes + a) = acc.pack();
+        if (!DOTS) break;  // one piece per thread
     }
-    *reinterpret_cast<uint4 *>(p.token_out + t * p.row_bytes + at) = acc.pack();
+    if constexpr (DOTS) store_dots<KC>(p, t, dot);
 }
 
 // d_w[t, j] = <token_in[t], rows_in[dst[t, j]]>: one warp per choice, 0 for a
@@ -163,15 +247,25 @@ __global__ void __launch_bounds__(128) dots_kernel(RowsParams p) {
     if (lane == 0) p.dw[c] = s;
 }
 
-template <int DT>
+template <int DT, int KC>
 cudaError_t run_rows(bool spread, const RowsParams &p, cudaStream_t s) {
     const int64_t pieces = p.row_bytes / 16;
+    if (p.dw && p.top_k <= KC) {
+        const unsigned threads = pieces >= 256 ? 256 : (unsigned)((pieces + 31) / 32 * 32);
+        return launch_pdl(spread ? spread_kernel<DT, KC, true> : collect_kernel<DT, KC, true>,
+                          (unsigned)p.num_tokens, threads, 0, s, p);
+    }
     const dim3 grid((unsigned)p.num_tokens, (unsigned)((pieces + 127) / 128));
-    cudaError_t e = spread ? launch_pdl(spread_kernel<DT>, grid, 128, 0, s, p)
-                           : launch_pdl(collect_kernel<DT>, grid, 128, 0, s, p);
+    const cudaError_t e = launch_pdl(
+        spread ? spread_kernel<DT, KC, false> : collect_kernel<DT, KC, false>, grid, 128, 0, s, p);
     if (e != cudaSuccess || !p.dw) return e;
-    const int64_t choices = p.num_tokens * p.top_k;
+    const int64_t choices = p.num_tokens * p.top_k;  // more choices than KC: the dots apart
     return launch_pdl(dots_kernel<DT>, (unsigned)((choices + 3) / 4), 128, 0, s, p);
+}
+
+template <int DT>
+cudaError_t run_rows(bool spread, const RowsParams &p, cudaStream_t s) {
+    return p.top_k <= 2 ? run_rows<DT, 2>(spread, p, s) : run_rows<DT, 8>(spread, p, s);
 }
 
 }  // namespace
