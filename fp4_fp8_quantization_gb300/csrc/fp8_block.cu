@@ -62,54 +62,97 @@ struct BlockParams {
     uint32_t *err;
 };
 
-// One warp per row; 16 lanes hold a block, 8 elements each.
+// 8 elements of a row from 16 bytes of bf16, or, for SwiGLU, 8 values
+// silu(gate) * up from 32 bytes of gate/up pairs.
 template <bool SWIGLU>
-__global__ void __launch_bounds__(kWarps * 32) fp8_block_kernel(BlockParams p) {
+struct Piece {
+    uint4 u[SWIGLU ? 2 : 1];
+    __device__ __forceinline__ void load(const uint16_t *row, int64_t k) {
+        const uint16_t *src = row + (SWIGLU ? 2 * k : k);
+        u[0] = ld_stream(src);
+        if constexpr (SWIGLU) u[1] = ld_stream(src + 8);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < (SWIGLU ? 2 : 1); ++i) u[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void values(float (&x)[8]) const {
+        if constexpr (SWIGLU) {
+            const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {  // gate in the low half, up in the high
+                const F2 h = swiglu2(__uint_as_float(w[i] << 16), __uint_as_float(w[i + 1] << 16),
+                                     __uint_as_float(w[i] & 0xFFFF0000u),
+                                     __uint_as_float(w[i + 1] & 0xFFFF0000u));
+                x[i] = f2_lo(h);
+                x[i + 1] = f2_hi(h);
+            }
+        } else {
+            unpack8(u[0], x);
+        }
+    }
+};
+
+// One warp per U * 256 consecutive elements of a row, all of its loads issued
+// first; 16 lanes hold a block, 8 elements each.
+template <bool SWIGLU, int U>
+__global__ void __launch_bounds__(kWarps * 32) fp8_block_kernel(BlockParams p, int segments) {
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int64_t t = item / segments;
     if (t >= p.rows) return;
+    const int64_t k0 = (item - t * segments) * (U * 256) + lane * 8;
     const int64_t KB = (p.K + kBlk - 1) / kBlk;
-    for (int64_t k0 = 0; k0 < p.K; k0 += 256) {
-        const int64_t k = k0 + lane * 8;
-        float x[8] = {};
-        if (k < p.K) {
-            if constexpr (SWIGLU) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.in + t * p.stride + 2 * k);
-                const uint4 a = src[0], b = src[1];
-                const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const uint16_t *row = p.in + t * p.stride;
+    Piece<SWIGLU> in[U];
 #pragma unroll
-                for (int i = 0; i < 8; i += 2) {  // gate in the low half, up in the high
-                    const F2 h = swiglu2(
-                        __uint_as_float(w[i] << 16), __uint_as_float(w[i + 1] << 16),
-                        __uint_as_float(w[i] & 0xFFFF0000u), __uint_as_float(w[i + 1] & 0xFFFF0000u));
-                    x[i] = f2_lo(h);
-                    x[i + 1] = f2_hi(h);
-                }
-            } else {
-                unpack8(*reinterpret_cast<const uint4 *>(p.in + t * p.stride + k), x);
-            }
-        }
+    for (int i = 0; i < U; ++i) {
+        if (k0 + i * 256 < p.K)
+            in[i].load(row, k0 + i * 256);
+        else
+            in[i].zero();
+    }
+    uint2 q[U];
+    float s[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        float x[8];
+        in[i].values(x);
         float m = amax8(x);
 #pragma unroll
         for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        const float s = block_scale(m);
-        const uint2 q = codes8(x, __fdiv_rn(1.0f, s));
-        if (k >= p.K) continue;
-        for (int j = 0; j < (p.dst ? p.top_k : 1); ++j) {
-            int64_t r = t;
-            if (p.dst) {
-                r = __ldg(p.dst + t * p.top_k + j);
-                if (r < 0 || r >= p.out_rows) {
-                    if (r != -1 && k == 0) set_error(p.err, MOEQ_DEVERR_BAD_INDEX);
-                    continue;
-                }
+        s[i] = block_scale(m);
+        q[i] = codes8(x, __fdiv_rn(1.0f, s[i]));
+    }
+    for (int j = 0; j < (p.dst ? p.top_k : 1); ++j) {
+        int64_t r = t;
+        if (p.dst) {
+            r = __ldg(p.dst + t * p.top_k + j);
+            if (r < 0 || r >= p.out_rows) {
+                if (r != -1 && k0 == 0) set_error(p.err, MOEQ_DEVERR_BAD_INDEX);
+                continue;
             }
-            *reinterpret_cast<uint2 *>(p.out + r * p.K + k) = q;
-            if ((lane & 15) == 0) p.scales[r * KB + k / kBlk] = s;
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int64_t k = k0 + i * 256;
+            if (k < p.K && store_ok(r < p.out_rows, p.err)) {
+                *reinterpret_cast<uint2 *>(p.out + r * p.K + k) = q[i];
+                if ((lane & 15) == 0) p.scales[r * KB + k / kBlk] = s[i];
+            }
         }
     }
+}
+
+template <bool SWIGLU, int U>
+cudaError_t run_fp8_block(const BlockParams &p, cudaStream_t s) {
+    const int64_t segments = (p.K + U * 256 - 1) / (U * 256);
+    const int64_t blocks = (p.rows * segments + kWarps - 1) / kWarps;
+    if (blocks >= (int64_t)1 << 31) return cudaErrorNotSupported;
+    return launch_pdl(fp8_block_kernel<SWIGLU, U>, (unsigned)blocks, kWarps * 32, 0, s, p,
+                      (int)segments);
 }
 
 // One CTA per 128 x 128 weight block (grid: K blocks, N blocks, experts): 16
@@ -158,9 +201,11 @@ __global__ void __launch_bounds__(256) fp8_block_weight_kernel(const uint16_t *w
 cudaError_t launch_fp8_block(const Fp8BlockArgs &a, cudaStream_t s) {
     const BlockParams p{static_cast<const uint16_t *>(a.in), a.stride, a.rows, a.K, a.dst,
                         a.top_k, a.out_rows, a.out, a.scales, a.err};
-    const unsigned blocks = (unsigned)((a.rows + kWarps - 1) / kWarps);
-    return launch_pdl(a.swiglu ? fp8_block_kernel<true> : fp8_block_kernel<false>, blocks,
-                      kWarps * 32, 0, s, p);
+#ifndef MOEQ_QB_U
+#define MOEQ_QB_U 4
+#define MOEQ_QB_US 2
+#endif
+    return a.swiglu ? run_fp8_block<true, MOEQ_QB_US>(p, s) : run_fp8_block<false, MOEQ_QB_U>(p, s);
 }
 
 cudaError_t launch_fp8_block_weight(const void *w, int64_t E, int64_t N, int64_t K, uint8_t *out,
