@@ -24,6 +24,9 @@
 #include "launch.h"
 #include "tensormap.h"
 
+#ifndef MOEQ_B_TMAST
+#define MOEQ_B_TMAST 1
+#endif
 namespace moeq {
 
 namespace {
@@ -44,7 +47,7 @@ struct BlockCfg {
     // with; the host checks the compiled count before launching)
     static constexpr bool NREG = COLS_W == 128;
     static constexpr int LAUNCH_REGS = 65536 / THREADS / 8 * 8;
-    static constexpr int NREG_CTRL = 72;
+    static constexpr int NREG_CTRL = 56;
     static constexpr int NREG_SUM =
         NREG ? (THREADS * LAUNCH_REGS - 32 * SUM_WARP0 * NREG_CTRL) / (32 * SUM_WARPS) / 8 * 8 : 0;
     static constexpr int BUF_BYTES = 2048;  // staging of a 32 x 32 bf16 chunk per warp
@@ -54,6 +57,7 @@ struct BlockCfg {
                             32 * SUM_WARP0 * NREG_CTRL + 32 * SUM_WARPS * NREG_SUM <=
                                 THREADS * LAUNCH_REGS),
                   "register split by warpgroups");
+    static_assert(CHUNKS_W % 2 == 0, "the two load buffers alternate across K blocks");
     static_assert(COLS_W % 32 == 0 && 128 % COLS_W == 0, "a warp's columns share one scale");
 };
 
@@ -79,24 +83,13 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
                    "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
-// Scales 4 q .. 4 q + 3 of a row of kb (0 past its end): 16 bytes at once
-// where every row is aligned for it.
-__device__ __forceinline__ float4 load_scales4(const float *row, int q, int kb) {
-    if ((kb & 3) == 0) return __ldg(reinterpret_cast<const float4 *>(row) + q);
-    float v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = 4 * q + i < kb ? __ldg(row + 4 * q + i) : 0.0f;
-    return make_float4(v[0], v[1], v[2], v[3]);
-}
-
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
     gemm_fp8_block_kernel(const __grid_constant__ CUtensorMap tmA,
                           const __grid_constant__ CUtensorMap tmB,
                           const __grid_constant__ CUtensorMap tmC, const BlockGemmParams p) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full_bar[C::STAGES], empty_bar[C::STAGES];
-    __shared__ uint64_t tfull_bar[C::NBUF], tempty_bar[C::NBUF];
+    __shared__ uint64_t full_bar[C::STAGES], done_bar[C::STAGES], tempty_bar[C::NBUF];
     __shared__ uint64_t drain_bar;
     __shared__ uint32_t tmem_slot, stages_done;
     __shared__ int abort_flag;
@@ -114,12 +107,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&full_bar[s], 1);
-            mbar_init(&empty_bar[s], 1);
+            mbar_init(&done_bar[s], 1);
         }
-        for (int b = 0; b < C::NBUF; ++b) {
-            mbar_init(&tfull_bar[b], 1);
-            mbar_init(&tempty_bar[b], C::SUM_WARPS);
-        }
+        for (int b = 0; b < C::NBUF; ++b) mbar_init(&tempty_bar[b], C::SUM_WARPS);
         mbar_init(&drain_bar, 1);
         abort_flag = 0;
         stages_done = 0;
@@ -183,7 +173,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const int e = __ldg(p.expert_ids + tl.g);
                 const int row0 = (int)__ldg(p.offsets + tl.g) + tl.mb * C::BM;
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_v, p.err)) {
+                    if (!mbar_wait(&done_bar[stage], phase ^ 1u, abort_v, p.err)) {
                         ok = false;
                         break;
                     }
@@ -202,40 +192,50 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             stages_done = issued;
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            int stage = 0, buf = 0;
-            uint32_t phase = 0, bphase = 0;
-            bool ok = true;
-            for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
-                for (int kb = 0; kb < KB; ++kb) {
-                    if (!mbar_wait(&tempty_bar[buf], bphase ^ 1u, abort_v, p.err) ||
-                        !mbar_wait(&full_bar[stage], phase, abort_v, p.err)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t sa = smem_u32(smem + stage * C::STAGE_BYTES);
+        // the whole warp walks the loop (so that addresses and descriptors
+        // are warp-uniform), one thread issues; one commit per K block tells
+        // both the loads (stage free) and the sums (accumulator full)
+        const bool leader = elect_one();
+        const uint64_t da0 = sdesc_sw128(smem_u32(smem));
+        const uint64_t db0 = sdesc_sw128(smem_u32(smem) + C::A_BYTES);
+        int stage = 0, buf = 0;
+        uint32_t phase = 0, bphase = 0;
+        bool ok = true;
+        for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
+            for (int kb = 0; kb < KB; ++kb) {
+                // the operands are mostly there first: their wait is paid while
+                // the accumulator is still being read
+                if (!mbar_wait(&full_bar[stage], phase, abort_v, p.err) ||
+                    !mbar_wait(&tempty_bar[buf], bphase ^ 1u, abort_v, p.err)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (leader) {
+                    const uint32_t off = (uint32_t)(stage * C::STAGE_BYTES) >> 4;
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        mma_f8f6f4(tmem + buf * C::BN, sdesc_sw128(sa + ks * 32),
-                                   sdesc_sw128(sa + C::A_BYTES + ks * 32),
+                        mma_f8f6f4(tmem + buf * C::BN, da0 + off + 2 * ks, db0 + off + 2 * ks,
                                    idesc_f8_e4m3(C::BM, C::BN), ks ? 1u : 0u);
-                    tc_commit(&empty_bar[stage]);
-                    tc_commit(&tfull_bar[buf]);
-                    if (++stage == C::STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                    if (++buf == C::NBUF) {
-                        buf = 0;
-                        bphase ^= 1u;
-                    }
+                    tc_commit(&done_bar[stage]);
+                }
+                __syncwarp();
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+                if (++buf == C::NBUF) {
+                    buf = 0;
+                    bphase ^= 1u;
                 }
             }
-            // every tcgen05 operation issued here completes before TMEM is freed
+        }
+        // every tcgen05 operation issued here completes before TMEM is freed
+        if (leader) {
             tc_commit(&drain_bar);
             mbar_drain(&drain_bar, 0);
         }
+        __syncwarp();
     }
     } else {
         if constexpr (C::NREG)
@@ -245,8 +245,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const uint32_t toff = ((uint32_t)(quad * 32) << 16) + cgrp * C::COLS_W;
         const uint32_t sbuf = smem_u32(smem + C::STAGES * C::STAGE_BYTES) + (warp - C::SUM_WARP0) * C::BUF_BYTES;
         const int NBLK = (p.N + 127) / 128;
-        int buf = 0;
-        uint32_t bphase = 0;
+        int buf = 0, stage = 0;
+        uint32_t phase = 0;
         bool ok = true;
         for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
             const Tile tl = decode_tile(prefix, G, t, NB);
@@ -263,59 +263,69 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             F2 acc[C::COLS_W / 2];
 #pragma unroll
             for (int i = 0; i < C::COLS_W / 2; ++i) acc[i] = f2(0.0f, 0.0f);
-            float4 a4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b4 = a4, an = a4, bn = a4;
-            if (work) {
-                an = load_scales4(sa, 0, KB);
-                bn = load_scales4(sb, 0, KB);
-            }
-#pragma unroll 1
-            for (int kb = 0; kb < KB; ++kb) {
-                const int j = kb & 3;
-                if (j == 0) {
-                    a4 = an;
-                    b4 = bn;
-                    if (work && kb + 4 < KB) {
-                        an = load_scales4(sa, (kb >> 2) + 1, KB);
-                        bn = load_scales4(sb, (kb >> 2) + 1, KB);
+            if (!work) {  // only hands the accumulators on
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!mbar_wait(&done_bar[stage], phase, abort_v, p.err)) {
+                        ok = false;
+                        break;
                     }
-                }
-                const float av = j == 0 ? a4.x : j == 1 ? a4.y : j == 2 ? a4.z : a4.w;
-                const float bv = j == 0 ? b4.x : j == 1 ? b4.y : j == 2 ? b4.z : b4.w;
-                const float s = __fmul_rn(av, bv);
-                const F2 s2 = f2(s, s);
-                if (!mbar_wait(&tfull_bar[buf], bphase, abort_v, p.err)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                if (work) {
-#pragma unroll
-                    for (int ch = 0; ch < C::CHUNKS_W; ++ch) {
-                        uint32_t r[32];
-                        tmem_ld32(tmem + buf * C::BN + toff + ch * 32, r);
-                        tmem_ld_wait32(r);
-                        if (ch == C::CHUNKS_W - 1) {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&tempty_bar[buf]);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            acc[ch * 16 + i] =
-                                fma2(f2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), s2,
-                                     acc[ch * 16 + i]);
-                    }
-                } else {
-                    tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&tempty_bar[buf]);
+                    if (++buf == C::NBUF) buf = 0;
+                    if (++stage == C::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
-                if (++buf == C::NBUF) {
-                    buf = 0;
-                    bphase ^= 1u;
-                }
+                continue;
             }
-            if (!ok || !work) continue;
+            // the next K block's scales are on their way during this one
+            float an = __ldg(sa), bn = __ldg(sb);
+            // the load of the next 32 columns (of the next K block at the end
+            // of this one) is in flight while the last 32 are added
+            uint32_t r[2][32];
+            ok = mbar_wait(&done_bar[stage], phase, abort_v, p.err);
+            if (!ok) break;
+            tc_fence_after();
+            tmem_ld32(tmem + buf * C::BN + toff, r[0]);
+#pragma unroll 1
+            for (int kb = 0; kb < KB; ++kb) {
+                const float s = __fmul_rn(an, bn);
+                if (kb + 1 < KB) {
+                    an = __ldg(++sa);
+                    bn = __ldg(++sb);
+                }
+                const F2 s2 = f2(s, s);
+#pragma unroll
+                for (int ch = 0; ch < C::CHUNKS_W; ++ch) {
+                    tmem_ld_wait32(r[ch & 1]);
+                    if (ch < C::CHUNKS_W - 1) {
+                        tmem_ld32(tmem + buf * C::BN + toff + (ch + 1) * 32, r[(ch + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&tempty_bar[buf]);
+                        if (++buf == C::NBUF) buf = 0;
+                        if (++stage == C::STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                        if (kb + 1 < KB) {
+                            ok = mbar_wait(&done_bar[stage], phase, abort_v, p.err);
+                            if (!ok) break;
+                            tc_fence_after();
+                            tmem_ld32(tmem + buf * C::BN + toff, r[0]);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        acc[ch * 16 + i] = fma2(f2(__uint_as_float(r[ch & 1][2 * i]),
+                                                   __uint_as_float(r[ch & 1][2 * i + 1])),
+                                                s2, acc[ch * 16 + i]);
+                }
+                if (!ok) break;
+            }
+            if (!ok) break;
             // bf16 out through the warp's 32 x 32 staging buffer (64-byte rows
             // whose 16-byte pieces are XOR-swizzled by row pair, the tensor
             // map's 64-byte swizzle): one tensor store where all 32 rows lie in
@@ -324,7 +334,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int ch = 0; ch < C::CHUNKS_W; ++ch) {
                 const int nc = ncol0 + ch * 32;
                 if (nc >= p.N) break;
-                if (lane == 0) bulk_wait_read_all();
+                if (MOEQ_B_TMAST && lane == 0) bulk_wait_read_all();
                 __syncwarp();
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -337,7 +347,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     st_shared_v4(sbuf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), w[0], w[1], w[2],
                                  w[3]);
                 }
-                if (nvalid == 32) {
+                if (MOEQ_B_TMAST && nvalid == 32) {
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
@@ -433,7 +443,12 @@ cudaError_t run_block_gemm(const GemmBlockArgs &a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_gemm_fp8_block(const GemmBlockArgs &a, cudaStream_t s) {
-    return run_block_gemm<256, 4, 8>(a, s);
+#ifndef MOEQ_B_BN
+#define MOEQ_B_BN 256
+#define MOEQ_B_ST 4
+#define MOEQ_B_SW 8
+#endif
+    return run_block_gemm<MOEQ_B_BN, MOEQ_B_ST, MOEQ_B_SW>(a, s);
 }
 
 }  // namespace moeq
