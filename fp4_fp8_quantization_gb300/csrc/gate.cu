@@ -10,10 +10,12 @@
 //   d_x_{i_r} = s q_r (d_w_r - <q, d_w>), 0 elsewhere, q = w / s  (normalised)
 //
 // One warp per token with the whole row of logits in registers (E <= 1024),
-// one pass over memory each way.  Selection compares order-preserving integer
-// images of the logits: each round is one warp maximum of those and one
-// minimum of the indices that hold it.  exp is the library's own (common.cuh);
-// sums are fp32 in a fixed order.
+// one pass over memory each way.  Lane l holds logits l NV .. l NV + NV - 1,
+// read as vectors, so that among equal logits the lowest lane has the lowest
+// index.  Selection compares order-preserving integer images of the logits;
+// each lane keeps its best one at hand, and a round is one warp maximum of
+// those.  16-bit logits carry their index in the low half of the image, which
+// makes every image distinct.  Sums are fp32 in a fixed order.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -26,22 +28,37 @@ namespace {
 constexpr uint32_t kNegInfKey = 0x007FFFFFu;  // order_key(-inf)
 constexpr int kGateWarps = 4;
 
+constexpr float kInf = __builtin_huge_valf();
+
 template <int DT>
-__device__ __forceinline__ float load_logit(const void *row, int j) {
-    if constexpr (DT == MOEQ_FP32) return __ldg(static_cast<const float *>(row) + j);
-    const uint16_t b = __ldg(static_cast<const uint16_t *>(row) + j);
+__device__ __forceinline__ float logit_of(uint32_t b) {
+    if constexpr (DT == MOEQ_FP32) return __uint_as_float(b);
     if constexpr (DT == MOEQ_BF16) return bf16_bits_to_f32(b);
-    return __half2float(__ushort_as_half(b));
+    return __half2float(__ushort_as_half((unsigned short)b));
 }
 
 template <int DT>
-__device__ __forceinline__ void store_logit(void *row, int j, float v) {
+__device__ __forceinline__ uint32_t bits_of(float v) {
+    if constexpr (DT == MOEQ_FP32) return __float_as_uint(v);
+    if constexpr (DT == MOEQ_BF16) return f32_to_bf16_bits(v);
+    return __half_as_ushort(__float2half_rn(v));
+}
+
+template <int DT>
+constexpr int kSize = DT == MOEQ_FP32 ? 4 : 2;
+
+template <int DT>
+__device__ __forceinline__ float load_logit(const uint8_t *row, int j) {
+    if constexpr (DT == MOEQ_FP32) return __ldg(reinterpret_cast<const float *>(row) + j);
+    return logit_of<DT>(__ldg(reinterpret_cast<const uint16_t *>(row) + j));
+}
+
+template <int DT>
+__device__ __forceinline__ void store_logit(uint8_t *row, int j, float v) {
     if constexpr (DT == MOEQ_FP32)
-        static_cast<float *>(row)[j] = v;
-    else if constexpr (DT == MOEQ_BF16)
-        static_cast<uint16_t *>(row)[j] = (uint16_t)f32_to_bf16_bits(v);
+        reinterpret_cast<float *>(row)[j] = v;
     else
-        static_cast<uint16_t *>(row)[j] = __half_as_ushort(__float2half_rn(v));
+        reinterpret_cast<uint16_t *>(row)[j] = (uint16_t)bits_of<DT>(v);
 }
 
 // An integer that orders as the float does (-0 = +0); 0 for NaN, which ranks
@@ -56,35 +73,33 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-__device__ __forceinline__ float exp_diff(float x, float m) {
-    return f2_lo(exp_neg2(__fadd_rn(x, -m), 0.0f));
+// The same of a 16-bit logit, in 16 bits.
+template <int DT>
+__device__ __forceinline__ uint32_t order_key16(float x) {
+    const uint32_t b = bits_of<DT>(__fadd_rn(x, 0.0f));  // exact: x came from 16 bits
+    if (x != x) return 0u;
+    return b ^ ((b >> 15) ? 0xFFFFu : 0x8000u);
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+template <int DT>
+__device__ __forceinline__ float key16_value(uint32_t k) {
+    return logit_of<DT>(k ^ ((k >> 15) ? 0x8000u : 0xFFFFu));
+}
+
+// order_key16(-inf)
+template <int DT>
+constexpr uint32_t kNegInfKey16 = DT == MOEQ_BF16 ? 0x007Fu : 0x03FFu;
+
+// exp(x - m) for x <= m: within 2 + 1.2 |x - m| ulp, NaN for a NaN or for
+// infinity minus infinity.
+__device__ __forceinline__ float exp_diff(float x, float m) { return __expf(__fadd_rn(x, -m)); }
+
+// Sum over groups of LANES consecutive lanes, the same in each of them.
+template <int LANES = 32>
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    for (int o = LANES / 2; o; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
     return v;
-}
-
-// The denominator of the plain weights: sum over the row of exp(x - m), NaN
-// where the row holds a NaN or m is +inf (m finite otherwise).
-template <int NV>
-__device__ __forceinline__ float row_total(const float (&x)[NV], float m) {
-    float t = 0.0f;
-    bool nan = m == __int_as_float(0x7F800000);
-#pragma unroll
-    for (int i = 0; i < NV; i += 2) {
-        if constexpr (NV == 1) {
-            t = exp_diff(x[0], m);
-            nan |= x[0] != x[0];
-        } else {
-            const F2 e = exp_neg2(__fadd_rn(x[i], -m), __fadd_rn(x[i + 1], -m));
-            t = __fadd_rn(t, __fadd_rn(f2_lo(e), f2_hi(e)));
-            nan |= x[i] != x[i] || x[i + 1] != x[i + 1];
-        }
-    }
-    t = warp_sum(t);
-    return __any_sync(0xFFFFFFFFu, nan) ? __int_as_float(0x7FFFFFFF) : t;
 }
 
 struct GateParams {
@@ -101,16 +116,184 @@ struct GateParams {
     uint32_t *err;
 };
 
-// Logits j = 32 i + lane of a row; -inf past its end.
+// Whether every row starts where vectors of a lane's logits (16 bytes at
+// most) can be read and written.
 template <int DT, int NV>
-__device__ __forceinline__ void load_row(const GateParams &p, int64_t t, int lane, float (&x)[NV]) {
-    const uint8_t *row = p.logits + t * p.stride;
+__device__ __forceinline__ bool rows_aligned(int64_t stride) {
+    constexpr int kBytes = NV * kSize<DT> < 16 ? NV * kSize<DT> : 16;
+    return stride % kBytes == 0;
+}
+
+// The lane's logits; -inf past the row's end.
+template <int DT, int NV>
+__device__ __forceinline__ void load_row(const uint8_t *row, int E, int j0, bool vec,
+                                         float (&x)[NV]) {
+    constexpr int kBytes = NV * kSize<DT>;
+    if (vec && j0 + NV <= E) {
+        const uint8_t *a = row + (int64_t)j0 * kSize<DT>;
+        uint32_t w[kBytes < 4 ? 1 : kBytes / 4];
+        if constexpr (kBytes >= 16) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int j = 32 * i + lane;
-        x[i] = j < p.E ? load_logit<DT>(row, j) : __int_as_float(0xFF800000);
+            for (int i = 0; i < kBytes / 16; ++i) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(a) + i);
+                w[4 * i] = u.x;
+                w[4 * i + 1] = u.y;
+                w[4 * i + 2] = u.z;
+                w[4 * i + 3] = u.w;
+            }
+        } else if constexpr (kBytes == 8) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(a));
+            w[0] = u.x;
+            w[1] = u.y;
+        } else if constexpr (kBytes == 4) {
+            w[0] = __ldg(reinterpret_cast<const uint32_t *>(a));
+        } else {
+            w[0] = __ldg(reinterpret_cast<const uint16_t *>(a));
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            x[i] = logit_of<DT>(DT == MOEQ_FP32 ? w[i * kSize<DT> / 4]
+                                                : (w[i / 2] >> (16 * (i & 1))) & 0xFFFFu);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) x[i] = j0 + i < E ? load_logit<DT>(row, j0 + i) : -kInf;
     }
 }
+
+template <int DT, int NV>
+__device__ __forceinline__ void store_row(uint8_t *row, int E, int j0, bool vec,
+                                          const float (&g)[NV]) {
+    constexpr int kBytes = NV * kSize<DT>;
+    if (vec && j0 + NV <= E && kBytes >= 8) {
+        uint8_t *a = row + (int64_t)j0 * kSize<DT>;
+        uint32_t w[kBytes < 8 ? 2 : kBytes / 4];
+#pragma unroll
+        for (int i = 0; i < (kBytes < 8 ? 0 : kBytes / 4); ++i)
+            w[i] = DT == MOEQ_FP32
+                       ? bits_of<DT>(g[i % NV])
+                       : bits_of<DT>(g[2 * i % NV]) | (bits_of<DT>(g[(2 * i + 1) % NV]) << 16);
+        if constexpr (kBytes >= 16) {
+#pragma unroll
+            for (int i = 0; i < kBytes / 16; ++i)
+                st_global_v4(a + 16 * i, w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        } else {
+            *reinterpret_cast<uint2 *>(a) = make_uint2(w[0], w[1]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (j0 + i < E) store_logit<DT>(row, j0 + i, g[i]);
+    }
+}
+
+// A lane's candidates; take(own) removes the best one in the lane where own.
+//
+// fp32, up to 8: images and indices, sorted (an odd-even transposition sort,
+// which keeps equal ones in the order of their indices).
+template <int DT, int NV>
+struct Candidates {
+    uint32_t key[NV];
+    int idx[NV];
+    __device__ __forceinline__ uint32_t best() const { return key[0]; }
+    __device__ __forceinline__ int at() const { return idx[0]; }
+    __device__ __forceinline__ void init(const float (&x)[NV], int) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            key[i] = order_key(x[i]);
+            idx[i] = i;
+        }
+#pragma unroll
+        for (int pass = 0; pass < NV; ++pass)
+#pragma unroll
+            for (int i = pass & 1; i + 1 < NV; i += 2) {
+                const bool swap = key[i + 1] > key[i];
+                const uint32_t k = max(key[i], key[i + 1]);
+                key[i + 1] = min(key[i], key[i + 1]);
+                key[i] = k;
+                const int a = swap ? idx[i + 1] : idx[i];
+                idx[i + 1] = swap ? idx[i] : idx[i + 1];
+                idx[i] = a;
+            }
+    }
+    __device__ __forceinline__ void take(bool own) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            key[i] = own ? (i + 1 < NV ? key[(i + 1) % NV] : 0u) : key[i];
+            if (i + 1 < NV) idx[i] = own ? idx[(i + 1) % NV] : idx[i];
+        }
+    }
+};
+
+// fp32, more: images in index order; the best is found again by a scan.
+template <int NV>
+struct ScannedCandidates {
+    uint32_t key[NV];
+    uint32_t top;
+    int pos;
+    __device__ __forceinline__ uint32_t best() const { return top; }
+    __device__ __forceinline__ int at() const { return pos; }
+    __device__ __forceinline__ void init(const float (&x)[NV], int) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) key[i] = order_key(x[i]);
+        scan();
+    }
+    __device__ __forceinline__ void scan() {
+        top = 0u;
+        pos = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (key[i] > top) {  // the lowest index of equal ones
+                top = key[i];
+                pos = i;
+            }
+    }
+    __device__ __forceinline__ void take(bool own) {
+        if (!own) return;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (i == pos) key[i] = 0u;
+        scan();
+    }
+};
+template <>
+struct Candidates<MOEQ_FP32, 16> : ScannedCandidates<16> {};
+template <>
+struct Candidates<MOEQ_FP32, 32> : ScannedCandidates<32> {};
+
+// 16-bit logits: images that hold the index, sorted; the best is the first.
+template <int DT, int NV>
+struct SortedCandidates {
+    uint32_t key[NV];
+    __device__ __forceinline__ uint32_t best() const { return key[0]; }
+    __device__ __forceinline__ void init(const float (&x)[NV], int j0) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            key[i] = (order_key16<DT>(x[i]) << 16) | (uint32_t)(0xFFFF - (j0 + i));
+        // odd-even merge sort, largest first (NV is a power of two)
+#pragma unroll
+        for (int n = 1; n < NV; n *= 2)
+#pragma unroll
+            for (int h = n; h >= 1; h /= 2)
+#pragma unroll
+                for (int a = h % n; a + h < NV; a += 2 * h)
+#pragma unroll
+                    for (int b = 0; b < h; ++b)
+                        if (a + b + h < NV && (a + b) / (2 * n) == (a + b + h) / (2 * n)) {
+                            const uint32_t u = key[a + b], v = key[a + b + h];
+                            key[a + b] = max(u, v);
+                            key[a + b + h] = min(u, v);
+                        }
+    }
+    __device__ __forceinline__ void take(bool own) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            key[i] = own ? (i + 1 < NV ? key[(i + 1) % NV] : 0u) : key[i];
+    }
+};
+template <int NV>
+struct Candidates<MOEQ_BF16, NV> : SortedCandidates<MOEQ_BF16, NV> {};
+template <int NV>
+struct Candidates<MOEQ_FP16, NV> : SortedCandidates<MOEQ_FP16, NV> {};
 
 template <int DT, int NV>
 __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateParams p) {
@@ -120,120 +303,177 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateParams p) {
     const int64_t t = (int64_t)blockIdx.x * kGateWarps + (threadIdx.x >> 5);
     if (t >= p.num_tokens) return;
     float x[NV];
-    load_row<DT>(p, t, lane, x);
-    uint32_t key[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) key[i] = order_key(x[i]);
-    int my_id = -1;          // lane r: choice r
+    load_row<DT>(p.logits + t * p.stride, p.E, lane * NV, rows_aligned<DT, NV>(p.stride), x);
+    Candidates<DT, NV> c;
+    c.init(x, lane * NV);
+    // lane r: choice r.  A round past the last logit above -inf finds an image
+    // that is not above kNegInf and is dropped below.
+    int my_j = 0;
     uint32_t my_key = 0u, top = 0u;
     for (int r = 0; r < p.top_k; ++r) {
-        uint32_t best = 0u;
-        int bi = 0;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                bi = i;
-            }
-        const uint32_t mx = __reduce_max_sync(0xFFFFFFFFu, best);
+        const uint32_t mx = __reduce_max_sync(0xFFFFFFFFu, c.best());
+        int j = 0;
+        if constexpr (DT == MOEQ_FP32) {
+            const int owner = __ffs((int)__ballot_sync(0xFFFFFFFFu, c.best() == mx)) - 1;
+            j = owner * NV + __shfl_sync(0xFFFFFFFFu, c.at(), owner);
+            c.take(lane == owner);
+        } else {
+            c.take(c.best() == mx);  // images are distinct
+        }
         if (r == 0) top = mx;
-        if (mx <= kNegInfKey) break;  // nothing left to choose
-        const int j = (int)__reduce_min_sync(0xFFFFFFFFu, best == mx ? 32u * bi + lane : 0xFFFFFFFFu);
         if (lane == r) {
-            my_id = j;
+            my_j = j;
             my_key = mx;
         }
-        if (lane == (j & 31)) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (i == j >> 5) key[i] = 0u;
-        }
     }
+    constexpr uint32_t kNone = DT == MOEQ_FP32 ? kNegInfKey : (kNegInfKey16<DT> << 16 | 0xFFFFu);
+    int id = -1;
     float w = 0.0f;
-    if (top > kNegInfKey) {
-        const float m = key_value(top);
-        const float e = my_id >= 0 ? exp_diff(key_value(my_key), m) : 0.0f;
-        float total = row_total(x, m);
-        if (p.normalize && total == total) total = warp_sum(e);
-        if (my_id >= 0 || total != total) w = __fmul_rn(__fdiv_rn(e, total), p.scale);
+    if (top > kNone) {
+        float m, e = 0.0f;
+        if constexpr (DT == MOEQ_FP32) {
+            m = key_value(top);
+            if (my_key > kNone) {
+                id = my_j;
+                e = exp_diff(key_value(my_key), m);
+            }
+        } else {
+            m = key16_value<DT>(top >> 16);
+            if (my_key > kNone) {
+                id = 0xFFFF - (int)(my_key & 0xFFFFu);
+                e = exp_diff(key16_value<DT>(my_key >> 16), m);
+            }
+        }
+        // a NaN logit, or m infinite, makes either denominator NaN
+        float total = 0.0f;
+        if (p.normalize) {
+            bool nan = false;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) nan |= x[i] != x[i];
+            total = lanes_sum(e);
+            if (__any_sync(0xFFFFFFFFu, nan)) total = __int_as_float(0x7FFFFFFF);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) total = __fadd_rn(total, exp_diff(x[i], m));
+            total = lanes_sum(total);
+        }
+        w = __fmul_rn(__fdiv_rn(e, total), p.scale);
     }
-    if (lane < p.top_k) {
-        p.ids[t * p.top_k + lane] = my_id;
+    if (lane < p.top_k && store_ok(t < p.num_tokens, p.err)) {
+        p.ids[t * p.top_k + lane] = id;
         p.weights[t * p.top_k + lane] = w;
     }
 }
 
-template <int DT, int NV>
-__global__ void __launch_bounds__(kGateWarps * 32) gate_grad_kernel(GateParams p) {
+// The gradient: LANES lanes per token (top_k <= LANES), each with V vectors of
+// 16 bytes of the row (coalesced), so that the sums over lanes are shared by
+// the 32 / LANES tokens of a warp.  Every logit's part of the row is stored
+// first, then the chosen ones over it.
+template <int DT, int LANES, int V>
+__global__ void __launch_bounds__(kGateWarps * 32) gate_grad_kernel(GateParams p, int vec) {
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * kGateWarps + (threadIdx.x >> 5);
-    if (t >= p.num_tokens) return;
-    float x[NV];
-    load_row<DT>(p, t, lane, x);
-    float m = __int_as_float(0xFF800000);
+    constexpr int W = 16 / kSize<DT>;  // logits per vector
+    const int lane = threadIdx.x & 31, sub = lane % LANES;
+    const int64_t slot = ((int64_t)blockIdx.x * kGateWarps + (threadIdx.x >> 5)) * (32 / LANES) +
+                         lane / LANES;
+    const bool active = slot < p.num_tokens;
+    const int64_t t = active ? slot : p.num_tokens - 1;
+    const uint8_t *in = p.logits + t * p.stride;
+    float x[V][W];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) m = fmaxf(m, x[i]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    const bool some = m > __int_as_float(0xFF800000);
+    for (int i = 0; i < V; ++i) load_row<DT>(in, p.E, (i * LANES + sub) * W, vec & 1, x[i]);
     int id = -1;
     float d = 0.0f, e = 0.0f;  // lane r: s d_w_r and exp(x_{i_r} - m) of choice r
-    if (lane < p.top_k) {
-        id = p.ids[t * p.top_k + lane];
+    if (sub < p.top_k) {
+        id = __ldg(p.ids + t * p.top_k + sub);
         if (id < -1 || id >= p.E) {
-            set_error(p.err, MOEQ_DEVERR_BAD_EXPERT);
+            if (active) set_error(p.err, MOEQ_DEVERR_BAD_EXPERT);
             id = -1;
         }
-        if (id >= 0) d = __fmul_rn(p.d_weights[t * p.top_k + lane], p.scale);
-        if (id >= 0 && some) e = exp_diff(load_logit<DT>(p.logits + t * p.stride, id), m);
+        if (id >= 0) d = __fmul_rn(__ldg(p.d_weights + t * p.top_k + sub), p.scale);
     }
-    float g[NV];
+    const float chosen = id >= 0 ? load_logit<DT>(in, id) : 0.0f;
+    float m = -kInf;
+    bool nan = false;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) g[i] = 0.0f;
-    if (some) {
-        float total = row_total(x, m);
-        if (p.normalize && total == total) total = warp_sum(e);
-        const float inv = __fdiv_rn(1.0f, total);
-        const float q = __fmul_rn(e, inv);
-        const float mean = warp_sum(id >= 0 ? __fmul_rn(q, d) : 0.0f);
-        if (!p.normalize) {
+    for (int i = 0; i < V; ++i)
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                g[i] = __fmul_rn(-mean, __fmul_rn(exp_diff(x[i], m), inv));
+        for (int k = 0; k < W; ++k) {
+            m = fmaxf(m, x[i][k]);
+            nan |= x[i][k] != x[i][k];
         }
-        // the chosen: s q d_w in the plain form (the mean is in already)
-        const float add = p.normalize ? __fmul_rn(q, __fadd_rn(d, -mean)) : __fmul_rn(q, d);
-        for (int r = 0; r < p.top_k; ++r) {
-            const int j = __shfl_sync(0xFFFFFFFFu, id, r);
-            const float a = __shfl_sync(0xFFFFFFFFu, add, r);
-            if (j < 0 || lane != (j & 31)) continue;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (i == j >> 5) g[i] = __fadd_rn(g[i], a);
+    for (int o = LANES / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    const bool some = m > -kInf;
+    if (id >= 0 && some) e = exp_diff(chosen, m);
+    float total = nan ? __int_as_float(0x7FFFFFFF) : e;
+    if (!p.normalize) {
+        total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+                x[i][k] = some ? exp_diff(x[i][k], m) : 0.0f;
+                total = __fadd_rn(total, x[i][k]);
+            }
+    }
+    total = lanes_sum<LANES>(total);
+    const float inv = some ? __fdiv_rn(1.0f, total) : 0.0f;
+    const float q = __fmul_rn(e, inv);
+    const float mean = lanes_sum<LANES>(id >= 0 ? __fmul_rn(q, d) : 0.0f);
+    const float part = __fmul_rn(-mean, inv);
+    constexpr int64_t kS = kSize<DT>;
+    uint8_t *out = p.d_logits + t * p.E * kS;
+    if (active && store_ok(t < p.num_tokens, p.err)) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float g[W];
+#pragma unroll
+            for (int k = 0; k < W; ++k) g[k] = p.normalize ? 0.0f : __fmul_rn(part, x[i][k]);
+            store_row<DT>(out, p.E, (i * LANES + sub) * W, vec & 2, g);
         }
     }
-    uint8_t *row = p.d_logits + t * p.E * (DT == MOEQ_FP32 ? 4 : 2);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int j = 32 * i + lane;
-        if (j < p.E) store_logit<DT>(row, j, g[i]);
-    }
+    __syncwarp();  // orders the stores above before those below
+    if (active && id >= 0) store_logit<DT>(out, id, __fmul_rn(q, __fadd_rn(d, -mean)));
 }
 
 template <int DT>
-cudaError_t run_gate(bool grad, const GateParams &p, cudaStream_t s) {
+cudaError_t run_grad(const GateParams &p, cudaStream_t s) {
+    constexpr int kS = kSize<DT>;
+    const int vec = (p.stride % 16 == 0) | (p.E * kS % 16 == 0 ? 2 : 0);
+    const int per8 = 8 * 16 / kS;  // logits of 8 lanes with one vector each
+    const int nv = (p.E + per8 - 1) / per8;
+    auto go = [&](void (*kern)(GateParams, int), int lanes) {
+        const int64_t per_cta = kGateWarps * 32 / lanes;
+        return launch_pdl(kern, (unsigned)((p.num_tokens + per_cta - 1) / per_cta), kGateWarps * 32,
+                          0, s, p, vec);
+    };
+    if (p.top_k <= 8 && nv <= 1) return go(gate_grad_kernel<DT, 8, 1>, 8);
+    if (p.top_k <= 8 && nv <= 2) return go(gate_grad_kernel<DT, 8, 2>, 8);
+    if (p.top_k <= 8 && nv <= 4) return go(gate_grad_kernel<DT, 8, 4>, 8);
+    if (nv <= 4) return go(gate_grad_kernel<DT, 32, 1>, 32);
+    if (nv <= 8) return go(gate_grad_kernel<DT, 32, 2>, 32);
+    if (nv <= 16) return go(gate_grad_kernel<DT, 32, 4>, 32);
+    return go(gate_grad_kernel<DT, 32, 8>, 32);
+}
+
+template <int DT>
+cudaError_t run_gate(const GateParams &p, cudaStream_t s) {
     const unsigned blocks = (unsigned)((p.num_tokens + kGateWarps - 1) / kGateWarps);
     const int nv = (p.E + 31) / 32;
-    void (*kern)(GateParams) =
-        nv <= 1    ? (grad ? gate_grad_kernel<DT, 1> : gate_kernel<DT, 1>)
-        : nv <= 2  ? (grad ? gate_grad_kernel<DT, 2> : gate_kernel<DT, 2>)
-        : nv <= 4  ? (grad ? gate_grad_kernel<DT, 4> : gate_kernel<DT, 4>)
-        : nv <= 8  ? (grad ? gate_grad_kernel<DT, 8> : gate_kernel<DT, 8>)
-        : nv <= 16 ? (grad ? gate_grad_kernel<DT, 16> : gate_kernel<DT, 16>)
-                   : (grad ? gate_grad_kernel<DT, 32> : gate_kernel<DT, 32>);
+    void (*kern)(GateParams) = nv <= 1    ? gate_kernel<DT, 1>
+                               : nv <= 2  ? gate_kernel<DT, 2>
+                               : nv <= 4  ? gate_kernel<DT, 4>
+                               : nv <= 8  ? gate_kernel<DT, 8>
+                               : nv <= 16 ? gate_kernel<DT, 16>
+                                          : gate_kernel<DT, 32>;
     return launch_pdl(kern, blocks, kGateWarps * 32, 0, s, p);
+}
+
+template <int DT>
+cudaError_t run(const GateParams &p, cudaStream_t s) {
+    return p.d_logits ? run_grad<DT>(p, s) : run_gate<DT>(p, s);
 }
 
 }  // namespace
@@ -243,10 +483,9 @@ cudaError_t launch_gate(const GateArgs &a, cudaStream_t s) {
     GateParams p{static_cast<const uint8_t *>(a.logits), a.stride * size, a.num_tokens,
                  a.num_experts, a.top_k, a.normalize, a.scale, a.ids, a.weights, a.d_weights,
                  static_cast<uint8_t *>(a.d_logits), a.err};
-    const bool grad = a.d_logits != nullptr;
-    if (a.dtype == MOEQ_BF16) return run_gate<MOEQ_BF16>(grad, p, s);
-    if (a.dtype == MOEQ_FP16) return run_gate<MOEQ_FP16>(grad, p, s);
-    return run_gate<MOEQ_FP32>(grad, p, s);
+    if (a.dtype == MOEQ_BF16) return run<MOEQ_BF16>(p, s);
+    if (a.dtype == MOEQ_FP16) return run<MOEQ_FP16>(p, s);
+    return run<MOEQ_FP32>(p, s);
 }
 
 }  // namespace moeq

@@ -456,7 +456,7 @@ moeq_status moeq_dispatch_mxfp4(const void *tokens, int64_t token_stride, int64_
  * m = max x, i_r its choices:
  *   normalize == 0:  w_r = scale * exp(x_{i_r} - m) / sum over all experts of exp(x - m)
  *   normalize != 0:  w_r = scale * exp(x_{i_r} - m) / sum over the choices of exp(x - m)
- * fp32 throughout, exp as in the library's SiLU.
+ * fp32 throughout; exp(d) is within 2 + 1.2 |d| ulp.
  *   logits      dtype [num_tokens, num_experts], row stride logit_stride elements.
  *   topk_ids    int32 [num_tokens, top_k] (out);  weights fp32 [num_tokens, top_k] (out).
  * A logit of -inf (a masked expert) or NaN is never chosen; a token with fewer
@@ -475,8 +475,9 @@ moeq_status moeq_gate_topk(moeq_dtype dtype, const void *logits, int64_t logit_s
  * i_r = j of scale * d_weights_r,
  *   normalize == 0:  d_logits = p * (g - <p, g>)
  *   normalize != 0:  d_logits_{i_r} = scale * q_r * (d_weights_r - <q, d_weights>), 0 elsewhere.
- *   logits, topk_ids  as given to and returned by moeq_gate_topk (an id of -1 is skipped;
- *               any other id outside the experts too, and sets MOEQ_DEVERR_BAD_EXPERT).
+ *   logits, topk_ids  as given to and returned by moeq_gate_topk: a token's ids are
+ *               distinct (an id of -1 is skipped; any other id outside the experts too,
+ *               and sets MOEQ_DEVERR_BAD_EXPERT).
  *   d_weights   fp32 [num_tokens, top_k];  d_logits dtype [num_tokens, num_experts] (out). */
 moeq_status moeq_gate_topk_grad(moeq_dtype dtype, const void *logits, int64_t logit_stride,
                                 int64_t num_tokens, int32_t num_experts, int32_t top_k,
