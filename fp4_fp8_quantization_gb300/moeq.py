@@ -103,8 +103,16 @@ def lib():
     return _lib
 
 
+# The handle of the current stream without building a torch.cuda.Stream
+# (0.2 us a call against 2.9).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None and _raw_device is not None:
+            return _raw_stream(_raw_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -138,7 +146,7 @@ def _ptr_rows(t, dtype, name):
 
 
 def _call(fn, *args):
-    st = getattr(lib(), fn)(*args)
+    st = getattr(_lib or lib(), fn)(*args)
     if st != 0:
         raise MoeqError(fn, st)
 
@@ -389,10 +397,12 @@ def _rows_of(t, name, shape=None, dtype=None):
         raise ValueError(f"{name}: must be a CUDA tensor")
     if t.dtype not in DTYPES if dtype is None else t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype or tuple(DTYPES)}")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape or '2-D'}")
-    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name}: must have unit column stride")
+    if not t.is_contiguous():
+        n, m = t.shape
+        if m > 1 and t.stride(1) != 1 or n > 1 and t.stride(0) < m:
+            raise ValueError(f"{name}: must have unit column stride")
     return t.data_ptr()
 
 
@@ -401,17 +411,16 @@ def _row_stride(t):
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
-def _shaped(t, shape, dtype, name):
-    """Pointer of a contiguous CUDA tensor of this shape and dtype (or None)."""
-    if t is not None and tuple(t.shape) != tuple(shape):
+def _shaped(t, shape, dtype, name, optional=False):
+    """Pointer of a contiguous CUDA tensor of this shape and dtype; None is
+    None where that is allowed."""
+    if t is None and optional:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: required" if t is None else f"{name}: expected a torch.Tensor")
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     return _ptr(t, dtype, name)
-
-
-def _given(t, name):
-    if t is None:
-        raise ValueError(f"{name}: required")
-    return t
 
 
 def _choices(dst_info, num_tokens):
@@ -431,7 +440,7 @@ def gate_topk(logits, topk_ids, weights, normalize=True, scale=1.0, stream=None)
     k = _choices(topk_ids, T)
     _call("moeq_gate_topk", DTYPES[logits.dtype], p, _row_stride(logits), T, E, k, bool(normalize),
           scale, _ptr(topk_ids, torch.int32, "topk_ids"),
-          _shaped(_given(weights, "weights"), (T, k), torch.float32, "weights"), _stream(stream))
+          _shaped(weights, (T, k), torch.float32, "weights"), _stream(stream))
 
 
 def gate_topk_grad(logits, topk_ids, d_weights, d_logits, normalize=True, scale=1.0, stream=None):
@@ -443,8 +452,8 @@ def gate_topk_grad(logits, topk_ids, d_weights, d_logits, normalize=True, scale=
     k = _choices(topk_ids, T)
     _call("moeq_gate_topk_grad", DTYPES[logits.dtype], p, _row_stride(logits), T, E, k,
           bool(normalize), scale, _ptr(topk_ids, torch.int32, "topk_ids"),
-          _shaped(_given(d_weights, "d_weights"), (T, k), torch.float32, "d_weights"),
-          _shaped(_given(d_logits, "d_logits"), (T, E), logits.dtype, "d_logits"), _stream(stream))
+          _shaped(d_weights, (T, k), torch.float32, "d_weights"),
+          _shaped(d_logits, (T, E), logits.dtype, "d_logits"), _stream(stream))
 
 
 def permute_topk(tokens, dst_info, rows, weights=None, stream=None):
@@ -457,8 +466,8 @@ def permute_topk(tokens, dst_info, rows, weights=None, stream=None):
     k = _choices(dst_info, T)
     _call("moeq_permute_topk", DTYPES[tokens.dtype], p, _row_stride(tokens), T, H,
           _ptr(dst_info, torch.int32, "dst_info"), k,
-          _shaped(weights, (T, k), torch.float32, "weights"),
-          _shaped(_given(rows, "rows"), (rows.shape[0], H), tokens.dtype, "rows"), rows.shape[0],
+          _shaped(weights, (T, k), torch.float32, "weights", True),
+          _shaped(rows, (rows.shape[0], H), tokens.dtype, "rows"), rows.shape[0],
           _stream(stream))
 
 
@@ -470,16 +479,16 @@ def permute_topk_grad(d_rows, dst_info, d_tokens, weights=None, tokens=None, d_w
     p = _rows_of(d_tokens, "d_tokens")
     T, H = d_tokens.shape
     k = _choices(dst_info, T)
-    if d_weights is not None:
-        _given(tokens, "tokens")
+    if d_weights is not None and tokens is None:
+        raise ValueError("tokens: required for d_weights")
     _call("moeq_permute_topk_grad", DTYPES[d_tokens.dtype],
           _shaped(d_rows, (d_rows.shape[0], H), d_tokens.dtype, "d_rows"), d_rows.shape[0], T, H,
           _ptr(dst_info, torch.int32, "dst_info"), k,
-          _shaped(weights, (T, k), torch.float32, "weights"),
+          _shaped(weights, (T, k), torch.float32, "weights", True),
           _shaped(d_tokens, (T, H), d_tokens.dtype, "d_tokens"),
           None if tokens is None else _rows_of(tokens, "tokens", (T, H), d_tokens.dtype),
           H if tokens is None else _row_stride(tokens),
-          _shaped(d_weights, (T, k), torch.float32, "d_weights"), _stream(stream))
+          _shaped(d_weights, (T, k), torch.float32, "d_weights", True), _stream(stream))
 
 
 def combine_topk(rows, dst_info, out, weights=None, stream=None):
@@ -492,8 +501,8 @@ def combine_topk(rows, dst_info, out, weights=None, stream=None):
     _call("moeq_combine_topk", DTYPES[out.dtype],
           _shaped(rows, (rows.shape[0], H), out.dtype, "rows"), rows.shape[0], T, H,
           _ptr(dst_info, torch.int32, "dst_info"), k,
-          _shaped(weights, (T, k), torch.float32, "weights"), _shaped(out, (T, H), out.dtype, "out"),
-          _stream(stream))
+          _shaped(weights, (T, k), torch.float32, "weights", True),
+          _shaped(out, (T, H), out.dtype, "out"), _stream(stream))
 
 
 def combine_topk_grad(d_out, dst_info, d_rows, weights=None, rows=None, d_weights=None,
@@ -504,15 +513,15 @@ def combine_topk_grad(d_out, dst_info, d_rows, weights=None, rows=None, d_weight
     p = _rows_of(d_out, "d_out")
     T, H = d_out.shape
     k = _choices(dst_info, T)
-    if d_weights is not None:
-        _given(rows, "rows")
+    if d_weights is not None and rows is None:
+        raise ValueError("rows: required for d_weights")
     n = d_rows.shape[0]
     _call("moeq_combine_topk_grad", DTYPES[d_out.dtype], p, _row_stride(d_out), T, H,
           _ptr(dst_info, torch.int32, "dst_info"), k,
-          _shaped(weights, (T, k), torch.float32, "weights"),
+          _shaped(weights, (T, k), torch.float32, "weights", True),
           _shaped(d_rows, (n, H), d_out.dtype, "d_rows"), n,
-          _shaped(rows, (n, H), d_out.dtype, "rows"),
-          _shaped(d_weights, (T, k), torch.float32, "d_weights"), _stream(stream))
+          _shaped(rows, (n, H), d_out.dtype, "rows", True),
+          _shaped(d_weights, (T, k), torch.float32, "d_weights", True), _stream(stream))
 
 
 def _blocks128(n):
@@ -525,8 +534,8 @@ def quantize_fp8_block(inp, out, scales, stream=None):
     p = _rows_of(inp, "inp", dtype=torch.bfloat16)
     T, K = inp.shape
     _call("moeq_quantize_fp8_block", p, _row_stride(inp), T, K,
-          _shaped(_given(out, "out"), (T, K), _U8, "out"),
-          _shaped(_given(scales, "scales"), (T, _blocks128(K)), torch.float32, "scales"),
+          _shaped(out, (T, K), _U8, "out"),
+          _shaped(scales, (T, _blocks128(K)), torch.float32, "scales"),
           _stream(stream))
 
 
@@ -539,7 +548,7 @@ def quantize_fp8_block_topk(tokens, dst_info, out, scales, stream=None):
     n = out.shape[0]
     _call("moeq_quantize_fp8_block_topk", p, _row_stride(tokens), T, K,
           _ptr(dst_info, torch.int32, "dst_info"), k, _shaped(out, (n, K), _U8, "out"),
-          _shaped(_given(scales, "scales"), (n, _blocks128(K)), torch.float32, "scales"), n,
+          _shaped(scales, (n, _blocks128(K)), torch.float32, "scales"), n,
           _stream(stream))
 
 
@@ -548,8 +557,8 @@ def swiglu_quantize_fp8_block(y, out, scales, stream=None):
     2j = gate_j, 2j + 1 = up_j; out [rows, I], scales [rows, ceil(I / 128)]."""
     T, I = y.shape[0], y.shape[1] // 2
     _call("moeq_swiglu_quantize_fp8_block", _shaped(y, (T, 2 * I), torch.bfloat16, "y"), T, I,
-          _shaped(_given(out, "out"), (T, I), _U8, "out"),
-          _shaped(_given(scales, "scales"), (T, _blocks128(I)), torch.float32, "scales"),
+          _shaped(out, (T, I), _U8, "out"),
+          _shaped(scales, (T, _blocks128(I)), torch.float32, "scales"),
           _stream(stream))
 
 
@@ -558,8 +567,8 @@ def quantize_fp8_block_weight(w, out, scales, stream=None):
     K] -> out of that shape, scales fp32 [E, ceil(N / 128), ceil(K / 128)]."""
     E, N, K = w.shape
     _call("moeq_quantize_fp8_block_weight", _ptr(w, torch.bfloat16, "w"), E, N, K,
-          _shaped(_given(out, "out"), (E, N, K), _U8, "out"),
-          _shaped(_given(scales, "scales"), (E, _blocks128(N), _blocks128(K)), torch.float32,
+          _shaped(out, (E, N, K), _U8, "out"),
+          _shaped(scales, (E, _blocks128(N), _blocks128(K)), torch.float32,
                   "scales"), _stream(stream))
 
 
@@ -572,10 +581,10 @@ def grouped_matmul_fp8_block(c, a, b, a_scales, b_scales, a_offsets, expert_ids,
     G = expert_ids.numel() if num_active_experts is None else num_active_experts
     E, N, K = b.shape
     T = a.shape[0]
-    _call("moeq_grouped_matmul_fp8_block", _shaped(_given(c, "c"), (T, N), torch.bfloat16, "c"),
+    _call("moeq_grouped_matmul_fp8_block", _shaped(c, (T, N), torch.bfloat16, "c"),
           _shaped(a, (T, K), _U8, "a"), _ptr(b, _U8, "b"),
-          _shaped(_given(a_scales, "a_scales"), (T, _blocks128(K)), torch.float32, "a_scales"),
-          _shaped(_given(b_scales, "b_scales"), (E, _blocks128(N), _blocks128(K)), torch.float32,
+          _shaped(a_scales, (T, _blocks128(K)), torch.float32, "a_scales"),
+          _shaped(b_scales, (E, _blocks128(N), _blocks128(K)), torch.float32,
                   "b_scales"),
           _ptr(a_offsets, _U32, "a_offsets"), _ptr(expert_ids, torch.int32, "expert_ids"), T, N, K,
           E, max_tokens_per_expert, G, _stream(stream))
