@@ -24,9 +24,6 @@
 #include "launch.h"
 #include "tensormap.h"
 
-#ifndef MOEQ_B_TMAST
-#define MOEQ_B_TMAST 1
-#endif
 namespace moeq {
 
 namespace {
@@ -72,6 +69,12 @@ struct BlockGemmParams {
     uint32_t *err;
 };
 
+// A value that every lane of the (converged) warp holds, in a form the
+// compiler keeps in uniform registers.
+__device__ __forceinline__ uint32_t warp_uniform(uint32_t v) {
+    return __reduce_max_sync(0xFFFFFFFFu, v);
+}
+
 // Waits for the thread's tensor-memory loads; r is written by them.
 __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -86,8 +89,8 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
     gemm_fp8_block_kernel(const __grid_constant__ CUtensorMap tmA,
-                          const __grid_constant__ CUtensorMap tmB,
-                          const __grid_constant__ CUtensorMap tmC, const BlockGemmParams p) {
+                          const __grid_constant__ CUtensorMap tmA32,
+                          const __grid_constant__ CUtensorMap tmB, const BlockGemmParams p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full_bar[C::STAGES], done_bar[C::STAGES], tempty_bar[C::NBUF];
     __shared__ uint64_t drain_bar;
@@ -97,7 +100,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const int warp = threadIdx.x >> 5;
+    const int warp = (int)warp_uniform(threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     const int G = p.num_groups;
     const int NB = (p.N + C::BN - 1) / C::BN;
@@ -116,8 +119,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         prefix[0] = 0;
         fence_barrier_init();
         prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmA32);
         prefetch_tensormap(&tmB);
-        prefetch_tensormap(&tmC);
     }
     // everything above touches only shared memory and the kernel parameters
     pdl_wait();
@@ -157,8 +160,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t total = prefix[G];
-    const uint32_t tmem = tmem_slot;
+    const uint32_t total = warp_uniform(prefix[G]);
+    const uint32_t tmem = warp_uniform(tmem_slot);
 
     if (warp < C::SUM_WARP0) {
     if constexpr (C::NREG) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::NREG_CTRL));
@@ -171,15 +174,27 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
                 const Tile tl = decode_tile(prefix, G, t, NB);
                 const int e = __ldg(p.expert_ids + tl.g);
-                const int row0 = (int)__ldg(p.offsets + tl.g) + tl.mb * C::BM;
+                const uint32_t r0 = __ldg(p.offsets + tl.g), r1 = __ldg(p.offsets + tl.g + 1);
+                const int row0 = (int)r0 + tl.mb * C::BM;
+                // of a partial m-block only the 32-row boxes that hold rows of the
+                // group are loaded; what the rest of the stage holds only reaches
+                // rows that are dropped
+                const int boxes = (min((int)r1 - row0, C::BM) + 31) / 32;
+                const uint32_t tx = boxes * 32 * C::BK + C::B_BYTES;
                 for (int kb = 0; kb < KB; ++kb) {
                     if (!mbar_wait(&done_bar[stage], phase ^ 1u, abort_v, p.err)) {
                         ok = false;
                         break;
                     }
                     uint8_t *sa = smem + stage * C::STAGE_BYTES;
-                    mbar_arrive_expect_tx(&full_bar[stage], C::STAGE_BYTES);
-                    tma_load_2d(sa, &tmA, &full_bar[stage], kb * C::BK, row0, pol);
+                    mbar_arrive_expect_tx(&full_bar[stage], tx);
+                    if (boxes == C::BM / 32) {
+                        tma_load_2d(sa, &tmA, &full_bar[stage], kb * C::BK, row0, pol);
+                    } else {
+                        for (int i = 0; i < boxes; ++i)
+                            tma_load_2d(sa + i * 32 * C::BK, &tmA32, &full_bar[stage], kb * C::BK,
+                                        row0 + i * 32, pol);
+                    }
                     tma_load_3d(sa + C::A_BYTES, &tmB, &full_bar[stage], kb * C::BK,
                                 tl.nb * C::BN, e, pol);
                     ++issued;
@@ -205,11 +220,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int kb = 0; kb < KB; ++kb) {
                 // the operands are mostly there first: their wait is paid while
                 // the accumulator is still being read
-                if (!mbar_wait(&full_bar[stage], phase, abort_v, p.err) ||
-                    !mbar_wait(&tempty_bar[buf], bphase ^ 1u, abort_v, p.err)) {
-                    ok = false;
-                    break;
-                }
+                ok = mbar_wait(&full_bar[stage], phase, abort_v, p.err) &&
+                     mbar_wait(&tempty_bar[buf], bphase ^ 1u, abort_v, p.err);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
                 tc_fence_after();
                 if (leader) {
                     const uint32_t off = (uint32_t)(stage * C::STAGE_BYTES) >> 4;
@@ -327,15 +341,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             if (!ok) break;
             // bf16 out through the warp's 32 x 32 staging buffer (64-byte rows
-            // whose 16-byte pieces are XOR-swizzled by row pair, the tensor
-            // map's 64-byte swizzle): one tensor store where all 32 rows lie in
-            // the group, else the group's rows by four lanes each
+            // whose 16-byte pieces are XOR-swizzled by row pair, free of bank
+            // conflicts), stored with four lanes per row
 #pragma unroll
             for (int ch = 0; ch < C::CHUNKS_W; ++ch) {
                 const int nc = ncol0 + ch * 32;
                 if (nc >= p.N) break;
-                if (MOEQ_B_TMAST && lane == 0) bulk_wait_read_all();
-                __syncwarp();
+                __syncwarp();  // the last chunk has been read
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     uint32_t w[4];
@@ -347,28 +359,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     st_shared_v4(sbuf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), w[0], w[1], w[2],
                                  w[3]);
                 }
-                if (MOEQ_B_TMAST && nvalid == 32) {
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tma_store_2d(&tmC, sbuf, nc, (int)(row - lane));
-                        bulk_commit();
-                    }
-                } else {
-                    __syncwarp();
-                    const int k = lane & 3, n = nc + k * 8;
+                __syncwarp();
+                const int k = lane & 3, n = nc + k * 8;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int rr = (lane >> 2) + 8 * i;
-                        const uint4 v = ld_shared_v4(sbuf + rr * 64 + ((k ^ ((rr >> 1) & 3)) << 4));
-                        if (rr < nvalid && n < p.N &&
-                            store_ok(row - lane + rr < p.total_rows && n + 8 <= p.N, p.err))
-                            st_global_v4(p.c + (row - lane + rr) * p.N + n, v.x, v.y, v.z, v.w);
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    const int rr = (lane >> 2) + 8 * i;
+                    const uint4 v = ld_shared_v4(sbuf + rr * 64 + ((k ^ ((rr >> 1) & 3)) << 4));
+                    if (rr < nvalid && n < p.N &&
+                        store_ok(row - lane + rr < p.total_rows && n + 8 <= p.N, p.err))
+                        st_global_v4(p.c + (row - lane + rr) * p.N + n, v.x, v.y, v.z, v.w);
                 }
             }
         }
-        if (lane == 0) bulk_wait_all();
     }
 
     pdl_trigger();
@@ -394,22 +396,14 @@ template <int BN, int STAGES, int SUM_WARPS>
 cudaError_t run_block_gemm(const GemmBlockArgs &a, cudaStream_t s) {
     using C = BlockCfg<BN, STAGES, SUM_WARPS>;
     const int64_t T = a.groups.total_rows;
-    CUtensorMap tA, tB, tC;
+    CUtensorMap tA, tA32, tB;
     cuuint64_t da[2] = {(cuuint64_t)a.K, (cuuint64_t)T};
     cuuint64_t sa[1] = {(cuuint64_t)a.K};
     cuuint64_t db[3] = {(cuuint64_t)a.K, (cuuint64_t)a.N, (cuuint64_t)a.groups.num_experts};
     cuuint64_t sb[2] = {(cuuint64_t)a.K, (cuuint64_t)(a.K * a.N)};
-    if (!make_map(&tA, a.a, 2, da, sa, C::BM)) return cudaErrorInvalidValue;
-    if (!make_map(&tB, a.b, 3, db, sb, BN)) return cudaErrorInvalidValue;
-    // bf16 output, boxes of 32 rows x 32 columns in the staging buffer's swizzle
-    cuuint64_t dc[2] = {(cuuint64_t)a.N, (cuuint64_t)T};
-    cuuint64_t sc[1] = {(cuuint64_t)a.N * 2};
-    cuuint32_t bc[2] = {32, 32}, ec[2] = {1, 1};
-    if (encode_fn()(&tC, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.c, dc, sc, bc, ec,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-                    CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    if (!make_map(&tA, a.a, 2, da, sa, C::BM) || !make_map(&tA32, a.a, 2, da, sa, 32))
         return cudaErrorInvalidValue;
+    if (!make_map(&tB, a.b, 3, db, sb, BN)) return cudaErrorInvalidValue;
     const BlockGemmParams p{a.groups.row_offsets, a.groups.expert_ids, a.groups.num_groups,
                             a.groups.num_experts, T, (int)a.N, (int)a.K, a.a_scales, a.b_scales,
                             static_cast<uint16_t *>(a.c), a.err};
@@ -437,7 +431,7 @@ cudaError_t run_block_gemm(const GemmBlockArgs &a, cudaStream_t s) {
     // upper bound of the tiles the offsets can give
     const int64_t tiles = (T / C::BM + a.groups.num_groups) * ((a.N + BN - 1) / BN);
     const unsigned grid = (unsigned)(tiles < sm_count() ? tiles : sm_count());
-    return launch_pdl(kern, grid, C::THREADS, C::SMEM_BYTES, s, tA, tB, tC, p);
+    return launch_pdl(kern, grid, C::THREADS, C::SMEM_BYTES, s, tA, tA32, tB, p);
 }
 
 }  // namespace
