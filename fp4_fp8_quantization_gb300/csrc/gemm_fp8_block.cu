@@ -18,7 +18,7 @@
 //    one paired fused multiply-add per two elements.
 // Persistent CTAs, one per SM, walk the tiles of all groups (n fastest).
 // Every wait is bounded and sets the device error word instead of hanging.
-#include <cstring>
+#include <algorithm>
 
 #include "common.cuh"
 #include "launch.h"
@@ -28,9 +28,11 @@ namespace moeq {
 
 namespace {
 
-template <int BN_, int STAGES_, int SUM_WARPS_>
+template <int BM_, int BN_, int STAGES_, int SUM_WARPS_>
 struct BlockCfg {
-    static constexpr int BM = 128, BN = BN_, STAGES = STAGES_, SUM_WARPS = SUM_WARPS_;
+    static constexpr int MMA_M = 128;
+    static constexpr int BM = BM_;     // rows of an m-block; the MMAs' other rows are dropped
+    static constexpr int BN = BN_, STAGES = STAGES_, SUM_WARPS = SUM_WARPS_;
     static constexpr int BK = 128;
     static constexpr int NBUF = 512 / BN < 4 ? 512 / BN : 4;   // accumulators
     static constexpr int TMEM_COLS = NBUF * BN;
@@ -38,18 +40,23 @@ struct BlockCfg {
     static constexpr int COLS_W = BN / (SUM_WARPS / 4), CHUNKS_W = COLS_W / 32;
     static constexpr int SUM_WARP0 = 4;  // warps 0 and 1 work, 2 and 3 fill their warpgroup
     static constexpr int THREADS = 32 * (SUM_WARP0 + SUM_WARPS);
-    // 128 sums per thread do not fit the 168 registers that 384 threads leave
-    // each: the control warpgroup gives up registers to the two sum warpgroups
-    // (setmaxnreg redistributes exactly the registers the block is launched
-    // with; the host checks the compiled count before launching)
-    static constexpr bool NREG = COLS_W == 128;
+    // the sums and two 32-column loads do not fit the registers that all the
+    // threads of an SM leave each: the control warpgroup gives up registers to
+    // the sum warpgroups (setmaxnreg redistributes exactly the registers the
+    // block is launched with; the host checks the compiled count before
+    // launching)
     static constexpr int LAUNCH_REGS = 65536 / THREADS / 8 * 8;
+    static constexpr bool NREG = COLS_W + 64 + 48 > LAUNCH_REGS;
     static constexpr int NREG_CTRL = 56;
     static constexpr int NREG_SUM =
         NREG ? (THREADS * LAUNCH_REGS - 32 * SUM_WARP0 * NREG_CTRL) / (32 * SUM_WARPS) / 8 * 8 : 0;
     static constexpr int BUF_BYTES = 2048;  // staging of a 32 x 32 bf16 chunk per warp
     static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SUM_WARPS * BUF_BYTES + 1024;
     static_assert(SMEM_BYTES + 4 * (kMaxGroups + 1) + 512 <= 227 * 1024, "shared memory per CTA");
+    // an MMA reads MMA_M rows of A, past a smaller m-block's end whatever is there
+    static_assert(B_BYTES + SUM_WARPS * BUF_BYTES >= (MMA_M - BM) * BK, "A reads stay inside");
+    static_assert((TMEM_COLS & (TMEM_COLS - 1)) == 0 && TMEM_COLS <= 512, "tensor memory");
+    static_assert(STAGE_BYTES % 1024 == 0 && BM % 32 == 0, "stage alignment");
     static_assert(!NREG || (NREG_SUM >= LAUNCH_REGS && NREG_SUM <= 248 &&
                             32 * SUM_WARP0 * NREG_CTRL + 32 * SUM_WARPS * NREG_SUM <=
                                 THREADS * LAUNCH_REGS),
@@ -188,7 +195,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     }
                     uint8_t *sa = smem + stage * C::STAGE_BYTES;
                     mbar_arrive_expect_tx(&full_bar[stage], tx);
-                    if (boxes == C::BM / 32) {
+                    if (C::BM == 128 && boxes == 4) {
                         tma_load_2d(sa, &tmA, &full_bar[stage], kb * C::BK, row0, pol);
                     } else {
                         for (int i = 0; i < boxes; ++i)
@@ -230,7 +237,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         mma_f8f6f4(tmem + buf * C::BN, da0 + off + 2 * ks, db0 + off + 2 * ks,
-                                   idesc_f8_e4m3(C::BM, C::BN), ks ? 1u : 0u);
+                                   idesc_f8_e4m3(C::MMA_M, C::BN), ks ? 1u : 0u);
                     tc_commit(&done_bar[stage]);
                 }
                 __syncwarp();
@@ -266,7 +273,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const Tile tl = decode_tile(prefix, G, t, NB);
             const int e = __ldg(p.expert_ids + tl.g);
             const uint32_t r0 = __ldg(p.offsets + tl.g);
-            const int left = (int)(__ldg(p.offsets + tl.g + 1) - r0) - (tl.mb * C::BM + quad * 32);
+            const int left = quad * 32 < C::BM ? (int)(__ldg(p.offsets + tl.g + 1) - r0) -
+                                                     (tl.mb * C::BM + quad * 32)
+                                               : 0;
             const int nvalid = left <= 0 ? 0 : (left >= 32 ? 32 : left);  // this warp's rows
             const int64_t row = (int64_t)r0 + tl.mb * C::BM + quad * 32 + lane;
             const int ncol0 = tl.nb * C::BN + cgrp * C::COLS_W;
@@ -373,6 +382,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
     }
 
+    // this CTA's loads, MMAs and stores are all issued
     pdl_trigger();
     tc_fence_before();
     __syncthreads();
@@ -392,9 +402,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
 }
 
-template <int BN, int STAGES, int SUM_WARPS>
+template <class C>
 cudaError_t run_block_gemm(const GemmBlockArgs &a, cudaStream_t s) {
-    using C = BlockCfg<BN, STAGES, SUM_WARPS>;
     const int64_t T = a.groups.total_rows;
     CUtensorMap tA, tA32, tB;
     cuuint64_t da[2] = {(cuuint64_t)a.K, (cuuint64_t)T};
@@ -403,7 +412,7 @@ cudaError_t run_block_gemm(const GemmBlockArgs &a, cudaStream_t s) {
     cuuint64_t sb[2] = {(cuuint64_t)a.K, (cuuint64_t)(a.K * a.N)};
     if (!make_map(&tA, a.a, 2, da, sa, C::BM) || !make_map(&tA32, a.a, 2, da, sa, 32))
         return cudaErrorInvalidValue;
-    if (!make_map(&tB, a.b, 3, db, sb, BN)) return cudaErrorInvalidValue;
+    if (!make_map(&tB, a.b, 3, db, sb, C::BN)) return cudaErrorInvalidValue;
     const BlockGemmParams p{a.groups.row_offsets, a.groups.expert_ids, a.groups.num_groups,
                             a.groups.num_experts, T, (int)a.N, (int)a.K, a.a_scales, a.b_scales,
                             static_cast<uint16_t *>(a.c), a.err};
@@ -422,27 +431,43 @@ cudaError_t run_block_gemm(const GemmBlockArgs &a, cudaStream_t s) {
             // to launch a build that differs
             cudaFuncAttributes fa;
             attr_err = cudaFuncGetAttributes(&fa, kern);
-            if (attr_err == cudaSuccess && fa.numRegs != C::LAUNCH_REGS)
+            if (attr_err == cudaSuccess && fa.numRegs < C::LAUNCH_REGS)
                 attr_err = cudaErrorInvalidConfiguration;
         }
         return attr_err == cudaSuccess ? 1 : 0;
     });
     if (attr_err != cudaSuccess) return attr_err;
     // upper bound of the tiles the offsets can give
-    const int64_t tiles = (T / C::BM + a.groups.num_groups) * ((a.N + BN - 1) / BN);
-    const unsigned grid = (unsigned)(tiles < sm_count() ? tiles : sm_count());
+    const int64_t tiles = (T / C::BM + std::min<int64_t>(a.groups.num_groups, T)) *
+                          ((a.N + C::BN - 1) / C::BN);
+    const unsigned grid = (unsigned)std::min<int64_t>(tiles, sm_count());
     return launch_pdl(kern, grid, C::THREADS, C::SMEM_BYTES, s, tA, tA32, tB, p);
 }
 
 }  // namespace
 
+// Two tile shapes.  128 x 256: the least operand traffic per product, for
+// everything that has rows.  64 x 128: twice the CTAs per group and a ring of
+// eight stages, for few rows, where the time is the stream of the weights and
+// the SMs that take part in it.  The choice compares, per K block and in ns,
+// the full waves of tiles, each at the rate of memory or of one CTA's loop
+// (430 and 330 ns measured on streams that leave SMs idle), and the last
+// partial one at the latter.  Measured with K 4096, N 1536 (small against large
+// tiles): 8 rows over 8 experts 14.6 / 18.8 us, 16 over 16 27.2 / 22.9, 32 over
+// 29 38.5 / 43.5, 4096 over 128 135 / 142, 8192 over 128 160 / 146, 512 over 8
+// 15.6 / 19.8.
 cudaError_t launch_gemm_fp8_block(const GemmBlockArgs &a, cudaStream_t s) {
-#ifndef MOEQ_B_BN
-#define MOEQ_B_BN 256
-#define MOEQ_B_ST 4
-#define MOEQ_B_SW 8
-#endif
-    return run_block_gemm<MOEQ_B_BN, MOEQ_B_ST, MOEQ_B_SW>(a, s);
+    const int64_t T = a.groups.total_rows, g = std::min<int64_t>(a.groups.num_groups, T);
+    const int64_t sms = sm_count();
+    auto cost = [&](int64_t bm, int64_t bn, int64_t loop_ns) {
+        // m-blocks of g groups of about equal size: half of one is empty each
+        const int64_t tiles = std::max(g, T / bm + g / 2) * ((a.N + bn - 1) / bn);
+        const int64_t stream_ns = sms * bn * 128 / 6800;  // a wave's weights at 6.8 TB/s
+        return tiles / sms * std::max(loop_ns, stream_ns) + (tiles % sms ? loop_ns : 0);
+    };
+    if (cost(64, 128, 330) < cost(128, 256, 430))
+        return run_block_gemm<BlockCfg<64, 128, 8, 8>>(a, s);
+    return run_block_gemm<BlockCfg<128, 256, 4, 8>>(a, s);
 }
 
 }  // namespace moeq
