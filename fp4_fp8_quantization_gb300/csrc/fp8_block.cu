@@ -12,8 +12,11 @@
 // All are streaming kernels, bound by memory: 2 bytes read and 1 written per
 // element (1 per choice for routed tokens, each token read and quantized
 // once; 4 read for SwiGLU).
+#include <algorithm>
+
 #include "common.cuh"
 #include "launch.h"
+#include "tensormap.h"
 
 namespace moeq {
 
@@ -76,14 +79,17 @@ struct Piece {
 #pragma unroll
         for (int i = 0; i < (SWIGLU ? 2 : 1); ++i) u[i] = make_uint4(0u, 0u, 0u, 0u);
     }
-    __device__ __forceinline__ void values(float (&x)[8]) const {
+    // tab: the SiLU table, or null to compute
+    __device__ __forceinline__ void values(float (&x)[8], const float *tab) const {
         if constexpr (SWIGLU) {
             const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {  // gate in the low half, up in the high
-                const F2 h = swiglu2(__uint_as_float(w[i] << 16), __uint_as_float(w[i + 1] << 16),
-                                     __uint_as_float(w[i] & 0xFFFF0000u),
-                                     __uint_as_float(w[i + 1] & 0xFFFF0000u));
+                const F2 h = tab ? swiglu2_tab(w[i], w[i + 1], tab)
+                                 : swiglu2(__uint_as_float(w[i] << 16),
+                                           __uint_as_float(w[i + 1] << 16),
+                                           __uint_as_float(w[i] & 0xFFFF0000u),
+                                           __uint_as_float(w[i + 1] & 0xFFFF0000u));
                 x[i] = f2_lo(h);
                 x[i + 1] = f2_hi(h);
             }
@@ -93,38 +99,47 @@ struct Piece {
     }
 };
 
-// One warp per U * 256 consecutive elements of a row, all of its loads issued
-// first; 16 lanes hold a block, 8 elements each.
+// U * 256 consecutive elements of a row, a warp's work: 16 lanes hold a
+// block, 8 elements each.
 template <bool SWIGLU, int U>
-__global__ void __launch_bounds__(kWarps * 32) fp8_block_kernel(BlockParams p, int segments) {
-    pdl_wait();
-    pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int64_t t = item / segments;
-    if (t >= p.rows) return;
-    const int64_t k0 = (item - t * segments) * (U * 256) + lane * 8;
-    const int64_t KB = (p.K + kBlk - 1) / kBlk;
-    const uint16_t *row = p.in + t * p.stride;
+struct Item {
     Piece<SWIGLU> in[U];
+    float x[U][8];
+    int64_t t, k0;  // row, and the lane's first element
+    // all of the loads at once
+    __device__ __forceinline__ void load(const BlockParams &p, int64_t item, int segments,
+                                         int lane) {
+        t = item / segments;
+        k0 = (item - t * segments) * (U * 256) + lane * 8;
+        const uint16_t *row = p.in + t * p.stride;
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-        if (k0 + i * 256 < p.K)
-            in[i].load(row, k0 + i * 256);
-        else
-            in[i].zero();
+        for (int i = 0; i < U; ++i) {
+            if (t < p.rows && k0 + i * 256 < p.K)
+                in[i].load(row, k0 + i * 256);
+            else
+                in[i].zero();
+        }
     }
+    __device__ __forceinline__ void values(const float *tab) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) in[i].values(x[i], tab);
+    }
+};
+
+// Quantizes and stores the values x of the item at row t, element k0.
+template <int U>
+__device__ __forceinline__ void store_item(const BlockParams &p, const float (&x)[U][8], int64_t t,
+                                           int64_t k0, int lane) {
+    const int64_t KB = (p.K + kBlk - 1) / kBlk;
     uint2 q[U];
     float s[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        float x[8];
-        in[i].values(x);
-        float m = amax8(x);
+        float m = amax8(x[i]);
 #pragma unroll
         for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         s[i] = block_scale(m);
-        q[i] = codes8(x, __fdiv_rn(1.0f, s[i]));
+        q[i] = codes8(x[i], __fdiv_rn(1.0f, s[i]));
     }
     for (int j = 0; j < (p.dst ? p.top_k : 1); ++j) {
         int64_t r = t;
@@ -147,11 +162,64 @@ __global__ void __launch_bounds__(kWarps * 32) fp8_block_kernel(BlockParams p, i
 }
 
 template <bool SWIGLU, int U>
+__global__ void __launch_bounds__(kWarps * 32) fp8_block_kernel(BlockParams p, int segments) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    Item<SWIGLU, U> it;
+    it.load(p, (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), segments, lane);
+    if (it.t >= p.rows) return;
+    it.values(nullptr);
+    store_item<U>(p, it.x, it.t, it.k0, lane);
+}
+
+// SwiGLU with the gates' SiLU from a table of every bf16 value (the same bits
+// as computing it): persistent CTAs, each with its table.  The next item's
+// loads are in flight while one is quantized.
+constexpr int kTabWarps = 16, kTabCtas = 2;
+template <int U>
+__global__ void __launch_bounds__(kTabWarps * 32, kTabCtas)
+    fp8_block_swiglu_tab_kernel(BlockParams p, int segments) {
+    extern __shared__ float silu_tab[];
+    build_silu_table(silu_tab);
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t items = p.rows * segments, step = (int64_t)gridDim.x * kTabWarps;
+    int64_t item = (int64_t)blockIdx.x * kTabWarps + (threadIdx.x >> 5);
+    Item<true, U> it;
+    it.load(p, item, segments, lane);
+    while (item < items) {
+        it.values(silu_tab);
+        const int64_t t = it.t, k0 = it.k0;
+        float x[U][8];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[i][k] = it.x[i][k];
+        item += step;
+        it.load(p, item, segments, lane);
+        store_item<U>(p, x, t, k0, lane);
+    }
+}
+
+template <bool SWIGLU, int U>
 cudaError_t run_fp8_block(const BlockParams &p, cudaStream_t s) {
     const int64_t segments = (p.K + U * 256 - 1) / (U * 256);
     const int64_t blocks = (p.rows * segments + kWarps - 1) / kWarps;
     if (blocks >= (int64_t)1 << 31) return cudaErrorNotSupported;
     return launch_pdl(fp8_block_kernel<SWIGLU, U>, (unsigned)blocks, kWarps * 32, 0, s, p,
+                      (int)segments);
+}
+
+// kSiluTableBytes (32 KB) of dynamic shared memory need no opt-in.
+template <int U>
+cudaError_t run_swiglu_tab(const BlockParams &p, cudaStream_t s) {
+    const int64_t segments = (p.K + U * 256 - 1) / (U * 256);
+    const int64_t blocks = (p.rows * segments + kTabWarps - 1) / kTabWarps;
+    const unsigned grid = (unsigned)std::min<int64_t>(blocks, sm_count() * kTabCtas);
+    return launch_pdl(fp8_block_swiglu_tab_kernel<U>, grid, kTabWarps * 32, kSiluTableBytes, s, p,
                       (int)segments);
 }
 
@@ -201,11 +269,11 @@ __global__ void __launch_bounds__(256) fp8_block_weight_kernel(const uint16_t *w
 cudaError_t launch_fp8_block(const Fp8BlockArgs &a, cudaStream_t s) {
     const BlockParams p{static_cast<const uint16_t *>(a.in), a.stride, a.rows, a.K, a.dst,
                         a.top_k, a.out_rows, a.out, a.scales, a.err};
-#ifndef MOEQ_QB_U
-#define MOEQ_QB_U 4
-#define MOEQ_QB_US 2
-#endif
-    return a.swiglu ? run_fp8_block<true, MOEQ_QB_US>(p, s) : run_fp8_block<false, MOEQ_QB_U>(p, s);
+    if (!a.swiglu) return run_fp8_block<false, 4>(p, s);
+    // the table pays for its construction from about 2^24 values on: 8191 x 1536
+    // 16.8 us computed, 17.2 by table; 131072 x 1536 230 and 208
+    if (a.rows * a.K < (int64_t)1 << 24) return run_fp8_block<true, 2>(p, s);
+    return run_swiglu_tab<2>(p, s);
 }
 
 cudaError_t launch_fp8_block_weight(const void *w, int64_t E, int64_t N, int64_t K, uint8_t *out,

@@ -305,6 +305,23 @@ def test_swiglu_quantize_bit_exact(R, I):
     _check_bytes(q, s, ref)
 
 
+def test_swiglu_quantize_large_is_the_small_one():
+    """Past 2^24 values the SiLU comes from a table: the bytes of the same rows
+    in a small call, every bf16 gate among them."""
+    R, I = 16400, 1040
+    y = synth.bf16_normal((R, 2 * I), 2.0, seed=3, device=DEV)
+    bits = torch.arange(1 << 16, device=DEV, dtype=torch.int32).to(torch.int16)
+    y[-64:].view(torch.int16).view(-1, 2)[: 1 << 16, 0] = bits   # 64 rows hold 66560 gates
+    q = torch.zeros((R, I), dtype=torch.uint8, device=DEV)
+    s = torch.zeros((R, (I + 127) // 128), device=DEV)
+    moeq.swiglu_quantize_fp8_block(y, q, s)
+    for r0 in range(0, R, 8200):
+        q2, s2 = torch.ones_like(q[:8200]), torch.ones_like(s[:8200])
+        moeq.swiglu_quantize_fp8_block(y[r0:r0 + 8200], q2, s2)
+        assert torch.equal(q[r0:r0 + 8200], q2)
+        assert torch.equal(s[r0:r0 + 8200].view(torch.int32), s2.view(torch.int32))
+
+
 @pytest.mark.parametrize("E,N,K", [(1, 1, 16), (3, 128, 128), (2, 200, 336), (4, 136, 1024)])
 def test_quantize_weight_bit_exact(E, N, K):
     w = synth.bf16_normal((E, N, K), 0.1, seed=N, outlier_p=0.001, outlier_scale=100.0)
