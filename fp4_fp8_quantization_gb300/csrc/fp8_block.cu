@@ -269,11 +269,28 @@ __global__ void __launch_bounds__(256) fp8_block_weight_kernel(const uint16_t *w
 cudaError_t launch_fp8_block(const Fp8BlockArgs &a, cudaStream_t s) {
     const BlockParams p{static_cast<const uint16_t *>(a.in), a.stride, a.rows, a.K, a.dst,
                         a.top_k, a.out_rows, a.out, a.scales, a.err};
-    if (!a.swiglu) return run_fp8_block<false, 4>(p, s);
-    // the table pays for its construction from about 2^24 values on: 8191 x 1536
-    // 16.8 us computed, 17.2 by table; 131072 x 1536 230 and 208
-    if (a.rows * a.K < (int64_t)1 << 24) return run_fp8_block<true, 2>(p, s);
-    return run_swiglu_tab<2>(p, s);
+    // of at most 4 (3 with SwiGLU) loads per lane the most that leave the fewest
+    // of a row's last warp without an element: 13119 x 592 SwiGLU 19.1 us with 2
+    // of them, 14.7 with 3; 5775 x 1376 rows 8.7 us with 4, 6.7 with 3
+    const int64_t n = (a.K + 255) / 256;
+    int u = 1;
+    for (int i = 2; i <= (a.swiglu ? 3 : 4); ++i)
+        if ((n + i - 1) / i * i <= (n + u - 1) / u * u) u = i;
+    if (!a.swiglu)
+        return u == 1   ? run_fp8_block<false, 1>(p, s)
+               : u == 2 ? run_fp8_block<false, 2>(p, s)
+               : u == 3 ? run_fp8_block<false, 3>(p, s)
+                        : run_fp8_block<false, 4>(p, s);
+    // the table pays for its construction from about 2^25 values on: 8191 x 1536
+    // 16.8 us computed, 19.1 by table; 32768 x 1536 57.9 and 54.1; 131072 x 1536
+    // 222 and 201
+    if (a.rows * a.K < (int64_t)1 << 25)
+        return u == 1   ? run_fp8_block<true, 1>(p, s)
+               : u == 2 ? run_fp8_block<true, 2>(p, s)
+                        : run_fp8_block<true, 3>(p, s);
+    return u == 1   ? run_swiglu_tab<1>(p, s)
+           : u == 2 ? run_swiglu_tab<2>(p, s)
+                    : run_swiglu_tab<3>(p, s);
 }
 
 cudaError_t launch_fp8_block_weight(const void *w, int64_t E, int64_t N, int64_t K, uint8_t *out,

@@ -108,49 +108,83 @@ struct Choices {
     }
 };
 
-// The KC dot products of a CTA's threads, summed and stored in d_w.  Every
-// thread calls it; the order of the sum is fixed by the CTA's size.
-template <int KC>
+// How the pieces of a token are dealt out.
+enum Form {
+    kPiece,  // one per thread: grid (tokens, shares of a row)
+    kFlat,   // one per thread of a flat grid, for short rows
+    kCta,    // a CTA per token, with the dots of the weights' gradient
+    kWarp    // a warp per token with the dots, for short rows
+};
+
+struct Place {
+    int64_t t, at, step;  // token, first byte and stride of the thread's pieces
+};
+
+template <int FORM>
+__device__ __forceinline__ Place my_place(const RowsParams &p) {
+    if constexpr (FORM == kPiece)
+        return {(int64_t)blockIdx.x, ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * 16,
+                p.row_bytes};
+    if constexpr (FORM == kFlat) {  // the host keeps tokens * pieces below 2^32
+        const uint32_t i = blockIdx.x * blockDim.x + threadIdx.x;
+        const uint32_t pieces = (uint32_t)(p.row_bytes >> 4), t = i / pieces;
+        return {(int64_t)t, (int64_t)(i - t * pieces) * 16, p.row_bytes};
+    }
+    if constexpr (FORM == kCta)
+        return {(int64_t)blockIdx.x, (int64_t)threadIdx.x * 16, (int64_t)blockDim.x * 16};
+    return {(int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5),
+            (int64_t)(threadIdx.x & 31) * 16, 512};
+}
+
+// The KC dot products of a token's threads, summed and stored in d_w.  Every
+// thread of the token calls it; the order of the sum is fixed by their number.
+template <int FORM, int KC>
 __device__ __forceinline__ void store_dots(const RowsParams &p, int64_t t, float (&s)[KC]) {
-    __shared__ float part[8][KC];
 #pragma unroll
     for (int j = 0; j < KC; ++j)
 #pragma unroll
         for (int o = 16; o; o >>= 1) s[j] = __fadd_rn(s[j], __shfl_xor_sync(0xFFFFFFFFu, s[j], o));
-    if ((threadIdx.x & 31) == 0) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (FORM == kWarp) {
 #pragma unroll
-        for (int j = 0; j < KC; ++j) part[threadIdx.x >> 5][j] = s[j];
-    }
-    __syncthreads();
-    if ((int)threadIdx.x < p.top_k) {
-        float v = 0.0f;
-        for (int i = 0; i < (int)(blockDim.x >> 5); ++i) v = __fadd_rn(v, part[i][threadIdx.x]);
-        p.dw[t * p.top_k + threadIdx.x] = v;
+        for (int j = 0; j < KC; ++j)
+            if (lane == j && j < p.top_k) p.dw[t * p.top_k + j] = s[j];
+    } else {
+        __shared__ float part[4][KC];
+        if (lane == 0) {
+#pragma unroll
+            for (int j = 0; j < KC; ++j) part[threadIdx.x >> 5][j] = s[j];
+        }
+        __syncthreads();
+        if ((int)threadIdx.x < p.top_k) {
+            float v = 0.0f;
+            for (int i = 0; i < (int)(blockDim.x >> 5); ++i) v = __fadd_rn(v, part[i][threadIdx.x]);
+            p.dw[t * p.top_k + threadIdx.x] = v;
+        }
     }
 }
 
-// Token -> rows.  Without dots: one 16-byte piece of a token per thread, grid
-// (tokens, pieces / threads).  With dots (top_k <= KC): one CTA per token; the
-// rows that the dots read are loaded KC at a time, so that a token and its
-// rows are each touched once.
-template <int DT, int KC, bool DOTS>
-__global__ void __launch_bounds__(256) spread_kernel(RowsParams p) {
+// Token -> rows.  With dots (top_k <= KC) the rows that they read are loaded
+// KC at a time, so that a token and its rows are each touched once.
+template <int DT, int KC, int FORM>
+__global__ void __launch_bounds__(160) spread_kernel(RowsParams p) {
+    constexpr bool DOTS = FORM == kCta || FORM == kWarp;
     pdl_wait();
     pdl_trigger();
-    const int64_t t = blockIdx.x;
-    int64_t at = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * 16;
+    const Place me = my_place<FORM>(p);
+    if (me.t >= p.num_tokens) return;  // a whole warp, or no dots
     float dot[KC] = {};
     for (int j0 = 0; j0 < (DOTS ? KC : p.top_k); j0 += KC) {
         Choices<KC> ch;
-        ch.load(p, t, j0, at == 0);
-        for (int64_t a = at; a < p.row_bytes; a += (int64_t)blockDim.x * 16) {
+        ch.load(p, me.t, j0, me.at == 0);
+        for (int64_t a = me.at; a < p.row_bytes; a += me.step) {
             uint4 y[DOTS ? KC : 1];
             if constexpr (DOTS) {
 #pragma unroll
                 for (int j = 0; j < KC; ++j)
                     if (ch.row[j] >= 0) y[j] = ld_stream(p.rows_in + ch.row[j] + a);
             }
-            const uint4 u = *reinterpret_cast<const uint4 *>(p.token_in + t * p.token_stride + a);
+            const uint4 u = *reinterpret_cast<const uint4 *>(p.token_in + me.t * p.token_stride + a);
             Vec<DT> x;
             x.from(u);
 #pragma unroll
@@ -172,28 +206,28 @@ __global__ void __launch_bounds__(256) spread_kernel(RowsParams p) {
                     for (int i = 0; i < Vec<DT>::N; ++i) dot[j] = __fmaf_rn(x.v[i], v.v[i], dot[j]);
                 }
             }
-            if (!DOTS) break;  // one piece per thread
         }
     }
-    if constexpr (DOTS) store_dots<KC>(p, t, dot);
+    if constexpr (DOTS) store_dots<FORM, KC>(p, me.t, dot);
 }
 
-// Rows -> token, in the same two forms; KC rows are in flight at a time.
-template <int DT, int KC, bool DOTS>
-__global__ void __launch_bounds__(256) collect_kernel(RowsParams p) {
+// Rows -> token; KC rows are in flight at a time.
+template <int DT, int KC, int FORM>
+__global__ void __launch_bounds__(160) collect_kernel(RowsParams p) {
+    constexpr bool DOTS = FORM == kCta || FORM == kWarp;
     pdl_wait();
     pdl_trigger();
-    const int64_t t = blockIdx.x;
-    const int64_t at = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * 16;
+    const Place me = my_place<FORM>(p);
+    if (me.t >= p.num_tokens) return;  // a whole warp, or no dots
     float dot[KC] = {};
     Choices<KC> ch;
-    ch.load(p, t, 0, at == 0);
-    for (int64_t a = at; a < p.row_bytes; a += (int64_t)blockDim.x * 16) {
+    ch.load(p, me.t, 0, me.at == 0);
+    for (int64_t a = me.at; a < p.row_bytes; a += me.step) {
         Vec<DT> acc, x;
 #pragma unroll
         for (int i = 0; i < Vec<DT>::N; ++i) acc.v[i] = 0.0f;
         if constexpr (DOTS)
-            x.from(*reinterpret_cast<const uint4 *>(p.token_in + t * p.token_stride + a));
+            x.from(*reinterpret_cast<const uint4 *>(p.token_in + me.t * p.token_stride + a));
         for (int j0 = 0;;) {
             uint4 y[KC];
 #pragma unroll
@@ -212,13 +246,12 @@ __global__ void __launch_bounds__(256) collect_kernel(RowsParams p) {
             }
             j0 += KC;
             if (DOTS || j0 >= p.top_k) break;
-            ch.load(p, t, j0, at == 0);
+            ch.load(p, me.t, j0, me.at == 0);  // one piece per thread: read once
         }
-        if (store_ok(t < p.num_tokens, p.err))
-            *reinterpret_cast<uint4 *>(p.token_out + t * p.row_bytes + a) = acc.pack();
-        if (!DOTS) break;  // one piece per thread
+        if (store_ok(me.t < p.num_tokens, p.err))
+            *reinterpret_cast<uint4 *>(p.token_out + me.t * p.row_bytes + a) = acc.pack();
     }
-    if constexpr (DOTS) store_dots<KC>(p, t, dot);
+    if constexpr (DOTS) store_dots<FORM, KC>(p, me.t, dot);
 }
 
 // d_w[t, j] = <token_in[t], rows_in[dst[t, j]]>: one warp per choice, 0 for a
@@ -247,15 +280,14 @@ __global__ void __launch_bounds__(128) dots_kernel(RowsParams p) {
     if (lane == 0) p.dw[c] = s;
 }
 
-// Threads of a CTA for rows of `pieces` pieces: a whole short row, else the
-// first of the sizes that leaves the fewest threads of a row's last share
-// without a piece.  Small CTAs whose shares fill them are the faster ones
-// (16384 tokens, top-8, 4096 bf16: collect 182 us with 128 threads, 204 with
-// 256; with dots, two thirds idle in the last share of 320 pieces, 63 us
-// against 51), but one-piece CTAs below 96 threads are bound by their launch
-// rate (320 pieces: 83 us with 64, 44 with 160).
+// Threads of a CTA for rows of `pieces` pieces: the first of the sizes that
+// leaves the fewest threads of a row's last share without a piece.  Small CTAs
+// whose shares fill them are the faster ones (16384 tokens, top-8, 4096 bf16:
+// collect 182 us with 128 threads, 204 with 256; with dots, two thirds idle in
+// the last share of 320 pieces, 63 us against 51), but one-piece CTAs below 96
+// threads are bound by their launch rate (320 pieces: 83 us with 64, 44 with
+// 160).
 unsigned cta_threads(int64_t pieces, const int (&sizes)[3]) {
-    if (pieces <= 128) return (unsigned)(pieces + 31) / 32 * 32;
     int best = 0;
     int64_t idle = INT64_MAX;
     for (const int n : sizes) {
@@ -268,25 +300,42 @@ unsigned cta_threads(int64_t pieces, const int (&sizes)[3]) {
     return (unsigned)best;
 }
 
+template <int DT, int KC, int FORM>
+cudaError_t launch_rows(bool spread, dim3 grid, unsigned threads, const RowsParams &p,
+                        cudaStream_t s) {
+    return launch_pdl(spread ? spread_kernel<DT, KC, FORM> : collect_kernel<DT, KC, FORM>, grid,
+                      threads, 0, s, p);
+}
+
 template <int DT, int KC>
 cudaError_t run_rows(bool spread, const RowsParams &p, cudaStream_t s) {
-    const int64_t pieces = p.row_bytes / 16;
-    if (p.dw && p.top_k <= KC)
-        return launch_pdl(spread ? spread_kernel<DT, KC, true> : collect_kernel<DT, KC, true>,
-                          (unsigned)p.num_tokens, cta_threads(pieces, {128, 96, 64}), 0, s, p);
-    const unsigned threads = cta_threads(pieces, {128, 160, 96});
-    const dim3 grid((unsigned)p.num_tokens, (unsigned)((pieces + threads - 1) / threads));
-    const cudaError_t e = launch_pdl(
-        spread ? spread_kernel<DT, KC, false> : collect_kernel<DT, KC, false>, grid, threads, 0, s,
-        p);
+    const int64_t pieces = p.row_bytes / 16, T = p.num_tokens;
+    // several tokens per CTA for rows that would leave one mostly empty: top-4
+    // of 15769 x 112 fp16 33 -> 13 us forward and gradient
+    const bool shorts = pieces < 96;
+    if (p.dw && p.top_k <= KC) {
+        if (shorts) return launch_rows<DT, KC, kWarp>(spread, (unsigned)((T + 3) / 4), 128, p, s);
+        return launch_rows<DT, KC, kCta>(spread, (unsigned)T, cta_threads(pieces, {128, 96, 64}),
+                                         p, s);
+    }
+    cudaError_t e;
+    if (shorts && T * pieces < (int64_t)1 << 32) {
+        e = launch_rows<DT, KC, kFlat>(spread, (unsigned)((T * pieces + 127) / 128), 128, p, s);
+    } else {
+        const unsigned threads = cta_threads(pieces, {128, 160, 96});
+        e = launch_rows<DT, KC, kPiece>(
+            spread, dim3((unsigned)T, (unsigned)((pieces + threads - 1) / threads)), threads, p, s);
+    }
     if (e != cudaSuccess || !p.dw) return e;
-    const int64_t choices = p.num_tokens * p.top_k;  // more choices than KC: the dots apart
+    const int64_t choices = T * p.top_k;  // more choices than KC: the dots apart
     return launch_pdl(dots_kernel<DT>, (unsigned)((choices + 3) / 4), 128, 0, s, p);
 }
 
 template <int DT>
 cudaError_t run_rows(bool spread, const RowsParams &p, cudaStream_t s) {
-    return p.top_k <= 2 ? run_rows<DT, 2>(spread, p, s) : run_rows<DT, 8>(spread, p, s);
+    if (p.top_k <= 2) return run_rows<DT, 2>(spread, p, s);
+    if (p.top_k <= 4) return run_rows<DT, 4>(spread, p, s);
+    return run_rows<DT, 8>(spread, p, s);
 }
 
 }  // namespace

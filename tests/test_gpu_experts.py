@@ -104,6 +104,36 @@ def test_gate_rows_without_choices():
     assert moeq.get_device_error() == 0
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("E,k", [(3, 2), (23, 6), (32, 1), (39, 8), (72, 4), (129, 8)])
+def test_gate_many_tokens(E, k, normalize, dtype):
+    """Many tokens: against the oracle's rule on whole arrays (a stable sort),
+    with masked experts, ties, rows without a choice and NaN rows."""
+    T = 40037
+    g = torch.Generator(device=DEV)
+    g.manual_seed(E)
+    x = (torch.randn(T, E, generator=g, device=DEV) * 2).to(dtype)
+    if E > 2:
+        x[5::7, 1] = x[5::7, 0]
+    x[::11, : E // 2] = float("-inf")
+    x[17] = float("-inf")
+    x[40000, E - 1] = float("nan")
+    ids, w = _gate(x, k, normalize, 1.5)
+    v = torch.where(torch.isnan(x), float("-inf"), x).double()
+    top = torch.sort(v, dim=1, descending=True, stable=True)
+    val, want = top.values[:, :k], top.indices[:, :k].int()
+    want = torch.where(val > float("-inf"), want, -1)
+    assert torch.equal(ids, want)
+    over = val if normalize else v
+    ref = 1.5 * torch.exp(val - torch.logsumexp(over, 1, keepdim=True)).nan_to_num(0.0)
+    row = torch.ones(T, dtype=torch.bool, device=DEV)
+    row[40000] = False
+    assert torch.isnan(w[40000][ids[40000] >= 0]).all()
+    rel = _gate_tol(f64(x[row]), 1.0)
+    close(w[row], f64(ref[row]), rel * f64(ref[row]) + 1e-37)
+
+
 def test_gate_strided_rows_and_bad_ids():
     wide = torch.randn(50, 96, generator=torch.Generator().manual_seed(1)).to(DEV)
     ids, w = _gate(wide[:, :64], 4, True, 1.0)
@@ -129,6 +159,7 @@ def _dst(T, k, R, rng, drop=0.15):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("weighted", [False, True])
 @pytest.mark.parametrize("T,H,k,strided", [(1, 8, 1, False), (5, 16, 3, True), (33, 264, 2, True),
+                                           (130, 120, 4, False), (6, 1536, 4, True),
                                            (7, 1032, 8, False), (3, 4104, 5, True),
                                            (70, 64, 11, False), (2, 8192, 32, False)])
 def test_rows_and_gradients(T, H, k, strided, weighted, dtype):
@@ -245,7 +276,7 @@ def _check_bytes(q, s, ref):
     assert np.array_equal(s.cpu().numpy().view(np.uint32), ref[1].view(np.uint32))
 
 
-@pytest.mark.parametrize("R,K,pad", [(1, 16, 0), (3, 128, 8), (5, 144, 0), (17, 272, 16),
+@pytest.mark.parametrize("R,K,pad", [(1, 16, 0), (300, 592, 0), (64, 1376, 0), (7, 512, 24), (3, 128, 8), (5, 144, 0), (17, 272, 16),
                                      (4, 1040, 0), (2, 2064, 0), (130, 384, 0), (3, 7168, 0)])
 def test_quantize_rows_bit_exact(R, K, pad):
     wide = _activations(R, K + pad, seed=K + R)
@@ -293,7 +324,7 @@ def test_quantize_rows_special_values():
     _check_bytes(q, s, X.quantize_rows(x.float().numpy()))
 
 
-@pytest.mark.parametrize("R,I", [(1, 16), (7, 144), (130, 128), (33, 1536), (5, 2064)])
+@pytest.mark.parametrize("R,I", [(1, 16), (9, 384), (3, 592), (7, 144), (130, 128), (33, 1536), (5, 2064)])
 def test_swiglu_quantize_bit_exact(R, I):
     y = synth.bf16_normal((R, 2 * I), 2.0, seed=I)
     y[0, 0], y[R - 1, 2] = -float("inf"), 3e38
@@ -306,9 +337,9 @@ def test_swiglu_quantize_bit_exact(R, I):
 
 
 def test_swiglu_quantize_large_is_the_small_one():
-    """Past 2^24 values the SiLU comes from a table: the bytes of the same rows
+    """Past 2^25 values the SiLU comes from a table: the bytes of the same rows
     in a small call, every bf16 gate among them."""
-    R, I = 16400, 1040
+    R, I = 32800, 1040
     y = synth.bf16_normal((R, 2 * I), 2.0, seed=3, device=DEV)
     bits = torch.arange(1 << 16, device=DEV, dtype=torch.int32).to(torch.int16)
     y[-64:].view(torch.int16).view(-1, 2)[: 1 << 16, 0] = bits   # 64 rows hold 66560 gates
