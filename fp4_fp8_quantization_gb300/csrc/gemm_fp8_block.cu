@@ -28,7 +28,7 @@ namespace moeq {
 
 namespace {
 
-template <int BM_, int BN_, int STAGES_, int SUM_WARPS_>
+template <int BM_, int BN_, int STAGES_, int SUM_WARPS_, bool ASYNC_>
 struct BlockCfg {
     static constexpr int MMA_M = 128;
     static constexpr int BM = BM_;     // rows of an m-block; the MMAs' other rows are dropped
@@ -47,12 +47,16 @@ struct BlockCfg {
     // launching)
     static constexpr int LAUNCH_REGS = 65536 / THREADS / 8 * 8;
     static constexpr bool NREG = COLS_W + 64 + 48 > LAUNCH_REGS;
-    static constexpr int NREG_CTRL = 56;
+    static constexpr int NREG_CTRL = COLS_W == 128 ? 56 : 80;
     static constexpr int NREG_SUM =
         NREG ? (THREADS * LAUNCH_REGS - 32 * SUM_WARP0 * NREG_CTRL) / (32 * SUM_WARPS) / 8 * 8 : 0;
-    static constexpr int BUF_BYTES = 2048;  // staging of a 32 x 32 bf16 chunk per warp
+    // staging per warp of its 32 rows: ASYNC all of its columns, which leave by
+    // tensor stores during the next tile; else one 32-column chunk at a time
+    static constexpr bool ASYNC = ASYNC_;
+    static constexpr int BUF_BYTES = ASYNC ? 32 * COLS_W * 2 : 2048;
     static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SUM_WARPS * BUF_BYTES + 1024;
-    static_assert(SMEM_BYTES + 4 * (kMaxGroups + 1) + 512 <= 227 * 1024, "shared memory per CTA");
+    static_assert(SMEM_BYTES + 12 * (kMaxGroups + 1) + 512 <= 227 * 1024, "shared memory per CTA");
+    static_assert(!ASYNC || COLS_W % 64 == 0, "boxes of 64 columns");
     // an MMA reads MMA_M rows of A, past a smaller m-block's end whatever is there
     static_assert(B_BYTES + SUM_WARPS * BUF_BYTES >= (MMA_M - BM) * BK, "A reads stay inside");
     static_assert((TMEM_COLS & (TMEM_COLS - 1)) == 0 && TMEM_COLS <= 512, "tensor memory");
@@ -82,6 +86,13 @@ __device__ __forceinline__ uint32_t warp_uniform(uint32_t v) {
     return __reduce_max_sync(0xFFFFFFFFu, v);
 }
 
+// Two fp32 -> two bf16 (round to nearest even), the first in the low half.
+__device__ __forceinline__ uint32_t bf16x2(F2 v) {
+    uint32_t b;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b) : "f"(f2_hi(v)), "f"(f2_lo(v)));
+    return b;
+}
+
 // Waits for the thread's tensor-memory loads; r is written by them.
 __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -97,13 +108,16 @@ template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
     gemm_fp8_block_kernel(const __grid_constant__ CUtensorMap tmA,
                           const __grid_constant__ CUtensorMap tmA32,
-                          const __grid_constant__ CUtensorMap tmB, const BlockGemmParams p) {
+                          const __grid_constant__ CUtensorMap tmB,
+                          const __grid_constant__ CUtensorMap tmC, const BlockGemmParams p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full_bar[C::STAGES], done_bar[C::STAGES], tempty_bar[C::NBUF];
     __shared__ uint64_t drain_bar;
     __shared__ uint32_t tmem_slot, stages_done;
     __shared__ int abort_flag;
+    // per group: tiles before it, first row, expert
     __shared__ uint32_t prefix[kMaxGroups + 1];
+    __shared__ int first_row[kMaxGroups + 1], expert[kMaxGroups];
 
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -139,6 +153,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     for (int g = threadIdx.x; g < G; g += blockDim.x) {
         const uint32_t r0 = __ldg(p.offsets + g), r1 = __ldg(p.offsets + g + 1);
         const int e = __ldg(p.expert_ids + g);
+        first_row[g] = (int)r0;
+        if (g == G - 1) first_row[G] = (int)r1;
+        expert[g] = e;
         uint32_t n = 0;
         if (r1 < r0 || (int64_t)r1 > p.total_rows) {
             if (blockIdx.x == 0) set_error(p.err, MOEQ_DEVERR_BAD_OFFSETS);
@@ -180,13 +197,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             bool ok = true;
             for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
                 const Tile tl = decode_tile(prefix, G, t, NB);
-                const int e = __ldg(p.expert_ids + tl.g);
-                const uint32_t r0 = __ldg(p.offsets + tl.g), r1 = __ldg(p.offsets + tl.g + 1);
-                const int row0 = (int)r0 + tl.mb * C::BM;
+                const int e = expert[tl.g], r1 = first_row[tl.g + 1];
+                const int row0 = first_row[tl.g] + tl.mb * C::BM;
                 // of a partial m-block only the 32-row boxes that hold rows of the
                 // group are loaded; what the rest of the stage holds only reaches
                 // rows that are dropped
-                const int boxes = (min((int)r1 - row0, C::BM) + 31) / 32;
+                const int boxes = (min(r1 - row0, C::BM) + 31) / 32;
                 const uint32_t tx = boxes * 32 * C::BK + C::B_BYTES;
                 for (int kb = 0; kb < KB; ++kb) {
                     if (!mbar_wait(&done_bar[stage], phase ^ 1u, abort_v, p.err)) {
@@ -266,23 +282,41 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const uint32_t toff = ((uint32_t)(quad * 32) << 16) + cgrp * C::COLS_W;
         const uint32_t sbuf = smem_u32(smem + C::STAGES * C::STAGE_BYTES) + (warp - C::SUM_WARP0) * C::BUF_BYTES;
         const int NBLK = (p.N + 127) / 128;
+        // what this warp has of a tile: rows [row, row + nvalid) and columns from
+        // ncol, the scales of its lanes' rows and of its column block (a lane past
+        // the last row takes that row's, its sums are dropped)
+        struct Part {
+            int row, nvalid, ncol;
+            const float *sa, *sb;
+            __device__ bool work(int N) const { return nvalid > 0 && ncol < N; }
+        };
+        auto part_of = [&](uint32_t t) {
+            const Tile tl = decode_tile(prefix, G, t, NB);
+            const int e = expert[tl.g], r1 = first_row[tl.g + 1];
+            Part w;
+            w.row = first_row[tl.g] + tl.mb * C::BM + quad * 32;
+            w.nvalid = quad * 32 < C::BM ? max(0, min(32, r1 - w.row)) : 0;
+            w.ncol = tl.nb * C::BN + cgrp * C::COLS_W;
+            w.sa = p.a_scales + (int64_t)(w.row + max(0, min(lane, w.nvalid - 1))) * KB;
+            w.sb = p.b_scales + ((int64_t)e * NBLK + min(w.ncol / 128, NBLK - 1)) * KB;
+            return w;
+        };
         int buf = 0, stage = 0;
         uint32_t phase = 0;
         bool ok = true;
+        Part cur = {}, nxt = {};
+        // the scales of the next K block, on their way during this one
+        float an = 0.0f, bn = 0.0f;
+        if (blockIdx.x < total) {
+            nxt = part_of(blockIdx.x);
+            if (nxt.work(p.N)) {
+                an = __ldg(nxt.sa);
+                bn = __ldg(nxt.sb);
+            }
+        }
         for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
-            const Tile tl = decode_tile(prefix, G, t, NB);
-            const int e = __ldg(p.expert_ids + tl.g);
-            const uint32_t r0 = __ldg(p.offsets + tl.g);
-            const int left = quad * 32 < C::BM ? (int)(__ldg(p.offsets + tl.g + 1) - r0) -
-                                                     (tl.mb * C::BM + quad * 32)
-                                               : 0;
-            const int nvalid = left <= 0 ? 0 : (left >= 32 ? 32 : left);  // this warp's rows
-            const int64_t row = (int64_t)r0 + tl.mb * C::BM + quad * 32 + lane;
-            const int ncol0 = tl.nb * C::BN + cgrp * C::COLS_W;
-            const bool work = nvalid > 0 && ncol0 < p.N;
-            // a row past the group's end takes the last row's scales (its sums are dropped)
-            const float *sa = p.a_scales + (lane < nvalid ? row : row - lane + max(nvalid - 1, 0)) * KB;
-            const float *sb = p.b_scales + ((int64_t)e * NBLK + min(ncol0 / 128, NBLK - 1)) * KB;
+            cur = nxt;
+            const bool work = cur.work(p.N);
             F2 acc[C::COLS_W / 2];
 #pragma unroll
             for (int i = 0; i < C::COLS_W / 2; ++i) acc[i] = f2(0.0f, 0.0f);
@@ -300,13 +334,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         phase ^= 1u;
                     }
                 }
-                continue;
-            }
-            // the next K block's scales are on their way during this one
-            float an = __ldg(sa), bn = __ldg(sb);
+            } else {
             // the load of the next 32 columns (of the next K block at the end
             // of this one) is in flight while the last 32 are added
             uint32_t r[2][32];
+            const float *sa = cur.sa, *sb = cur.sb;
             ok = mbar_wait(&done_bar[stage], phase, abort_v, p.err);
             if (!ok) break;
             tc_fence_after();
@@ -348,38 +380,84 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
                 if (!ok) break;
             }
+            }
             if (!ok) break;
+            // the next tile's place and first scales, while this one is stored
+            if (t + gridDim.x < total) {
+                nxt = part_of(t + gridDim.x);
+                if (nxt.work(p.N)) {
+                    an = __ldg(nxt.sa);
+                    bn = __ldg(nxt.sb);
+                }
+            }
+            if (!work) continue;
+            if constexpr (C::ASYNC) {
+                // the whole part into the warp's staging buffer, in boxes of 64
+                // columns (rows of 128 bytes in the tensor map's 128-byte swizzle);
+                // the last tile's stores have long read it
+                if (lane == 0) bulk_wait_read_all();
+                __syncwarp();
+#pragma unroll
+                for (int ch = 0; ch < C::COLS_W / 64; ++ch)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const F2 *v = acc + ch * 32 + j * 4;
+                        st_shared_v4(sbuf + ch * 4096 + lane * 128 + ((j ^ (lane & 7)) << 4),
+                                     bf16x2(v[0]), bf16x2(v[1]), bf16x2(v[2]), bf16x2(v[3]));
+                    }
+                if (cur.nvalid == 32) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        for (int ch = 0; ch < C::COLS_W / 64; ++ch)
+                            if (cur.ncol + ch * 64 < p.N)
+                                tma_store_2d(&tmC, sbuf + ch * 4096, cur.ncol + ch * 64, cur.row);
+                        bulk_commit();
+                    }
+                } else {  // the end of a group: its rows only, eight lanes each
+                    __syncwarp();
+                    const int k = lane & 7;
+                    for (int ch = 0; ch < C::COLS_W / 64; ++ch) {
+                        const int n = cur.ncol + ch * 64 + k * 8;
+                        for (int rr = lane >> 3; rr < cur.nvalid; rr += 4) {
+                            const uint4 v =
+                                ld_shared_v4(sbuf + ch * 4096 + rr * 128 + ((k ^ (rr & 7)) << 4));
+                            if (n < p.N && store_ok(cur.row + rr < p.total_rows, p.err))
+                                st_global_v4(p.c + (int64_t)(cur.row + rr) * p.N + n, v.x, v.y, v.z,
+                                             v.w);
+                        }
+                    }
+                }
+                continue;
+            }
             // bf16 out through the warp's 32 x 32 staging buffer (64-byte rows
             // whose 16-byte pieces are XOR-swizzled by row pair, free of bank
             // conflicts), stored with four lanes per row
+            const int k = lane & 3, lrow = lane >> 2;
+            uint16_t *out = p.c + (int64_t)(cur.row + lrow) * p.N + cur.ncol + k * 8;
 #pragma unroll
             for (int ch = 0; ch < C::CHUNKS_W; ++ch) {
-                const int nc = ncol0 + ch * 32;
+                const int nc = cur.ncol + ch * 32;
                 if (nc >= p.N) break;
                 __syncwarp();  // the last chunk has been read
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const F2 v = acc[ch * 16 + j * 4 + i];
-                        w[i] = f32_to_bf16_bits(f2_lo(v)) | (f32_to_bf16_bits(f2_hi(v)) << 16);
-                    }
-                    st_shared_v4(sbuf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), w[0], w[1], w[2],
-                                 w[3]);
+                    const F2 *v = acc + ch * 16 + j * 4;
+                    st_shared_v4(sbuf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), bf16x2(v[0]),
+                                 bf16x2(v[1]), bf16x2(v[2]), bf16x2(v[3]));
                 }
                 __syncwarp();
-                const int k = lane & 3, n = nc + k * 8;
+                const bool in_n = nc + k * 8 < p.N;  // N is a multiple of 8
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int rr = (lane >> 2) + 8 * i;
+                    const int rr = lrow + 8 * i;
                     const uint4 v = ld_shared_v4(sbuf + rr * 64 + ((k ^ ((rr >> 1) & 3)) << 4));
-                    if (rr < nvalid && n < p.N &&
-                        store_ok(row - lane + rr < p.total_rows && n + 8 <= p.N, p.err))
-                        st_global_v4(p.c + (row - lane + rr) * p.N + n, v.x, v.y, v.z, v.w);
+                    if (rr < cur.nvalid && in_n && store_ok(cur.row + rr < p.total_rows, p.err))
+                        st_global_v4(out + (int64_t)(8 * i) * p.N + ch * 32, v.x, v.y, v.z, v.w);
                 }
             }
         }
+        if (C::ASYNC && lane == 0) bulk_wait_all();
     }
 
     // this CTA's loads, MMAs and stores are all issued
@@ -405,7 +483,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 template <class C>
 cudaError_t run_block_gemm(const GemmBlockArgs &a, cudaStream_t s) {
     const int64_t T = a.groups.total_rows;
-    CUtensorMap tA, tA32, tB;
+    CUtensorMap tA, tA32, tB, tC;
     cuuint64_t da[2] = {(cuuint64_t)a.K, (cuuint64_t)T};
     cuuint64_t sa[1] = {(cuuint64_t)a.K};
     cuuint64_t db[3] = {(cuuint64_t)a.K, (cuuint64_t)a.N, (cuuint64_t)a.groups.num_experts};
@@ -413,6 +491,15 @@ cudaError_t run_block_gemm(const GemmBlockArgs &a, cudaStream_t s) {
     if (!make_map(&tA, a.a, 2, da, sa, C::BM) || !make_map(&tA32, a.a, 2, da, sa, 32))
         return cudaErrorInvalidValue;
     if (!make_map(&tB, a.b, 3, db, sb, C::BN)) return cudaErrorInvalidValue;
+    // bf16 output, boxes of 32 rows x 64 columns in the staging buffer's swizzle
+    cuuint64_t dc[2] = {(cuuint64_t)a.N, (cuuint64_t)T};
+    cuuint64_t sc[1] = {(cuuint64_t)a.N * 2};
+    cuuint32_t bc[2] = {64, 32}, ec[2] = {1, 1};
+    if (encode_fn()(&tC, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.c, dc, sc, bc, ec,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
     const BlockGemmParams p{a.groups.row_offsets, a.groups.expert_ids, a.groups.num_groups,
                             a.groups.num_experts, T, (int)a.N, (int)a.K, a.a_scales, a.b_scales,
                             static_cast<uint16_t *>(a.c), a.err};
@@ -441,7 +528,7 @@ cudaError_t run_block_gemm(const GemmBlockArgs &a, cudaStream_t s) {
     const int64_t tiles = (T / C::BM + std::min<int64_t>(a.groups.num_groups, T)) *
                           ((a.N + C::BN - 1) / C::BN);
     const unsigned grid = (unsigned)std::min<int64_t>(tiles, sm_count());
-    return launch_pdl(kern, grid, C::THREADS, C::SMEM_BYTES, s, tA, tA32, tB, p);
+    return launch_pdl(kern, grid, C::THREADS, C::SMEM_BYTES, s, tA, tA32, tB, tC, p);
 }
 
 }  // namespace
@@ -466,8 +553,13 @@ cudaError_t launch_gemm_fp8_block(const GemmBlockArgs &a, cudaStream_t s) {
         return tiles / sms * std::max(loop_ns, stream_ns) + (tiles % sms ? loop_ns : 0);
     };
     if (cost(64, 128, 330) < cost(128, 256, 430))
-        return run_block_gemm<BlockCfg<64, 128, 8, 8>>(a, s);
-    return run_block_gemm<BlockCfg<128, 256, 4, 8>>(a, s);
+        return run_block_gemm<BlockCfg<64, 128, 8, 8, false>>(a, s);
+    // short reductions: a tile's results leave while the next one is summed, for
+    // one stage of the ring (K 224: 90 us against 116 on 48816 x 3832; K 1536
+    // 772 / 808 on 131072 x 4096; K 2480 97.2 / 97.8; K 4096 342 / 334; K 7168
+    // 1554 / 1440, single launches)
+    if (a.K <= 20 * 128) return run_block_gemm<BlockCfg<128, 256, 3, 8, true>>(a, s);
+    return run_block_gemm<BlockCfg<128, 256, 4, 8, false>>(a, s);
 }
 
 }  // namespace moeq
