@@ -18,6 +18,18 @@
 //    one paired fused multiply-add per two elements.
 // Persistent CTAs, one per SM, walk the tiles of all groups (n fastest).
 // Every wait is bounded and sets the device error word instead of hanging.
+//
+// What bounds it: with many rows, about 700 cycles of a K block (128 x 256 tile)
+// whose MMAs take 512.  The 48 KB of operands written to and read from shared
+// memory account for it (96 KB at 128 bytes a cycle would be 768), the sums need
+// 560 of them and overlap, and above that the power limit: 65536 x 7168 x 4096,
+// 64 experts, 1.46 ms a single launch (2.64 PFLOP/s), 1.62 back to back at about
+// 1.5 GHz (2.37); the rowwise-scaled GEMM on the same operands 1.33 and 1.54.
+// With few rows the stream of the weights: 512 rows over 256 experts, K 7168, N
+// 4096, 0.93 ms, 103 % of the copy rate.
+// What did not help: 64-column tensor-memory loads, polling waits (both within
+// 1 %), the scales brought to shared memory by the two idle warps (10 % slower:
+// the wait for them joins each block's chain), CTAs of 128 x 128 (30 % slower).
 #include <algorithm>
 
 #include "common.cuh"
@@ -210,7 +222,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         break;
                     }
                     uint8_t *sa = smem + stage * C::STAGE_BYTES;
+                    bool stuck = false;
+#ifdef MOEQ_TEST_STUCK_STAGE
+                    // failure-detection test build: the first stage of the CTA's
+                    // first tile is announced but never loaded
+                    stuck = t == blockIdx.x && kb == 0;
+#endif
                     mbar_arrive_expect_tx(&full_bar[stage], tx);
+                    ++issued;
+                    if (stuck) {
+                        if (++stage == C::STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                        continue;
+                    }
                     if (C::BM == 128 && boxes == 4) {
                         tma_load_2d(sa, &tmA, &full_bar[stage], kb * C::BK, row0, pol);
                     } else {
@@ -220,7 +246,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     }
                     tma_load_3d(sa + C::A_BYTES, &tmB, &full_bar[stage], kb * C::BK,
                                 tl.nb * C::BN, e, pol);
-                    ++issued;
                     if (++stage == C::STAGES) {
                         stage = 0;
                         phase ^= 1u;
@@ -277,10 +302,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     } else {
         if constexpr (C::NREG)
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::NREG_SUM));
-        const int quad = warp & 3;               // TMEM lanes 32 quad .. 32 quad + 31
-        const int cgrp = (warp - C::SUM_WARP0) >> 2;        // columns COLS_W cgrp ...
+        const int quad = warp & 3;                    // TMEM lanes 32 quad .. 32 quad + 31
+        const int cgrp = (warp - C::SUM_WARP0) >> 2;  // columns COLS_W cgrp ...
         const uint32_t toff = ((uint32_t)(quad * 32) << 16) + cgrp * C::COLS_W;
-        const uint32_t sbuf = smem_u32(smem + C::STAGES * C::STAGE_BYTES) + (warp - C::SUM_WARP0) * C::BUF_BYTES;
+        const uint32_t sbuf = smem_u32(smem + C::STAGES * C::STAGE_BYTES) +
+                              (warp - C::SUM_WARP0) * C::BUF_BYTES;
         const int NBLK = (p.N + 127) / 128;
         // what this warp has of a tile: rows [row, row + nvalid) and columns from
         // ncol, the scales of its lanes' rows and of its column block (a lane past
