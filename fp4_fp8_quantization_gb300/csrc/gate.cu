@@ -9,13 +9,16 @@
 //   d_x = p (g - <p, g>),  g_j = sum_{r: i_r = j} s d_w_r       (plain)
 //   d_x_{i_r} = s q_r (d_w_r - <q, d_w>), 0 elsewhere, q = w / s  (normalised)
 //
-// One warp per token with the whole row of logits in registers (E <= 1024),
-// one pass over memory each way.  Lane l holds logits l NV .. l NV + NV - 1,
-// read as vectors, so that among equal logits the lowest lane has the lowest
-// index.  Selection compares order-preserving integer images of the logits;
-// each lane keeps its best one at hand, and a round is one warp maximum of
-// those.  16-bit logits carry their index in the low half of the image, which
-// makes every image distinct.  Sums are fp32 in a fixed order.
+// The whole row of a token is in the registers of L lanes (32, or 8 or 16 of a
+// warp where there are many tokens; E <= 1024), one pass over memory each way.
+// Lane l of them holds logits l NV .. l NV + NV - 1, read as vectors, so that
+// among equal logits the lowest lane has the lowest index.  Selection compares
+// order-preserving integer images of the logits that hold the index in their
+// low bits, so that a round is one maximum over the lanes; an fp32 image is
+// shortened for it, and a token whose choice the shortened ones do not decide
+// is chosen again from the whole ones.  Sums are fp32 in a fixed order.
+// Bound by the integer and selection instructions of the rounds (65537 tokens x
+// 128, top-8, fp32: forward 23 us, gradient 11 us, 5.6 and 10.5 of memory).
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -93,6 +96,15 @@ constexpr uint32_t kNegInfKey16 = DT == MOEQ_BF16 ? 0x007Fu : 0x03FFu;
 // exp(x - m) for x <= m: within 2 + 1.2 |x - m| ulp, NaN for a NaN or for
 // infinity minus infinity.
 __device__ __forceinline__ float exp_diff(float x, float m) { return __expf(__fadd_rn(x, -m)); }
+
+// Maximum over groups of LANES consecutive lanes, the same in each of them.
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+    if constexpr (LANES == 32) return __reduce_max_sync(0xFFFFFFFFu, v);
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
 
 // Sum over groups of LANES consecutive lanes, the same in each of them.
 template <int LANES = 32>
@@ -186,89 +198,28 @@ __device__ __forceinline__ void store_row(uint8_t *row, int E, int j0, bool vec,
     }
 }
 
-// A lane's candidates; take(own) removes the best one in the lane where own.
-//
-// fp32, up to 8: images and indices, sorted (an odd-even transposition sort,
-// which keeps equal ones in the order of their indices).
-template <int DT, int NV>
+// A lane's candidates as sorted images, each with its index in the low IB bits
+// (largest first: the lowest index of equal ones).  16-bit logits are whole in
+// what is left; an fp32 image loses its last IB bits.
+template <int DT, int NV, int L>
 struct Candidates {
+    static constexpr int log2(int v) { return v <= 1 ? 0 : 1 + log2(v / 2); }
+    static constexpr int IB = DT == MOEQ_FP32 ? log2(L * NV) : 16;
+    static constexpr uint32_t kIdx = (1u << IB) - 1u;
+    // the largest image of -inf
+    static constexpr uint32_t kNone =
+        DT == MOEQ_FP32 ? kNegInfKey : (kNegInfKey16<DT> << 16 | 0xFFFFu);
     uint32_t key[NV];
-    int idx[NV];
-    __device__ __forceinline__ uint32_t best() const { return key[0]; }
-    __device__ __forceinline__ int at() const { return idx[0]; }
-    __device__ __forceinline__ void init(const float (&x)[NV], int) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            key[i] = order_key(x[i]);
-            idx[i] = i;
-        }
-#pragma unroll
-        for (int pass = 0; pass < NV; ++pass)
-#pragma unroll
-            for (int i = pass & 1; i + 1 < NV; i += 2) {
-                const bool swap = key[i + 1] > key[i];
-                const uint32_t k = max(key[i], key[i + 1]);
-                key[i + 1] = min(key[i], key[i + 1]);
-                key[i] = k;
-                const int a = swap ? idx[i + 1] : idx[i];
-                idx[i + 1] = swap ? idx[i] : idx[i + 1];
-                idx[i] = a;
-            }
-    }
-    __device__ __forceinline__ void take(bool own) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            key[i] = own ? (i + 1 < NV ? key[(i + 1) % NV] : 0u) : key[i];
-            if (i + 1 < NV) idx[i] = own ? idx[(i + 1) % NV] : idx[i];
-        }
-    }
-};
-
-// fp32, more: images in index order; the best is found again by a scan.
-template <int NV>
-struct ScannedCandidates {
-    uint32_t key[NV];
-    uint32_t top;
-    int pos;
-    __device__ __forceinline__ uint32_t best() const { return top; }
-    __device__ __forceinline__ int at() const { return pos; }
-    __device__ __forceinline__ void init(const float (&x)[NV], int) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) key[i] = order_key(x[i]);
-        scan();
-    }
-    __device__ __forceinline__ void scan() {
-        top = 0u;
-        pos = 0;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (key[i] > top) {  // the lowest index of equal ones
-                top = key[i];
-                pos = i;
-            }
-    }
-    __device__ __forceinline__ void take(bool own) {
-        if (!own) return;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (i == pos) key[i] = 0u;
-        scan();
-    }
-};
-template <>
-struct Candidates<MOEQ_FP32, 16> : ScannedCandidates<16> {};
-template <>
-struct Candidates<MOEQ_FP32, 32> : ScannedCandidates<32> {};
-
-// 16-bit logits: images that hold the index, sorted; the best is the first.
-template <int DT, int NV>
-struct SortedCandidates {
-    uint32_t key[NV];
-    __device__ __forceinline__ uint32_t best() const { return key[0]; }
     __device__ __forceinline__ void init(const float (&x)[NV], int j0) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            key[i] = (order_key16<DT>(x[i]) << 16) | (uint32_t)(0xFFFF - (j0 + i));
+        for (int i = 0; i < NV; ++i) {
+            uint32_t k;
+            if constexpr (DT == MOEQ_FP32)
+                k = order_key(x[i]) & ~kIdx;
+            else
+                k = order_key16<DT>(x[i]) << 16;
+            key[i] = k | (kIdx - (uint32_t)(j0 + i));
+        }
         // odd-even merge sort, largest first (NV is a power of two)
 #pragma unroll
         for (int n = 1; n < NV; n *= 2)
@@ -284,179 +235,110 @@ struct SortedCandidates {
                             key[a + b + h] = min(u, v);
                         }
     }
-    __device__ __forceinline__ void take(bool own) {
+    // The token's best image, removed from its lane.
+    __device__ __forceinline__ uint32_t next() {
+        const uint32_t mx = lanes_max<L>(key[0]);
+        const bool own = key[0] == mx;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             key[i] = own ? (i + 1 < NV ? key[(i + 1) % NV] : 0u) : key[i];
+        return mx;
     }
 };
-template <int NV>
-struct Candidates<MOEQ_BF16, NV> : SortedCandidates<MOEQ_BF16, NV> {};
-template <int NV>
-struct Candidates<MOEQ_FP16, NV> : SortedCandidates<MOEQ_FP16, NV> {};
 
-template <int DT, int NV>
-__global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateParams p) {
-    pdl_wait();
-    pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * kGateWarps + (threadIdx.x >> 5);
-    if (t >= p.num_tokens) return;
-    float x[NV];
-    load_row<DT>(p.logits + t * p.stride, p.E, lane * NV, rows_aligned<DT, NV>(p.stride), x);
-    Candidates<DT, NV> c;
-    c.init(x, lane * NV);
-    // lane r: choice r.  A round past the last logit above -inf finds an image
-    // that is not above kNegInf and is dropped below.
-    int my_j = 0;
-    uint32_t my_key = 0u, top = 0u;
-    for (int r = 0; r < p.top_k; ++r) {
-        const uint32_t mx = __reduce_max_sync(0xFFFFFFFFu, c.best());
-        int j = 0;
-        if constexpr (DT == MOEQ_FP32) {
-            const int owner = __ffs((int)__ballot_sync(0xFFFFFFFFu, c.best() == mx)) - 1;
-            j = owner * NV + __shfl_sync(0xFFFFFFFFu, c.at(), owner);
-            c.take(lane == owner);
-        } else {
-            c.take(c.best() == mx);  // images are distinct
-        }
-        if (r == 0) top = mx;
-        if (lane == r) {
-            my_j = j;
-            my_key = mx;
-        }
-    }
-    constexpr uint32_t kNone = DT == MOEQ_FP32 ? kNegInfKey : (kNegInfKey16<DT> << 16 | 0xFFFFu);
-    int id = -1;
-    float w = 0.0f;
-    if (top > kNone) {
-        float m, e = 0.0f;
-        if constexpr (DT == MOEQ_FP32) {
-            m = key_value(top);
-            if (my_key > kNone) {
-                id = my_j;
-                e = exp_diff(key_value(my_key), m);
-            }
-        } else {
-            m = key16_value<DT>(top >> 16);
-            if (my_key > kNone) {
-                id = 0xFFFF - (int)(my_key & 0xFFFFu);
-                e = exp_diff(key16_value<DT>(my_key >> 16), m);
-            }
-        }
-        // a NaN logit, or m infinite, makes either denominator NaN
-        float total = 0.0f;
-        if (p.normalize) {
-            bool nan = false;
+// The same choice from whole fp32 images, for a warp with a token whose
+// shortened ones do not decide it: the token's lane r gets choice r (-1: none
+// left) and its logit.
+template <int NV, int L>
+__device__ __forceinline__ void choose_exactly(const float (&x)[NV], int top_k, int lane,
+                                               int &my_j, float &my_v) {
+    const int sub = lane % L;
+    uint32_t key[NV];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) nan |= x[i] != x[i];
-            total = lanes_sum(e);
-            if (__any_sync(0xFFFFFFFFu, nan)) total = __int_as_float(0x7FFFFFFF);
-        } else {
+    for (int i = 0; i < NV; ++i) key[i] = order_key(x[i]);
+    for (int r = 0; r < top_k; ++r) {
+        uint32_t best = 0u;
+        int at = 0;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) total = __fadd_rn(total, exp_diff(x[i], m));
-            total = lanes_sum(total);
+        for (int i = 0; i < NV; ++i)
+            if (key[i] > best) {  // the lowest index of equal ones
+                best = key[i];
+                at = i;
+            }
+        const uint32_t mx = lanes_max<L>(best);
+        const uint32_t has = __ballot_sync(0xFFFFFFFFu, best == mx) >> (lane - sub);
+        const int owner = __ffs((int)has) - 1;  // the token's first lane with it
+        const int j = owner * NV + __shfl_sync(0xFFFFFFFFu, at, owner, L);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (sub == owner && i == at) key[i] = 0u;
+        if (sub == r) {
+            my_j = mx > kNegInfKey ? j : -1;
+            my_v = key_value(mx);
         }
-        w = __fmul_rn(__fdiv_rn(e, total), p.scale);
-    }
-    if (lane < p.top_k && store_ok(t < p.num_tokens, p.err)) {
-        p.ids[t * p.top_k + lane] = id;
-        p.weights[t * p.top_k + lane] = w;
     }
 }
 
-// Many tokens, few experts, top_k <= KC: a lane per token.  A warp brings 32
-// columns of its 32 tokens through shared memory (whole lines in, a column out
-// per lane, rows 33 words apart so that neither side has bank conflicts), and
-// each lane keeps the sorted list of its best KC, entering a logit only above
-// the last of them, so that among equal ones the lowest index stays first.
-// The sum of the plain weights runs along with the list's first as maximum.
-template <int DT, int KC>
-__global__ void __launch_bounds__(kGateWarps * 32) gate_rows_kernel(GateParams p) {
-    __shared__ float tiles[kGateWarps][32 * 33];
+// L lanes per token (top_k <= L), each with NV consecutive logits.
+template <int DT, int NV, int L>
+__global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateParams p) {
+    using Cand = Candidates<DT, NV, L>;
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    float *tile = tiles[threadIdx.x >> 5];
-    const int64_t t0 = ((int64_t)blockIdx.x * kGateWarps + (threadIdx.x >> 5)) * 32;
-    if (t0 >= p.num_tokens) return;
-    const int rows = (int)(p.num_tokens - t0 < 32 ? p.num_tokens - t0 : 32);
-    const uint8_t *in = p.logits + t0 * p.stride;
-    float v[KC], total = 0.0f;
-    int id[KC];
+    const int lane = threadIdx.x & 31, sub = lane % L;
+    const int64_t warp = (int64_t)blockIdx.x * kGateWarps + (threadIdx.x >> 5);
+    const int64_t slot = warp * (32 / L) + lane / L;
+    const bool active = slot < p.num_tokens;
+    const int64_t t = active ? slot : p.num_tokens - 1;
+    const uint8_t *row = p.logits + t * p.stride;
+    float x[NV];
+    load_row<DT>(row, p.E, sub * NV, rows_aligned<DT, NV>(p.stride), x);
+    Cand c;
+    c.init(x, sub * NV);
+    // lane r of a token: choice r.  fp32: one round more than choices; where two
+    // rounds in a row find the same image but for the index, the order is not
+    // decided
+    const int rounds = p.top_k + (DT == MOEQ_FP32 ? 1 : 0);
+    bool tie = false;
+    uint32_t my_key = 0u, last = 0xFFFFFFFFu;
+    for (int r = 0; r < rounds; ++r) {
+        const uint32_t mx = c.next();
+        if constexpr (DT == MOEQ_FP32) tie |= mx > Cand::kNone && ((mx ^ last) >> Cand::IB) == 0u;
+        last = mx;
+        if (sub == r) my_key = mx;
+    }
+    int id = -1;
+    float v = 0.0f, w = 0.0f;
+    if (my_key > Cand::kNone && sub < p.top_k) {
+        id = (int)(Cand::kIdx - (my_key & Cand::kIdx));
+        if constexpr (DT == MOEQ_FP32)
+            v = load_logit<DT>(row, id);
+        else
+            v = key16_value<DT>(my_key >> 16);
+    }
+    if constexpr (DT == MOEQ_FP32)
+        if (__any_sync(0xFFFFFFFFu, tie)) choose_exactly<NV, L>(x, p.top_k, lane, id, v);
+    const float m = __shfl_sync(0xFFFFFFFFu, v, 0, L);
+    const bool some = __shfl_sync(0xFFFFFFFFu, id, 0, L) >= 0;
+    const float e = id >= 0 ? exp_diff(v, m) : 0.0f;
+    // a NaN logit, or m infinite, makes either denominator NaN
+    float total = e;
     bool nan = false;
+    if (p.normalize) {
 #pragma unroll
-    for (int i = 0; i < KC; ++i) {
-        v[i] = -kInf;
-        id[i] = -1;
+        for (int i = 0; i < NV; ++i) nan |= x[i] != x[i];
+        if (nan) total = __int_as_float(0x7FFFFFFF);
+    } else {
+        total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) total = __fadd_rn(total, exp_diff(x[i], m));
     }
-    for (int c0 = 0; c0 < p.E; c0 += 32) {
-        const int cols = min(p.E - c0, 32);
-#pragma unroll 1
-        for (int r0 = 0; r0 < rows; r0 += 8) {
-            float x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                x[i] = r0 + i < rows && lane < cols
-                           ? load_logit<DT>(in + (r0 + i) * p.stride, c0 + lane)
-                           : -kInf;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) tile[(r0 + i) * 33 + lane] = x[i];
-        }
-        __syncwarp();
-        const float m0 = v[0];
-#pragma unroll 4
-        for (int c = 0; c < cols; ++c) {
-            const float x = tile[lane * 33 + c];
-            nan |= x != x;
-            if (x > v[KC - 1]) {
-                v[KC - 1] = x;
-                id[KC - 1] = c0 + c;
-#pragma unroll
-                for (int i = KC - 1; i > 0; --i) {
-                    const bool up = v[i] > v[i - 1];
-                    const float a = v[i - 1], b = v[i];
-                    const int ia = id[i - 1], ib = id[i];
-                    v[i - 1] = up ? b : a;
-                    v[i] = up ? a : b;
-                    id[i - 1] = up ? ib : ia;
-                    id[i] = up ? ia : ib;
-                }
-            }
-        }
-        if (!p.normalize && v[0] > -kInf) {
-            float part = 0.0f;
-#pragma unroll 4
-            for (int c = 0; c < cols; ++c)
-                part = __fadd_rn(part, exp_diff(tile[lane * 33 + c], v[0]));
-            total = __fmaf_rn(total, exp_diff(m0, v[0]), part);
-        }
-        __syncwarp();
+    total = lanes_sum<L>(total);
+    if (some) w = __fmul_rn(__fdiv_rn(e, total), p.scale);
+    if (active && sub < p.top_k && store_ok(t < p.num_tokens, p.err)) {
+        p.ids[t * p.top_k + sub] = id;
+        p.weights[t * p.top_k + sub] = w;
     }
-    float e[KC], sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < KC; ++i) {
-        e[i] = i < p.top_k && id[i] >= 0 ? exp_diff(v[i], v[0]) : 0.0f;
-        sum = __fadd_rn(sum, e[i]);
-    }
-    if (p.normalize) total = sum;
-    if (nan) total = __int_as_float(0x7FFFFFFF);
-    // ids and weights leave through shared memory, in whole lines
-    float *ids = tile, *w = tile + 32 * KC;
-#pragma unroll
-    for (int i = 0; i < KC; ++i)
-        if (i < p.top_k) {
-            ids[lane * p.top_k + i] = __int_as_float(id[i]);
-            w[lane * p.top_k + i] =
-                id[0] < 0 ? 0.0f : __fmul_rn(__fdiv_rn(e[i], total), p.scale);
-        }
-    __syncwarp();
-    const int64_t at = t0 * p.top_k;
-    for (int i = lane; i < rows * p.top_k; i += 32)
-        if (store_ok(at + i < p.num_tokens * p.top_k, p.err)) {
-            p.ids[at + i] = __float_as_int(ids[i]);
-            p.weights[at + i] = w[i];
-        }
 }
 
 // The gradient: LANES lanes per token (top_k <= LANES), each with V vectors of
@@ -552,26 +434,31 @@ cudaError_t run_grad(const GateParams &p, cudaStream_t s) {
     return go(gate_grad_kernel<DT, 32, 8>, 32);
 }
 
+template <int DT, int NV, int L>
+cudaError_t run_gate_lanes(const GateParams &p, cudaStream_t s) {
+    const int64_t per_cta = kGateWarps * 32 / L;
+    return launch_pdl(gate_kernel<DT, NV, L>, (unsigned)((p.num_tokens + per_cta - 1) / per_cta),
+                      kGateWarps * 32, 0, s, p);
+}
+
 template <int DT>
 cudaError_t run_gate(const GateParams &p, cudaStream_t s) {
-    // a lane per token once that fills the GPU and the rows are short: 131072 x
-    // 32, top-8 15.0 us against 34.6 with a warp per token, 32768 x 64 11.2
-    // against 11.1, 8192 x 64 9.5 against 4.3, 65537 x 128 34.4 against 28.8
-    if (p.top_k <= 8 && p.E <= 64 && p.num_tokens >= 1024 * (int64_t)p.E)
-        return launch_pdl(p.top_k <= 2   ? gate_rows_kernel<DT, 2>
-                          : p.top_k <= 4 ? gate_rows_kernel<DT, 4>
-                                         : gate_rows_kernel<DT, 8>,
-                          (unsigned)((p.num_tokens + 32 * kGateWarps - 1) / (32 * kGateWarps)),
-                          kGateWarps * 32, 0, s, p);
-    const unsigned blocks = (unsigned)((p.num_tokens + kGateWarps - 1) / kGateWarps);
+    // many tokens: as few lanes per token as leave each at most 8 logits, so that
+    // the rounds of a warp's tokens are shared.  65536 tokens x 32, top-8: 8.3 us
+    // with 8 lanes, 20.4 with 32; x 64 11.7 / 22.7; x 128 23.3 with 16, 29.7 with
+    // 32, 32.7 with 8; but 1024 x 128 3.1 / 2.3
+    if (p.num_tokens >= 4096) {
+        if (p.E <= 32 && p.top_k <= 8) return run_gate_lanes<DT, 4, 8>(p, s);
+        if (p.E <= 64 && p.top_k <= 8) return run_gate_lanes<DT, 8, 8>(p, s);
+        if (p.E <= 128 && p.top_k <= 16) return run_gate_lanes<DT, 8, 16>(p, s);
+    }
     const int nv = (p.E + 31) / 32;
-    void (*kern)(GateParams) = nv <= 1    ? gate_kernel<DT, 1>
-                               : nv <= 2  ? gate_kernel<DT, 2>
-                               : nv <= 4  ? gate_kernel<DT, 4>
-                               : nv <= 8  ? gate_kernel<DT, 8>
-                               : nv <= 16 ? gate_kernel<DT, 16>
-                                          : gate_kernel<DT, 32>;
-    return launch_pdl(kern, blocks, kGateWarps * 32, 0, s, p);
+    return nv <= 1    ? run_gate_lanes<DT, 1, 32>(p, s)
+           : nv <= 2  ? run_gate_lanes<DT, 2, 32>(p, s)
+           : nv <= 4  ? run_gate_lanes<DT, 4, 32>(p, s)
+           : nv <= 8  ? run_gate_lanes<DT, 8, 32>(p, s)
+           : nv <= 16 ? run_gate_lanes<DT, 16, 32>(p, s)
+                      : run_gate_lanes<DT, 32, 32>(p, s);
 }
 
 template <int DT>

@@ -104,6 +104,24 @@ def test_gate_rows_without_choices():
     assert moeq.get_device_error() == 0
 
 
+@pytest.mark.parametrize("E,k", [(8, 3), (100, 8), (256, 8), (300, 32), (1024, 9)])
+def test_gate_orders_logits_that_differ_in_their_last_bits(E, k):
+    """fp32 logits one ulp apart, equal ones and both zeros among them."""
+    rng = np.random.default_rng(E)
+    base = rng.normal(size=(64, E)).astype(np.float32)
+    base[8:16] = 1.0
+    base[16:24] = 0.0
+    base[24:32] = -3.5
+    steps = rng.integers(-3, 4, size=(64, E))
+    x = (base.view(np.int32) + np.where(base == 0, 0, steps).astype(np.int32)).view(np.float32)
+    x[16:24, ::2] = -0.0
+    x[:, ::5] = x[:, 1::5][:, :1]
+    ids, w = _gate(torch.from_numpy(x).to(DEV), k, True, 1.0)
+    want_ids, want_w = X.gate_topk(x, k, True, 1.0)
+    assert np.array_equal(ids.cpu().numpy(), want_ids)
+    close(w, want_w, _gate_tol(x.astype(np.float64), 1.0) * want_w)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("normalize", [False, True])
 @pytest.mark.parametrize("E,k", [(3, 2), (23, 6), (32, 1), (39, 8), (72, 4), (129, 8)])
