@@ -26,14 +26,15 @@ inline EncodeTiledFn encode_fn() {
 
 // uint8 tensor map with 128-byte swizzled boxes of box_rows x 128 bytes.
 inline bool make_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims,
-                     const cuuint64_t *strides, cuuint32_t box_rows) {
+                     const cuuint64_t *strides, cuuint32_t box_rows,
+                     CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
     cuuint32_t box[3] = {128, box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void *>(base),
                      dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_SWIZZLE_128B, promotion,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }

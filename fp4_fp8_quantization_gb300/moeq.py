@@ -423,6 +423,13 @@ def _shaped(t, shape, dtype, name, optional=False):
     return _ptr(t, dtype, name)
 
 
+def _dtype_code(t, name):
+    code = DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {tuple(DTYPES)}")
+    return code
+
+
 def _choices(dst_info, num_tokens):
     if dst_info.dim() != 2 or dst_info.shape[0] != num_tokens or dst_info.shape[1] < 1:
         raise ValueError("dst_info: expected [num_tokens, top_k]")
@@ -476,12 +483,11 @@ def permute_topk_grad(d_rows, dst_info, d_tokens, weights=None, tokens=None, d_w
     """Gradient of permute_topk: d_tokens[t] (out) = the sum over j of
     weights[t, j] * d_rows[dst_info[t, j]]; with d_weights (out, fp32
     [num_tokens, top_k]) also <tokens[t], d_rows[dst_info[t, j]]>."""
-    p = _rows_of(d_tokens, "d_tokens")
     T, H = d_tokens.shape
     k = _choices(dst_info, T)
     if d_weights is not None and tokens is None:
         raise ValueError("tokens: required for d_weights")
-    _call("moeq_permute_topk_grad", DTYPES[d_tokens.dtype],
+    _call("moeq_permute_topk_grad", _dtype_code(d_tokens, "d_tokens"),
           _shaped(d_rows, (d_rows.shape[0], H), d_tokens.dtype, "d_rows"), d_rows.shape[0], T, H,
           _ptr(dst_info, torch.int32, "dst_info"), k,
           _shaped(weights, (T, k), torch.float32, "weights", True),
@@ -495,10 +501,9 @@ def combine_topk(rows, dst_info, out, weights=None, stream=None):
     """Rows back to their tokens: out[t] = the sum over j of weights[t, j] *
     rows[dst_info[t, j]] (weights None: 1).  rows bf16 / fp16 / fp32 [rows,
     hidden]; out of the same dtype [num_tokens, hidden]."""
-    p = _rows_of(out, "out")
     T, H = out.shape
     k = _choices(dst_info, T)
-    _call("moeq_combine_topk", DTYPES[out.dtype],
+    _call("moeq_combine_topk", _dtype_code(out, "out"),
           _shaped(rows, (rows.shape[0], H), out.dtype, "rows"), rows.shape[0], T, H,
           _ptr(dst_info, torch.int32, "dst_info"), k,
           _shaped(weights, (T, k), torch.float32, "weights", True),
