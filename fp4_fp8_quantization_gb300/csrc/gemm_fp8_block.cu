@@ -40,15 +40,18 @@ namespace moeq {
 
 namespace {
 
-template <int BM_, int BN_, int STAGES_, int SUM_WARPS_, bool ASYNC_>
+template <int BM_, int BN_, int STAGES_, int SUM_WARPS_, bool ASYNC_, int KSUB_>
 struct BlockCfg {
     static constexpr int MMA_M = 128;
     static constexpr int BM = BM_;     // rows of an m-block; the MMAs' other rows are dropped
     static constexpr int BN = BN_, STAGES = STAGES_, SUM_WARPS = SUM_WARPS_;
     static constexpr int BK = 128;
-    static constexpr int NBUF = 512 / BN < 4 ? 512 / BN : 4;   // accumulators
-    static constexpr int TMEM_COLS = NBUF * BN;
-    static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int KSUB = KSUB_;  // K blocks per stage, each with its accumulator
+    static constexpr int ACC_COLS = KSUB * BN;
+    static constexpr int NBUF = 512 / ACC_COLS < 4 ? 512 / ACC_COLS : 4;  // sets of accumulators
+    static constexpr int TMEM_COLS = NBUF * ACC_COLS;
+    static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK;  // of one K block
+    static constexpr int SUB_BYTES = A_BYTES + B_BYTES, STAGE_BYTES = KSUB * SUB_BYTES;
     static constexpr int COLS_W = BN / (SUM_WARPS / 4), CHUNKS_W = COLS_W / 32;
     static constexpr int SUM_WARP0 = 4;  // warps 0 and 1 work, 2 and 3 fill their warpgroup
     static constexpr int THREADS = 32 * (SUM_WARP0 + SUM_WARPS);
@@ -137,7 +140,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int lane = threadIdx.x & 31;
     const int G = p.num_groups;
     const int NB = (p.N + C::BN - 1) / C::BN;
-    const int KB = (p.K + C::BK - 1) / C::BK;
+    const int KB = (p.K + C::BK - 1) / C::BK;           // K blocks, and sets of KSUB
+    const int KS = (KB + C::KSUB - 1) / C::KSUB;
     volatile int *abort_v = &abort_flag;
 
     if (threadIdx.x == 0) {
@@ -151,7 +155,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         stages_done = 0;
         prefix[0] = 0;
         fence_barrier_init();
-        prefetch_tensormap(&tmA);
+        if (C::BM == 128) prefetch_tensormap(&tmA);
         prefetch_tensormap(&tmA32);
         prefetch_tensormap(&tmB);
     }
@@ -215,8 +219,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 // group are loaded; what the rest of the stage holds only reaches
                 // rows that are dropped
                 const int boxes = (min(r1 - row0, C::BM) + 31) / 32;
-                const uint32_t tx = boxes * 32 * C::BK + C::B_BYTES;
-                for (int kb = 0; kb < KB; ++kb) {
+                const uint32_t tx = C::KSUB * (boxes * 32 * C::BK + C::B_BYTES);
+                for (int kb = 0; kb < KS; ++kb) {
                     if (!mbar_wait(&done_bar[stage], phase ^ 1u, abort_v, p.err)) {
                         ok = false;
                         break;
@@ -237,15 +241,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         }
                         continue;
                     }
-                    if (C::BM == 128 && boxes == 4) {
-                        tma_load_2d(sa, &tmA, &full_bar[stage], kb * C::BK, row0, pol);
-                    } else {
-                        for (int i = 0; i < boxes; ++i)
-                            tma_load_2d(sa + i * 32 * C::BK, &tmA32, &full_bar[stage], kb * C::BK,
-                                        row0 + i * 32, pol);
+#pragma unroll
+                    for (int q = 0; q < C::KSUB; ++q) {  // past K: zeros
+                        uint8_t *s = sa + q * C::SUB_BYTES;
+                        const int k = (kb * C::KSUB + q) * C::BK;
+                        if (C::BM == 128 && boxes == 4) {
+                            tma_load_2d(s, &tmA, &full_bar[stage], k, row0, pol);
+                        } else {
+                            for (int i = 0; i < boxes; ++i)
+                                tma_load_2d(s + i * 32 * C::BK, &tmA32, &full_bar[stage], k,
+                                            row0 + i * 32, pol);
+                        }
+                        tma_load_3d(s + C::A_BYTES, &tmB, &full_bar[stage], k, tl.nb * C::BN, e, pol);
                     }
-                    tma_load_3d(sa + C::A_BYTES, &tmB, &full_bar[stage], kb * C::BK,
-                                tl.nb * C::BN, e, pol);
                     if (++stage == C::STAGES) {
                         stage = 0;
                         phase ^= 1u;
@@ -265,7 +273,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         uint32_t phase = 0, bphase = 0;
         bool ok = true;
         for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
-            for (int kb = 0; kb < KB; ++kb) {
+            for (int kb = 0; kb < KS; ++kb) {
                 // the operands are mostly there first: their wait is paid while
                 // the accumulator is still being read
                 ok = mbar_wait(&full_bar[stage], phase, abort_v, p.err) &&
@@ -276,9 +284,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (leader) {
                     const uint32_t off = (uint32_t)(stage * C::STAGE_BYTES) >> 4;
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_f8f6f4(tmem + buf * C::BN, da0 + off + 2 * ks, db0 + off + 2 * ks,
-                                   idesc_f8_e4m3(C::MMA_M, C::BN), ks ? 1u : 0u);
+                    for (int q = 0; q < 4 * C::KSUB; ++q) {
+                        const uint32_t at = off + (q / 4) * (C::SUB_BYTES >> 4) + 2 * (q & 3);
+                        mma_f8f6f4(tmem + buf * C::ACC_COLS + (q / 4) * C::BN, da0 + at, db0 + at,
+                                   idesc_f8_e4m3(C::MMA_M, C::BN), q & 3 ? 1u : 0u);
+                    }
                     tc_commit(&done_bar[stage]);
                 }
                 __syncwarp();
@@ -332,13 +342,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         bool ok = true;
         Part cur = {}, nxt = {};
         // the scales of the next K block, on their way during this one
-        float an = 0.0f, bn = 0.0f;
+        float an[C::KSUB] = {}, bn[C::KSUB] = {};
+        auto first_scales = [&]() {
+#pragma unroll
+            for (int q = 0; q < C::KSUB; ++q) {
+                an[q] = nxt.work(p.N) && q < KB ? __ldg(nxt.sa + q) : 0.0f;
+                bn[q] = nxt.work(p.N) && q < KB ? __ldg(nxt.sb + q) : 0.0f;
+            }
+        };
         if (blockIdx.x < total) {
             nxt = part_of(blockIdx.x);
-            if (nxt.work(p.N)) {
-                an = __ldg(nxt.sa);
-                bn = __ldg(nxt.sb);
-            }
+            first_scales();
         }
         for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
             cur = nxt;
@@ -347,7 +361,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < C::COLS_W / 2; ++i) acc[i] = f2(0.0f, 0.0f);
             if (!work) {  // only hands the accumulators on
-                for (int kb = 0; kb < KB; ++kb) {
+                for (int kb = 0; kb < KS; ++kb) {
                     if (!mbar_wait(&done_bar[stage], phase, abort_v, p.err)) {
                         ok = false;
                         break;
@@ -368,20 +382,31 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             ok = mbar_wait(&done_bar[stage], phase, abort_v, p.err);
             if (!ok) break;
             tc_fence_after();
-            tmem_ld32(tmem + buf * C::BN + toff, r[0]);
+            tmem_ld32(tmem + buf * C::ACC_COLS + toff, r[0]);
+            constexpr int CH = C::KSUB * C::CHUNKS_W;  // 32-column loads of a set
 #pragma unroll 1
-            for (int kb = 0; kb < KB; ++kb) {
-                const float s = __fmul_rn(an, bn);
-                if (kb + 1 < KB) {
-                    an = __ldg(++sa);
-                    bn = __ldg(++sb);
-                }
-                const F2 s2 = f2(s, s);
+            for (int kb = 0; kb < KS; ++kb) {
+                F2 s2[C::KSUB];
 #pragma unroll
-                for (int ch = 0; ch < C::CHUNKS_W; ++ch) {
+                for (int q = 0; q < C::KSUB; ++q) {
+                    const float s = __fmul_rn(an[q], bn[q]);
+                    s2[q] = f2(s, s);
+                    const int k = (kb + 1) * C::KSUB + q;
+                    if (k < KB) {
+                        an[q] = __ldg(sa + k);
+                        bn[q] = __ldg(sb + k);
+                    } else if (C::KSUB > 1) {
+                        an[q] = bn[q] = 0.0f;  // an absent block of the last set
+                    }
+                }
+#pragma unroll
+                for (int ch = 0; ch < CH; ++ch) {
+                    const int q = ch / C::CHUNKS_W, cc = ch % C::CHUNKS_W;
                     tmem_ld_wait32(r[ch & 1]);
-                    if (ch < C::CHUNKS_W - 1) {
-                        tmem_ld32(tmem + buf * C::BN + toff + (ch + 1) * 32, r[(ch + 1) & 1]);
+                    if (ch < CH - 1) {
+                        tmem_ld32(tmem + buf * C::ACC_COLS + toff +
+                                      (ch + 1) / C::CHUNKS_W * C::BN + (ch + 1) % C::CHUNKS_W * 32,
+                                  r[(ch + 1) & 1]);
                     } else {
                         tc_fence_before();
                         __syncwarp();
@@ -391,18 +416,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             stage = 0;
                             phase ^= 1u;
                         }
-                        if (kb + 1 < KB) {
+                        if (kb + 1 < KS) {
                             ok = mbar_wait(&done_bar[stage], phase, abort_v, p.err);
                             if (!ok) break;
                             tc_fence_after();
-                            tmem_ld32(tmem + buf * C::BN + toff, r[0]);
+                            tmem_ld32(tmem + buf * C::ACC_COLS + toff, r[0]);
                         }
                     }
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        acc[ch * 16 + i] = fma2(f2(__uint_as_float(r[ch & 1][2 * i]),
+                        acc[cc * 16 + i] = fma2(f2(__uint_as_float(r[ch & 1][2 * i]),
                                                    __uint_as_float(r[ch & 1][2 * i + 1])),
-                                                s2, acc[ch * 16 + i]);
+                                                s2[q], acc[cc * 16 + i]);
                 }
                 if (!ok) break;
             }
@@ -411,10 +436,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             // the next tile's place and first scales, while this one is stored
             if (t + gridDim.x < total) {
                 nxt = part_of(t + gridDim.x);
-                if (nxt.work(p.N)) {
-                    an = __ldg(nxt.sa);
-                    bn = __ldg(nxt.sb);
-                }
+                first_scales();
             }
             if (!work) continue;
             if constexpr (C::ASYNC) {
@@ -509,7 +531,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 template <class C>
 cudaError_t run_block_gemm(const GemmBlockArgs &a, cudaStream_t s) {
     const int64_t T = a.groups.total_rows;
-    CUtensorMap tA, tA32, tB, tC;
+    // the whole-block map of A is of the 128-row tiles, the output's of the
+    // asynchronous stores; a map takes the host about half a microsecond
+    CUtensorMap tA = {}, tA32, tB, tC = {};
     cuuint64_t da[2] = {(cuuint64_t)a.K, (cuuint64_t)T};
     cuuint64_t sa[1] = {(cuuint64_t)a.K};
     cuuint64_t db[3] = {(cuuint64_t)a.K, (cuuint64_t)a.N, (cuuint64_t)a.groups.num_experts};
@@ -519,7 +543,7 @@ cudaError_t run_block_gemm(const GemmBlockArgs &a, cudaStream_t s) {
     // 2560 74.0 / 78.2; 12000 rows, N 1880, 48 experts)
     const CUtensorMapL2promotion promotion = a.K % 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
                                                        : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
-    if (!make_map(&tA, a.a, 2, da, sa, C::BM, promotion) ||
+    if ((C::BM == 128 && !make_map(&tA, a.a, 2, da, sa, 128, promotion)) ||
         !make_map(&tA32, a.a, 2, da, sa, 32, promotion) ||
         !make_map(&tB, a.b, 3, db, sb, C::BN, promotion))
         return cudaErrorInvalidValue;
@@ -527,7 +551,8 @@ cudaError_t run_block_gemm(const GemmBlockArgs &a, cudaStream_t s) {
     cuuint64_t dc[2] = {(cuuint64_t)a.N, (cuuint64_t)T};
     cuuint64_t sc[1] = {(cuuint64_t)a.N * 2};
     cuuint32_t bc[2] = {64, 32}, ec[2] = {1, 1};
-    if (encode_fn()(&tC, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.c, dc, sc, bc, ec,
+    if (C::ASYNC &&
+        encode_fn()(&tC, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.c, dc, sc, bc, ec,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_NONE,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -566,15 +591,16 @@ cudaError_t run_block_gemm(const GemmBlockArgs &a, cudaStream_t s) {
 }  // namespace
 
 // Two tile shapes.  128 x 256: the least operand traffic per product, for
-// everything that has rows.  64 x 128: twice the CTAs per group and a ring of
-// eight stages, for few rows, where the time is the stream of the weights and
-// the SMs that take part in it.  The choice compares, per K block and in ns,
-// the full waves of tiles, each at the rate of memory or of one CTA's loop
-// (430 and 330 ns measured on streams that leave SMs idle), and the last
-// partial one at the latter.  Measured with K 4096, N 1536 (small against large
-// tiles): 8 rows over 8 experts 14.6 / 18.8 us, 16 over 16 27.2 / 22.9, 32 over
-// 29 38.5 / 43.5, 4096 over 128 135 / 142, 8192 over 128 160 / 146, 512 over 8
-// 15.6 / 19.8.
+// everything that has rows.  64 x 128: twice the CTAs per group, for few rows,
+// where the time is the stream of the weights and the SMs that take part in it;
+// its stages hold two K blocks, so that the waits of the issuing and summing
+// warps, which bound so small a block, are paid once for both (2 to 15 % of the
+// times below).  The choice compares, per K block and in ns, the full waves of
+// tiles, each at the rate of memory or of one CTA's loop (430 and 330 ns measured
+// on streams that leave SMs idle, one block per stage), and the last partial one
+// at the latter.  Measured with K 4096, N 1536 (small against large tiles): 8
+// rows over 8 experts 13.7 / 18.8 us, 16 over 16 27.2 / 22.9, 32 over 29 35.5 /
+// 43.5, 4096 over 128 131 / 142, 8192 over 128 160 / 146, 512 over 8 14.0 / 19.8.
 cudaError_t launch_gemm_fp8_block(const GemmBlockArgs &a, cudaStream_t s) {
     const int64_t T = a.groups.total_rows, g = std::min<int64_t>(a.groups.num_groups, T);
     const int64_t sms = sm_count();
@@ -585,13 +611,13 @@ cudaError_t launch_gemm_fp8_block(const GemmBlockArgs &a, cudaStream_t s) {
         return tiles / sms * std::max(loop_ns, stream_ns) + (tiles % sms ? loop_ns : 0);
     };
     if (cost(64, 128, 330) < cost(128, 256, 430))
-        return run_block_gemm<BlockCfg<64, 128, 8, 8, false>>(a, s);
+        return run_block_gemm<BlockCfg<64, 128, 4, 8, false, 2>>(a, s);
     // short reductions: a tile's results leave while the next one is summed, for
     // one stage of the ring (K 224: 90 us against 116 on 48816 x 3832; K 1536
     // 772 / 808 on 131072 x 4096; K 2480 97.2 / 97.8; K 4096 342 / 334; K 7168
     // 1554 / 1440, single launches)
-    if (a.K <= 20 * 128) return run_block_gemm<BlockCfg<128, 256, 3, 8, true>>(a, s);
-    return run_block_gemm<BlockCfg<128, 256, 4, 8, false>>(a, s);
+    if (a.K <= 20 * 128) return run_block_gemm<BlockCfg<128, 256, 3, 8, true, 1>>(a, s);
+    return run_block_gemm<BlockCfg<128, 256, 4, 8, false, 1>>(a, s);
 }
 
 }  // namespace moeq
