@@ -393,16 +393,19 @@ def grouped_matmul_swiglu_mx(fmt, c_q, c_sf, a, a_sf, b, b_sf, expert_scales, a_
 def _rows_of(t, name, shape=None, dtype=None):
     """Pointer of a 2-D CUDA tensor with unit column stride (rows may be
     strided) of one of DTYPES, or of dtype, and of the given shape."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2
+            and (t.dtype in DTYPES if dtype is None else t.dtype is dtype)
+            and (shape is None or t.shape == shape) and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
     if t.dtype not in DTYPES if dtype is None else t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype or tuple(DTYPES)}")
     if t.dim() != 2 or (shape is not None and t.shape != shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape or '2-D'}")
-    if not t.is_contiguous():
-        n, m = t.shape
-        if m > 1 and t.stride(1) != 1 or n > 1 and t.stride(0) < m:
-            raise ValueError(f"{name}: must have unit column stride")
+    n, m = t.shape
+    if m > 1 and t.stride(1) != 1 or n > 1 and t.stride(0) < m:
+        raise ValueError(f"{name}: must have unit column stride")
     return t.data_ptr()
 
 
@@ -414,6 +417,12 @@ def _row_stride(t):
 def _shaped(t, shape, dtype, name, optional=False):
     """Pointer of a contiguous CUDA tensor of this shape and dtype; None is
     None where that is allowed."""
+    # the checks in one expression: a call has many arguments and a small one
+    # takes little more than their checks
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.shape == shape
+            and (t.dtype is dtype or (type(dtype) is tuple and t.dtype in dtype))
+            and t.is_contiguous()):
+        return t.data_ptr()
     if t is None and optional:
         return None
     if not isinstance(t, torch.Tensor):
