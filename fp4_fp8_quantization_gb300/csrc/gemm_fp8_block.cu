@@ -27,9 +27,13 @@
 // 1.5 GHz (2.37); the rowwise-scaled GEMM on the same operands 1.33 and 1.54.
 // With few rows the stream of the weights: 512 rows over 256 experts, K 7168, N
 // 4096, 0.93 ms, 103 % of the copy rate.
-// What did not help: 64-column tensor-memory loads, polling waits (both within
-// 1 %), the scales brought to shared memory by the two idle warps (10 % slower:
-// the wait for them joins each block's chain), CTAs of 128 x 128 (30 % slower).
+// What did not help: 64-column tensor-memory loads, polling waits, a second
+// issuing warp (all within 1 %), the scales brought to shared memory by the two
+// idle warps (10 % slower: the wait for them joins each block's chain), CTAs of
+// 128 x 128 (30 %), an accumulator handed over by halves of 128 columns (10 %: A
+// is read twice), 16 sum warps of 64 columns (11 %), MMAs over CTA pairs (7 %:
+// each block waits for the sums of both), prefetches into L2 (10 %, 40 % for
+// rows that start inside lines: the load path has no requests to spare).
 #include <algorithm>
 
 #include "common.cuh"
