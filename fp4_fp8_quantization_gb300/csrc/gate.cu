@@ -18,7 +18,9 @@
 // shortened for it, and a token whose choice the shortened ones do not decide
 // is chosen again from the whole ones.  Sums are fp32 in a fixed order.
 // Bound by the integer and selection instructions of the rounds (65537 tokens x
-// 128, top-8, fp32: forward 23 us, gradient 11 us, 5.6 and 10.5 of memory).
+// 128, top-8, fp32: forward 20.5 us, gradient 10.7 us, 5.6 and 10.5 of memory).  The
+// lane's sorted images in shared memory instead of registers, so that a round
+// moves one of them: the same there, 0.2 us slower for few tokens.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -210,6 +212,24 @@ struct Candidates {
     static constexpr uint32_t kNone =
         DT == MOEQ_FP32 ? kNegInfKey : (kNegInfKey16<DT> << 16 | 0xFFFFu);
     uint32_t key[NV];
+    // Odd-even merge sort, largest first (NV is a power of two): from the step
+    // that compares keys h apart while runs of n are merged.
+    template <int n, int h>
+    __device__ __forceinline__ void merge_step() {
+        if constexpr (n < NV) {
+#pragma unroll
+            for (int i = h % n; i + h < NV; ++i)
+                if ((i - h % n) / h % 2 == 0 && i / (2 * n) == (i + h) / (2 * n)) {
+                    const uint32_t u = key[i], v = key[i + h];
+                    key[i] = max(u, v);
+                    key[i + h] = min(u, v);
+                }
+            if constexpr (h > 1)
+                merge_step<n, h / 2>();
+            else
+                merge_step<2 * n, 2 * n>();
+        }
+    }
     __device__ __forceinline__ void init(const float (&x)[NV], int j0) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -220,29 +240,7 @@ struct Candidates {
                 k = order_key16<DT>(x[i]) << 16;
             key[i] = k | (kIdx - (uint32_t)(j0 + i));
         }
-        // odd-even merge sort, largest first (NV is a power of two)
-#pragma unroll
-        for (int n = 1; n < NV; n *= 2)
-#pragma unroll
-            for (int h = n; h >= 1; h /= 2)
-#pragma unroll
-                for (int a = h % n; a + h < NV; a += 2 * h)
-#pragma unroll
-                    for (int b = 0; b < h; ++b)
-                        if (a + b + h < NV && (a + b) / (2 * n) == (a + b + h) / (2 * n)) {
-                            const uint32_t u = key[a + b], v = key[a + b + h];
-                            key[a + b] = max(u, v);
-                            key[a + b + h] = min(u, v);
-                        }
-    }
-    // The token's best image, removed from its lane.
-    __device__ __forceinline__ uint32_t next() {
-        const uint32_t mx = lanes_max<L>(key[0]);
-        const bool own = key[0] == mx;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            key[i] = own ? (i + 1 < NV ? key[(i + 1) % NV] : 0u) : key[i];
-        return mx;
+        merge_step<1, 1>();
     }
 };
 
@@ -293,19 +291,29 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateParams p) {
     const uint8_t *row = p.logits + t * p.stride;
     float x[NV];
     load_row<DT>(row, p.E, sub * NV, rows_aligned<DT, NV>(p.stride), x);
+    // a token's best images in the order of the rounds
+    __shared__ uint32_t chosen[kGateWarps][32 / L][L + 1];
+    uint32_t *out = chosen[threadIdx.x >> 5][lane / L];
     Cand c;
     c.init(x, sub * NV);
-    // lane r of a token: choice r.  fp32: one round more than choices; where two
-    // rounds in a row find the same image but for the index, the order is not
-    // decided
+    // fp32: one round more than choices; where two rounds in a row find the same
+    // image but for the index, the order is not decided
     const int rounds = p.top_k + (DT == MOEQ_FP32 ? 1 : 0);
-    bool tie = false;
-    uint32_t my_key = 0u, last = 0xFFFFFFFFu;
     for (int r = 0; r < rounds; ++r) {
-        const uint32_t mx = c.next();
-        if constexpr (DT == MOEQ_FP32) tie |= mx > Cand::kNone && ((mx ^ last) >> Cand::IB) == 0u;
-        last = mx;
-        if (sub == r) my_key = mx;
+        const uint32_t mx = lanes_max<L>(c.key[0]);
+        const bool own = c.key[0] == mx;  // one lane's while any image is left
+        if (own) out[r] = mx;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            c.key[i] = own ? (i + 1 < NV ? c.key[(i + 1) % NV] : 0u) : c.key[i];
+    }
+    __syncwarp();
+    uint32_t my_key = 0u;  // lane r of a token: choice r
+    bool tie = false;
+    if (sub < p.top_k) {
+        my_key = out[sub];
+        if constexpr (DT == MOEQ_FP32)
+            tie = my_key > Cand::kNone && ((my_key ^ out[sub + 1]) >> Cand::IB) == 0u;
     }
     int id = -1;
     float v = 0.0f, w = 0.0f;
@@ -444,14 +452,16 @@ cudaError_t run_gate_lanes(const GateParams &p, cudaStream_t s) {
 template <int DT>
 cudaError_t run_gate(const GateParams &p, cudaStream_t s) {
     // many tokens: as few lanes per token as leave each at most 8 logits, so that
-    // the rounds of a warp's tokens are shared.  65536 tokens x 32, top-8: 8.3 us
-    // with 8 lanes, 20.4 with 32; x 64 11.7 / 22.7; x 128 23.3 with 16, 29.7 with
-    // 32, 32.7 with 8; but 1024 x 128 3.1 / 2.3
-    if (p.num_tokens >= 4096) {
-        if (p.E <= 32 && p.top_k <= 8) return run_gate_lanes<DT, 4, 8>(p, s);
-        if (p.E <= 64 && p.top_k <= 8) return run_gate_lanes<DT, 8, 8>(p, s);
-        if (p.E <= 128 && p.top_k <= 16) return run_gate_lanes<DT, 8, 16>(p, s);
+    // the rounds of a warp's tokens are shared.  fp32, top-8, these lanes against
+    // 32: 65536 tokens x 32 experts 6.7 / 17.6 us, x 64 9.3 / 18.2, x 128 19.4 /
+    // 21.1; 16384 x 128 6.7 / 6.5 (bf16 6.0 / 6.1), 8192 x 64 3.5 / 3.8, x 128 5.0 /
+    // 4.4; 4096 x 64 3.1 / 2.7
+    if (p.num_tokens >= 8192 && p.top_k <= 8) {
+        if (p.E <= 32) return run_gate_lanes<DT, 4, 8>(p, s);
+        if (p.E <= 64) return run_gate_lanes<DT, 8, 8>(p, s);
     }
+    if (p.num_tokens >= 16384 && p.E <= 128 && p.top_k <= 16)
+        return run_gate_lanes<DT, 8, 16>(p, s);
     const int nv = (p.E + 31) / 32;
     return nv <= 1    ? run_gate_lanes<DT, 1, 32>(p, s)
            : nv <= 2  ? run_gate_lanes<DT, 2, 32>(p, s)

@@ -123,6 +123,22 @@ def test_gate_orders_logits_that_differ_in_their_last_bits(E, k):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T", [5, 17000])
+@pytest.mark.parametrize("E", [1, 8, 16, 32])
+def test_gate_takes_every_expert(E, T, dtype):
+    """top_k = num_experts: as many rounds as there are logits, with NaN and -inf
+    among them, in the last place too; equal logits in order."""
+    x = np.tile(np.random.default_rng(E).integers(-2, 3, size=(5, E)).astype(np.float32),
+                (T // 5, 1))
+    x[1::5, -1] = np.nan
+    x[2::5, 0] = -np.inf
+    x[3::5, -1] = -np.inf
+    ids, _ = _gate(torch.from_numpy(x).to(dtype).to(DEV), E, True, 1.0)
+    want, _ = X.gate_topk(x[:5].astype(np.float64), E, True, 1.0)
+    assert np.array_equal(ids.cpu().numpy(), np.tile(want, (T // 5, 1)))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("normalize", [False, True])
 @pytest.mark.parametrize("E,k", [(3, 2), (23, 6), (32, 1), (39, 8), (72, 4), (129, 8)])
 def test_gate_many_tokens(E, k, normalize, dtype):
