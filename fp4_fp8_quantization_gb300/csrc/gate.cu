@@ -18,7 +18,7 @@
 // shortened for it, and a token whose choice the shortened ones do not decide
 // is chosen again from the whole ones.  Sums are fp32 in a fixed order.
 // Bound by the integer and selection instructions of the rounds (65537 tokens x
-// 128, top-8, fp32: forward 20.5 us, gradient 10.7 us, 5.6 and 10.5 of memory).  The
+// 128, top-8, fp32: forward 18.7 us, gradient 10.6 us, 5.6 and 10.5 of memory).  The
 // lane's sorted images in shared memory instead of registers, so that a round
 // moves one of them: the same there, 0.2 us slower for few tokens.
 #include <cuda_fp16.h>
@@ -66,34 +66,15 @@ __device__ __forceinline__ void store_logit(uint8_t *row, int j, float v) {
         reinterpret_cast<uint16_t *>(row)[j] = (uint16_t)bits_of<DT>(v);
 }
 
-// An integer that orders as the float does (-0 = +0); 0 for NaN, which ranks
-// below -inf (kNegInfKey).
+// An integer that orders as the float, no NaN, does (-0 = +0).
 __device__ __forceinline__ uint32_t order_key(float x) {
     const uint32_t u = __float_as_uint(__fadd_rn(x, 0.0f));
-    if (x != x) return 0u;
-    return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+    return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 
 __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
-
-// The same of a 16-bit logit, in 16 bits.
-template <int DT>
-__device__ __forceinline__ uint32_t order_key16(float x) {
-    const uint32_t b = bits_of<DT>(__fadd_rn(x, 0.0f));  // exact: x came from 16 bits
-    if (x != x) return 0u;
-    return b ^ ((b >> 15) ? 0xFFFFu : 0x8000u);
-}
-
-template <int DT>
-__device__ __forceinline__ float key16_value(uint32_t k) {
-    return logit_of<DT>(k ^ ((k >> 15) ? 0x8000u : 0xFFFFu));
-}
-
-// order_key16(-inf)
-template <int DT>
-constexpr uint32_t kNegInfKey16 = DT == MOEQ_BF16 ? 0x007Fu : 0x03FFu;
 
 // exp(x - m) for x <= m: within 2 + 1.2 |x - m| ulp, NaN for a NaN or for
 // infinity minus infinity.
@@ -201,16 +182,16 @@ __device__ __forceinline__ void store_row(uint8_t *row, int E, int j0, bool vec,
 }
 
 // A lane's candidates as sorted images, each with its index in the low IB bits
-// (largest first: the lowest index of equal ones).  16-bit logits are whole in
-// what is left; an fp32 image loses its last IB bits.
+// (largest first: the lowest index of equal ones).  A 16-bit logit is whole in
+// what is left (fp16 needs 19 bits of an fp32 image), an fp32 one is shortened.
 template <int DT, int NV, int L>
 struct Candidates {
     static constexpr int log2(int v) { return v <= 1 ? 0 : 1 + log2(v / 2); }
-    static constexpr int IB = DT == MOEQ_FP32 ? log2(L * NV) : 16;
+    static constexpr int IB = log2(L * NV);
+    static_assert(IB <= 10, "images of 16-bit logits are whole");
     static constexpr uint32_t kIdx = (1u << IB) - 1u;
-    // the largest image of -inf
-    static constexpr uint32_t kNone =
-        DT == MOEQ_FP32 ? kNegInfKey : (kNegInfKey16<DT> << 16 | 0xFFFFu);
+    // the largest image of -inf; a NaN's is below kIdx
+    static constexpr uint32_t kNone = kNegInfKey;
     uint32_t key[NV];
     // Odd-even merge sort, largest first (NV is a power of two): from the step
     // that compares keys h apart while runs of n are merged.
@@ -230,15 +211,15 @@ struct Candidates {
                 merge_step<2 * n, 2 * n>();
         }
     }
-    __device__ __forceinline__ void init(const float (&x)[NV], int j0) {
+    // nan: whether a logit of the warp is one
+    __device__ __forceinline__ void init(const float (&x)[NV], int j0, bool nan) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            uint32_t k;
-            if constexpr (DT == MOEQ_FP32)
-                k = order_key(x[i]) & ~kIdx;
-            else
-                k = order_key16<DT>(x[i]) << 16;
-            key[i] = k | (kIdx - (uint32_t)(j0 + i));
+        for (int i = 0; i < NV; ++i)
+            key[i] = (order_key(x[i]) & ~kIdx) | (kIdx - (uint32_t)(j0 + i));
+        if (nan) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (x[i] != x[i]) key[i] &= kIdx;
         }
         merge_step<1, 1>();
     }
@@ -253,7 +234,7 @@ __device__ __forceinline__ void choose_exactly(const float (&x)[NV], int top_k, 
     const int sub = lane % L;
     uint32_t key[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) key[i] = order_key(x[i]);
+    for (int i = 0; i < NV; ++i) key[i] = x[i] == x[i] ? order_key(x[i]) : 0u;
     for (int r = 0; r < top_k; ++r) {
         uint32_t best = 0u;
         int at = 0;
@@ -294,8 +275,11 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateParams p) {
     // a token's best images in the order of the rounds
     __shared__ uint32_t chosen[kGateWarps][32 / L][L + 1];
     uint32_t *out = chosen[threadIdx.x >> 5][lane / L];
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) nan |= x[i] != x[i];
     Cand c;
-    c.init(x, sub * NV);
+    c.init(x, sub * NV, __any_sync(0xFFFFFFFFu, nan));
     // fp32: one round more than choices; where two rounds in a row find the same
     // image but for the index, the order is not decided
     const int rounds = p.top_k + (DT == MOEQ_FP32 ? 1 : 0);
@@ -322,7 +306,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateParams p) {
         if constexpr (DT == MOEQ_FP32)
             v = load_logit<DT>(row, id);
         else
-            v = key16_value<DT>(my_key >> 16);
+            v = __uint_as_float(__float_as_uint(key_value(my_key)) & ~Cand::kIdx);
     }
     if constexpr (DT == MOEQ_FP32)
         if (__any_sync(0xFFFFFFFFu, tie)) choose_exactly<NV, L>(x, p.top_k, lane, id, v);
@@ -331,10 +315,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateParams p) {
     const float e = id >= 0 ? exp_diff(v, m) : 0.0f;
     // a NaN logit, or m infinite, makes either denominator NaN
     float total = e;
-    bool nan = false;
     if (p.normalize) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) nan |= x[i] != x[i];
         if (nan) total = __int_as_float(0x7FFFFFFF);
     } else {
         total = 0.0f;
