@@ -20,9 +20,10 @@
 // Every wait is bounded and sets the device error word instead of hanging.
 //
 // What bounds it: with many rows, about 700 cycles of a K block (128 x 256 tile)
-// whose MMAs take 512.  The 48 KB of operands written to and read from shared
-// memory account for it (96 KB at 128 bytes a cycle would be 768), the sums need
-// 560 of them and overlap, and above that the power limit: 65536 x 7168 x 4096,
+// whose MMAs take 512.  Two things lie just above them: 48 KB of operands come
+// into the SM (70 bytes a cycle; more requests or reads of them slow it at once,
+// below), and the two accumulators' chain of MMAs, commit, 560 cycles of loads
+// and sums, and release.  Above that is the power limit: 65536 x 7168 x 4096,
 // 64 experts, 1.46 ms a single launch (2.64 PFLOP/s), 1.62 back to back at about
 // 1.5 GHz (2.37); the rowwise-scaled GEMM on the same operands 1.33 and 1.54.
 // With few rows the stream of the weights: 512 rows over 256 experts, K 7168, N
