@@ -594,6 +594,8 @@ def grouped_matmul_fp8_block(c, a, b, a_scales, b_scales, a_offsets, expert_ids,
     [a_offsets[g], a_offsets[g + 1]) of expert expert_ids[g]."""
     G = expert_ids.numel() if num_active_experts is None else num_active_experts
     E, N, K = b.shape
+    if expert_ids.numel() < G or a_offsets.numel() < G + 1:
+        raise ValueError(f"a_offsets, expert_ids: too short for {G} groups")
     T = a.shape[0]
     _call("moeq_grouped_matmul_fp8_block", _shaped(c, (T, N), torch.bfloat16, "c"),
           _shaped(a, (T, K), _U8, "a"), _ptr(b, _U8, "b"),

@@ -590,3 +590,18 @@ def test_layer_in_a_cuda_graph_is_the_same():
         ref += w[:, j, None].double() * torch.einsum("ti,thi->th", h, dn[e])
     assert float((out.double() - ref).norm() / ref.norm()) < 2 * 2.0 ** -4
     assert moeq.get_device_error() == 0
+
+
+def test_block_gemm_refuses_short_group_tables():
+    a = torch.zeros(4, 128, dtype=torch.uint8, device=DEV)
+    b = torch.zeros(2, 8, 128, dtype=torch.uint8, device=DEV)
+    c = torch.zeros(4, 8, dtype=torch.bfloat16, device=DEV)
+    sa, sb = torch.ones(4, 1, device=DEV), torch.ones(2, 1, 1, device=DEV)
+    offsets = torch.zeros(3, dtype=torch.int32, device=DEV)
+    ids = torch.zeros(2, dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError, match="too short"):
+        moeq.grouped_matmul_fp8_block(c, a, b, sa, sb, offsets[:2], ids)
+    with pytest.raises(ValueError, match="too short"):
+        moeq.grouped_matmul_fp8_block(c, a, b, sa, sb, offsets, ids, num_active_experts=3)
+    moeq.grouped_matmul_fp8_block(c, a, b, sa, sb, offsets, ids)
+    assert moeq.get_device_error() == 0
