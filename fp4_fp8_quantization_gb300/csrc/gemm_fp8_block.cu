@@ -288,9 +288,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int kb = 0; kb < KS; ++kb) {
                 // the operands are mostly there first: their wait is paid while
                 // the accumulator is still being read
-                ok = mbar_wait(&full_bar[stage], phase, abort_v, p.err) &&
-                     mbar_wait(&tempty_bar[buf], bphase ^ 1u, abort_v, p.err);
-                ok = __all_sync(0xFFFFFFFFu, ok);
+                ok = __all_sync(0xFFFFFFFFu,
+                                mbar_wait(&full_bar[stage], phase, abort_v, p.err) &&
+                                    mbar_wait(&tempty_bar[buf], bphase ^ 1u, abort_v, p.err));
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
@@ -349,6 +349,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             w.sb = p.b_scales + ((int64_t)e * NBLK + min(w.ncol / 128, NBLK - 1)) * KB;
             return w;
         };
+        // each lane polls by itself: where the barrier completes while another
+        // warp gives up, some would go on and some leave, and what follows is the
+        // whole warp's
+        auto sums_wait = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_v, p.err));
+        };
         int buf = 0, stage = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -374,11 +380,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int i = 0; i < C::COLS_W / 2; ++i) acc[i] = f2(0.0f, 0.0f);
             if (!work) {  // only hands the accumulators on
                 for (int kb = 0; kb < KS; ++kb) {
-                    if (!mbar_wait(&done_bar[stage], phase, abort_v, p.err)) {
-                        ok = false;
-                        break;
-                    }
-                    __syncwarp();
+                    ok = sums_wait(&done_bar[stage], phase);
+                    if (!ok) break;
                     if (lane == 0) mbar_arrive(&tempty_bar[buf]);
                     if (++buf == C::NBUF) buf = 0;
                     if (++stage == C::STAGES) {
@@ -391,7 +394,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             // of this one) is in flight while the last 32 are added
             uint32_t r[2][32];
             const float *sa = cur.sa, *sb = cur.sb;
-            ok = mbar_wait(&done_bar[stage], phase, abort_v, p.err);
+            ok = sums_wait(&done_bar[stage], phase);
             if (!ok) break;
             tc_fence_after();
             tmem_ld32(tmem + buf * C::ACC_COLS + toff, r[0]);
@@ -429,8 +432,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             phase ^= 1u;
                         }
                         if (kb + 1 < KS) {
-                            ok = mbar_wait(&done_bar[stage], phase, abort_v, p.err);
-                            if (!ok) break;
+                            // a warp that gives up leaves after the sums below,
+                            // so that they do not wait for the vote
+                            ok = sums_wait(&done_bar[stage], phase);
                             tc_fence_after();
                             tmem_ld32(tmem + buf * C::ACC_COLS + toff, r[0]);
                         }
@@ -441,7 +445,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                                    __uint_as_float(r[ch & 1][2 * i + 1])),
                                                 s2[q], acc[cc * 16 + i]);
                 }
-                if (!ok) break;
+                if (!ok) {
+                    tmem_ld_wait32(r[0]);
+                    break;
+                }
             }
             }
             if (!ok) break;
