@@ -845,7 +845,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const float rsr = (EPI == kSwiglu && p.row_scales && valid)
                                   ? bf16_bits_to_f32(__ldg(p.row_scales + row))
                                   : 1.0f;
-            if (!mbar_wait<PAIRED>(&tfull_bar[buf], aph, abort_v, p.err)) break;
+            // voted: each lane polls by itself, what follows is the whole warp's
+            if (!__all_sync(0xFFFFFFFFu,
+                            mbar_wait<PAIRED>(&tfull_bar[buf], aph, abort_v, p.err)))
+                break;
             tc_fence_after();
             const uint32_t tbase = tmem + lane_off + buf * C::ACC_COLS + cgrp * C::COLS_W;
             uint32_t sfbytes = 0;

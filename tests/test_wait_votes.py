@@ -77,7 +77,7 @@ def test_the_scan_tells_the_forms_apart():
     assert _waits(bare) == [(1, False)]
 
 
-@pytest.mark.parametrize("name,least", [("gemm_fp8_block.cu", 4)])
+@pytest.mark.parametrize("name,least", [("gemm_fp8_block.cu", 4), ("gemm.cu", 6)])
 def test_every_wait_is_one_lanes_or_voted(name, least):
     with open(os.path.join(CSRC, name)) as f:
         waits = _waits(f.read())
