@@ -607,6 +607,10 @@ cudaError_t run_block_gemm(const GemmBlockArgs &a, cudaStream_t s) {
     return launch_pdl(kern, grid, C::THREADS, C::SMEM_BYTES, s, tA, tA32, tB, tC, p);
 }
 
+// The forms below (the last two 128 x 256, results stored by tensor stores or
+// directly).
+enum Form { kSmallTile = 0, kLargeTileByTensor = 1, kLargeTile = 2 };
+
 }  // namespace
 
 // Two tile shapes.  128 x 256: the least operand traffic per product, for
@@ -629,13 +633,18 @@ cudaError_t launch_gemm_fp8_block(const GemmBlockArgs &a, cudaStream_t s) {
         const int64_t stream_ns = sms * bn * 128 / 6800;  // a wave's weights at 6.8 TB/s
         return tiles / sms * std::max(loop_ns, stream_ns) + (tiles % sms ? loop_ns : 0);
     };
-    if (cost(64, 128, 330) < cost(128, 256, 430))
-        return run_block_gemm<BlockCfg<64, 128, 4, 8, false, 2>>(a, s);
+    int tile = kSmallTile;
     // short reductions: a tile's results leave while the next one is summed, for
     // one stage of the ring (K 224: 90 us against 116 on 48816 x 3832; K 1536
     // 772 / 808 on 131072 x 4096; K 2480 97.2 / 97.8; K 4096 342 / 334; K 7168
     // 1554 / 1440, single launches)
-    if (a.K <= 20 * 128) return run_block_gemm<BlockCfg<128, 256, 3, 8, true, 1>>(a, s);
+    if (cost(64, 128, 330) >= cost(128, 256, 430))
+        tile = a.K <= 20 * 128 ? kLargeTileByTensor : kLargeTile;
+#ifdef MOEQ_FP8_BLOCK_TILE
+    tile = MOEQ_FP8_BLOCK_TILE;  // test builds: one form for every size
+#endif
+    if (tile == kSmallTile) return run_block_gemm<BlockCfg<64, 128, 4, 8, false, 2>>(a, s);
+    if (tile == kLargeTileByTensor) return run_block_gemm<BlockCfg<128, 256, 3, 8, true, 1>>(a, s);
     return run_block_gemm<BlockCfg<128, 256, 4, 8, false, 1>>(a, s);
 }
 
