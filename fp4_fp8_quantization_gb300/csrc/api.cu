@@ -593,6 +593,8 @@ moeq_status moeq_gate_topk(moeq_dtype dtype, const void *logits, int64_t logit_s
     if (num_tokens == 0) return MOEQ_OK;
     if (!topk_ids || !weights || !aligned16(topk_ids) || !aligned16(weights))
         return MOEQ_ERR_INVALID_ARG;
+    uint32_t *err = device_error_ptr();
+    if (!err) return cuda_status(cudaErrorInvalidDevice);
     moeq::GateArgs a = {};
     a.dtype = dtype;
     a.logits = logits;
@@ -604,6 +606,7 @@ moeq_status moeq_gate_topk(moeq_dtype dtype, const void *logits, int64_t logit_s
     a.scale = scale;
     a.ids = topk_ids;
     a.weights = weights;
+    a.err = err;
     return cuda_status(moeq::launch_gate(a, stream));
 }
 
@@ -758,7 +761,10 @@ moeq_status moeq_quantize_fp8_block_weight(const void *w, int64_t num_experts, i
     if (num_experts == 0 || N == 0) return MOEQ_OK;
     if (!w || !out || !scales || !aligned16(w) || !aligned16(out) || !aligned16(scales))
         return MOEQ_ERR_INVALID_ARG;
-    return cuda_status(moeq::launch_fp8_block_weight(w, num_experts, N, K, out, scales, stream));
+    uint32_t *err = device_error_ptr();
+    if (!err) return cuda_status(cudaErrorInvalidDevice);
+    return cuda_status(
+        moeq::launch_fp8_block_weight(w, num_experts, N, K, out, scales, err, stream));
 }
 
 moeq_status moeq_grouped_matmul_fp8_block(void *c, const uint8_t *a, const uint8_t *b,

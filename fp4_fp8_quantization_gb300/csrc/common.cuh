@@ -9,6 +9,7 @@
 #include <stdint.h>
 
 #include "../../include/moeq.h"
+#include "bounds.h"
 
 namespace moeq {
 
@@ -18,9 +19,10 @@ __device__ __forceinline__ void set_error(uint32_t *err, uint32_t bit) {
     if (err) atomicOr(err, bit);
 }
 
-// Store guard.  Debug builds (MOEQ_DEBUG_BOUNDS) check every global store of
-// the kernels against its buffer's extent first: a store outside it is
-// skipped and sets MOEQ_DEVERR_BOUNDS.  Release builds compile the check out.
+// Store guard.  Debug builds (MOEQ_DEBUG_BOUNDS) check the kernels' global
+// stores (all but the weight-layout helpers') against their buffers' extents
+// first: a store outside is skipped and sets MOEQ_DEVERR_BOUNDS.  Release builds
+// compile the check out.
 __device__ __forceinline__ bool store_ok(bool in_bounds, uint32_t *err) {
 #ifdef MOEQ_DEBUG_BOUNDS
     if (!in_bounds) set_error(err, MOEQ_DEVERR_BOUNDS);
@@ -30,6 +32,14 @@ __device__ __forceinline__ bool store_ok(bool in_bounds, uint32_t *err) {
     (void)err;
     return true;
 #endif
+}
+
+// The same by address: a store of `bytes` bytes at `at` to the buffer of `size`
+// bytes at `buf`.  An index can only fail a bound that no code before has
+// compared it with; an address also shows a wrong stride, width or base.
+__device__ __forceinline__ bool store_fits(const void *at, int64_t bytes, const void *buf,
+                                           int64_t size, uint32_t *err) {
+    return store_ok(range_inside(at, bytes, buf, size), err);
 }
 
 // ------------------------------------------------- programmatic launches

@@ -153,10 +153,13 @@ __device__ __forceinline__ void store_item(const BlockParams &p, const float (&x
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int64_t k = k0 + i * 256;
-            if (k < p.K && store_ok(r < p.out_rows, p.err)) {
-                *reinterpret_cast<uint2 *>(p.out + r * p.K + k) = q[i];
-                if ((lane & 15) == 0) p.scales[r * KB + k / kBlk] = s[i];
-            }
+            if (k >= p.K) continue;
+            uint8_t *out = p.out + r * p.K + k;
+            float *scale = p.scales + r * KB + k / kBlk;
+            if (store_fits(out, 8, p.out, p.out_rows * p.K, p.err))
+                *reinterpret_cast<uint2 *>(out) = q[i];
+            if ((lane & 15) == 0 && store_fits(scale, 4, p.scales, p.out_rows * KB * 4, p.err))
+                *scale = s[i];
         }
     }
 }
@@ -227,7 +230,7 @@ cudaError_t run_swiglu_tab(const BlockParams &p, cudaStream_t s) {
 // threads hold a row's 128 columns, 16 rows at a time.
 __global__ void __launch_bounds__(256) fp8_block_weight_kernel(const uint16_t *w, int64_t N,
                                                                int64_t K, uint8_t *out,
-                                                               float *scales) {
+                                                               float *scales, uint32_t *err) {
     pdl_wait();
     pdl_trigger();
     __shared__ float part[8];
@@ -254,13 +257,18 @@ __global__ void __launch_bounds__(256) fp8_block_weight_kernel(const uint16_t *w
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = fmaxf(m, part[i]);
     const float s = block_scale(m), r = __fdiv_rn(1.0f, s);
-    if (threadIdx.x == 0) scales[(e * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x] = s;
+    float *scale = scales + (e * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+    if (threadIdx.x == 0 &&
+        store_fits(scale, 4, scales, (int64_t)gridDim.z * gridDim.y * gridDim.x * 4, err))
+        *scale = s;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int64_t n = n0 + i * 16 + (threadIdx.x >> 4);
         float x[8];
         unpack8(u[i], x);
-        if (n < N && k < K) *reinterpret_cast<uint2 *>(out + (e * N + n) * K + k) = codes8(x, r);
+        uint8_t *o = out + (e * N + n) * K + k;
+        if (n < N && k < K && store_fits(o, 8, out, (int64_t)gridDim.z * N * K, err))
+            *reinterpret_cast<uint2 *>(o) = codes8(x, r);
     }
 }
 
@@ -294,10 +302,10 @@ cudaError_t launch_fp8_block(const Fp8BlockArgs &a, cudaStream_t s) {
 }
 
 cudaError_t launch_fp8_block_weight(const void *w, int64_t E, int64_t N, int64_t K, uint8_t *out,
-                                    float *scales, cudaStream_t s) {
+                                    float *scales, uint32_t *err, cudaStream_t s) {
     const dim3 grid((unsigned)((K + kBlk - 1) / kBlk), (unsigned)((N + kBlk - 1) / kBlk), (unsigned)E);
     return launch_pdl(fp8_block_weight_kernel, grid, 256, 0, s, static_cast<const uint16_t *>(w), N,
-                      K, out, scales);
+                      K, out, scales, err);
 }
 
 }  // namespace moeq

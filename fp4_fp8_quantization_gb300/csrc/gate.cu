@@ -155,12 +155,19 @@ __device__ __forceinline__ void load_row(const uint8_t *row, int E, int j0, bool
     }
 }
 
+// The guard of a store to the logits' gradient.
+template <int DT>
+__device__ __forceinline__ bool grad_fits(const GateParams &p, const uint8_t *at, int bytes) {
+    return store_fits(at, bytes, p.d_logits, p.num_tokens * p.E * kSize<DT>, p.err);
+}
+
 template <int DT, int NV>
-__device__ __forceinline__ void store_row(uint8_t *row, int E, int j0, bool vec,
+__device__ __forceinline__ void store_row(const GateParams &p, uint8_t *row, int j0, bool vec,
                                           const float (&g)[NV]) {
     constexpr int kBytes = NV * kSize<DT>;
-    if (vec && j0 + NV <= E && kBytes >= 8) {
+    if (vec && j0 + NV <= p.E && kBytes >= 8) {
         uint8_t *a = row + (int64_t)j0 * kSize<DT>;
+        if (!grad_fits<DT>(p, a, kBytes)) return;
         uint32_t w[kBytes < 8 ? 2 : kBytes / 4];
 #pragma unroll
         for (int i = 0; i < (kBytes < 8 ? 0 : kBytes / 4); ++i)
@@ -177,7 +184,8 @@ __device__ __forceinline__ void store_row(uint8_t *row, int E, int j0, bool vec,
     } else {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (j0 + i < E) store_logit<DT>(row, j0 + i, g[i]);
+            if (j0 + i < p.E && grad_fits<DT>(p, row + (int64_t)(j0 + i) * kSize<DT>, kSize<DT>))
+                store_logit<DT>(row, j0 + i, g[i]);
     }
 }
 
@@ -324,9 +332,12 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_kernel(GateParams p) {
     }
     total = lanes_sum<L>(total);
     if (some) w = __fmul_rn(__fdiv_rn(e, total), p.scale);
-    if (active && sub < p.top_k && store_ok(t < p.num_tokens, p.err)) {
-        p.ids[t * p.top_k + sub] = id;
-        p.weights[t * p.top_k + sub] = w;
+    if (active && sub < p.top_k) {
+        int32_t *ids = p.ids + t * p.top_k + sub;
+        float *weights = p.weights + t * p.top_k + sub;
+        const int64_t size = p.num_tokens * p.top_k * 4;
+        if (store_fits(ids, 4, p.ids, size, p.err)) *ids = id;
+        if (store_fits(weights, 4, p.weights, size, p.err)) *weights = w;
     }
 }
 
@@ -390,17 +401,18 @@ __global__ void __launch_bounds__(kGateWarps * 32) gate_grad_kernel(GateParams p
     const float part = __fmul_rn(-mean, inv);
     constexpr int64_t kS = kSize<DT>;
     uint8_t *out = p.d_logits + t * p.E * kS;
-    if (active && store_ok(t < p.num_tokens, p.err)) {
+    if (active) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float g[W];
 #pragma unroll
             for (int k = 0; k < W; ++k) g[k] = p.normalize ? 0.0f : __fmul_rn(part, x[i][k]);
-            store_row<DT>(out, p.E, (i * LANES + sub) * W, vec & 2, g);
+            store_row<DT>(p, out, (i * LANES + sub) * W, vec & 2, g);
         }
     }
     __syncwarp();  // orders the stores above before those below
-    if (active && id >= 0) store_logit<DT>(out, id, __fmul_rn(q, __fadd_rn(d, -mean)));
+    if (active && id >= 0 && grad_fits<DT>(p, out + id * kS, kSize<DT>))
+        store_logit<DT>(out, id, __fmul_rn(q, __fadd_rn(d, -mean)));
 }
 
 template <int DT>

@@ -476,8 +476,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
+                        // the box ends at N by its tensor map
                         for (int ch = 0; ch < C::COLS_W / 64; ++ch)
-                            if (cur.ncol + ch * 64 < p.N)
+                            if (cur.ncol + ch * 64 < p.N &&
+                                store_ok(cur.row >= 0 && cur.row + 32 <= p.total_rows, p.err))
                                 tma_store_2d(&tmC, sbuf + ch * 4096, cur.ncol + ch * 64, cur.row);
                         bulk_commit();
                     }
@@ -489,9 +491,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         for (int rr = lane >> 3; rr < cur.nvalid; rr += 4) {
                             const uint4 v =
                                 ld_shared_v4(sbuf + ch * 4096 + rr * 128 + ((k ^ (rr & 7)) << 4));
-                            if (n < p.N && store_ok(cur.row + rr < p.total_rows, p.err))
-                                st_global_v4(p.c + (int64_t)(cur.row + rr) * p.N + n, v.x, v.y, v.z,
-                                             v.w);
+                            uint16_t *out = p.c + (int64_t)(cur.row + rr) * p.N + n;
+                            if (n < p.N && store_fits(out, 16, p.c, p.total_rows * p.N * 2, p.err))
+                                st_global_v4(out, v.x, v.y, v.z, v.w);
                         }
                     }
                 }
@@ -519,8 +521,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 for (int i = 0; i < 4; ++i) {
                     const int rr = lrow + 8 * i;
                     const uint4 v = ld_shared_v4(sbuf + rr * 64 + ((k ^ ((rr >> 1) & 3)) << 4));
-                    if (rr < cur.nvalid && in_n && store_ok(cur.row + rr < p.total_rows, p.err))
-                        st_global_v4(out + (int64_t)(8 * i) * p.N + ch * 32, v.x, v.y, v.z, v.w);
+                    uint16_t *o = out + (int64_t)(8 * i) * p.N + ch * 32;
+                    if (rr < cur.nvalid && in_n &&
+                        store_fits(o, 16, p.c, p.total_rows * p.N * 2, p.err))
+                        st_global_v4(o, v.x, v.y, v.z, v.w);
                 }
             }
         }

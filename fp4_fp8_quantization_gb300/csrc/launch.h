@@ -184,7 +184,7 @@ struct Fp8BlockArgs {
 };
 cudaError_t launch_fp8_block(const Fp8BlockArgs &a, cudaStream_t s);
 cudaError_t launch_fp8_block_weight(const void *w, int64_t E, int64_t N, int64_t K, uint8_t *out,
-                                    float *scales, cudaStream_t s);
+                                    float *scales, uint32_t *err, cudaStream_t s);
 
 // Maximum number of groups the GEMM scheduler accepts.
 constexpr int kMaxGroups = 1024;

@@ -136,6 +136,10 @@ __device__ __forceinline__ Place my_place(const RowsParams &p) {
             (int64_t)(threadIdx.x & 31) * 16, 512};
 }
 
+__device__ __forceinline__ void store_dot(const RowsParams &p, int64_t choice, float v) {
+    if (store_fits(p.dw + choice, 4, p.dw, p.num_tokens * p.top_k * 4, p.err)) p.dw[choice] = v;
+}
+
 // The KC dot products of a token's threads, summed and stored in d_w.  Every
 // thread of the token calls it; the order of the sum is fixed by their number.
 template <int FORM, int KC>
@@ -148,7 +152,7 @@ __device__ __forceinline__ void store_dots(const RowsParams &p, int64_t t, float
     if constexpr (FORM == kWarp) {
 #pragma unroll
         for (int j = 0; j < KC; ++j)
-            if (lane == j && j < p.top_k) p.dw[t * p.top_k + j] = s[j];
+            if (lane == j && j < p.top_k) store_dot(p, t * p.top_k + j, s[j]);
     } else {
         __shared__ float part[4][KC];
         if (lane == 0) {
@@ -159,7 +163,7 @@ __device__ __forceinline__ void store_dots(const RowsParams &p, int64_t t, float
         if ((int)threadIdx.x < p.top_k) {
             float v = 0.0f;
             for (int i = 0; i < (int)(blockDim.x >> 5); ++i) v = __fadd_rn(v, part[i][threadIdx.x]);
-            p.dw[t * p.top_k + threadIdx.x] = v;
+            store_dot(p, t * p.top_k + threadIdx.x, v);
         }
     }
 }
@@ -197,8 +201,9 @@ __global__ void __launch_bounds__(160) spread_kernel(RowsParams p) {
                     for (int i = 0; i < Vec<DT>::N; ++i) v.v[i] = __fmul_rn(x.v[i], ch.w[j]);
                     o = v.pack();
                 }
-                if (store_ok(ch.row[j] + a < p.total_rows * p.row_bytes, p.err))
-                    *reinterpret_cast<uint4 *>(p.rows_out + ch.row[j] + a) = o;
+                uint8_t *out = p.rows_out + ch.row[j] + a;
+                if (store_fits(out, 16, p.rows_out, p.total_rows * p.row_bytes, p.err))
+                    *reinterpret_cast<uint4 *>(out) = o;
                 if constexpr (DOTS) {
                     Vec<DT> v;
                     v.from(y[j]);
@@ -248,8 +253,9 @@ __global__ void __launch_bounds__(160) collect_kernel(RowsParams p) {
             if (DOTS || j0 >= p.top_k) break;
             ch.load(p, me.t, j0, me.at == 0);  // one piece per thread: read once
         }
-        if (store_ok(me.t < p.num_tokens, p.err))
-            *reinterpret_cast<uint4 *>(p.token_out + me.t * p.row_bytes + a) = acc.pack();
+        uint8_t *out = p.token_out + me.t * p.row_bytes + a;
+        if (store_fits(out, 16, p.token_out, p.num_tokens * p.row_bytes, p.err))
+            *reinterpret_cast<uint4 *>(out) = acc.pack();
     }
     if constexpr (DOTS) store_dots<FORM, KC>(p, me.t, dot);
 }
@@ -277,7 +283,7 @@ __global__ void __launch_bounds__(128) dots_kernel(RowsParams p) {
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, o));
-    if (lane == 0) p.dw[c] = s;
+    if (lane == 0) store_dot(p, c, s);
 }
 
 // Threads of a CTA for rows of `pieces` pieces: the first of the sizes that
