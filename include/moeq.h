@@ -456,7 +456,8 @@ moeq_status moeq_dispatch_mxfp4(const void *tokens, int64_t token_stride, int64_
  * m = max x, i_r its choices:
  *   normalize == 0:  w_r = scale * exp(x_{i_r} - m) / sum over all experts of exp(x - m)
  *   normalize != 0:  w_r = scale * exp(x_{i_r} - m) / sum over the choices of exp(x - m)
- * fp32 throughout; exp(d) is within 2 + 1.2 |d| ulp.
+ * fp32 throughout: d = x - m is rounded (|d| 2^-24 of the result), exp(d) of the rounded
+ * d within 2 + 1.2 |d| ulp.
  *   logits      dtype [num_tokens, num_experts], row stride logit_stride elements.
  *   topk_ids    int32 [num_tokens, top_k] (out);  weights fp32 [num_tokens, top_k] (out).
  * A logit of -inf (a masked expert) or NaN is never chosen; a token with fewer
