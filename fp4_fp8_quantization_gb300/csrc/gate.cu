@@ -77,8 +77,8 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 
 // exp(x - m) for x <= m: with d the difference rounded to fp32, within
-// 2 + 1.2 |d| ulp of exp(d), to which the rounding adds |d| 2^-24 of the value
-// (0.5 |d| ulp at most).  NaN for a NaN or for infinity minus infinity.
+// 2 + 1.2 |d| ulp of exp(d), to which the rounding adds |d| 2^-24 of the value.
+// NaN for a NaN or for infinity minus infinity.
 __device__ __forceinline__ float exp_diff(float x, float m) { return __expf(__fadd_rn(x, -m)); }
 
 // Maximum over groups of LANES consecutive lanes, the same in each of them.
