@@ -33,7 +33,8 @@ class Fp8MoeLayer:
 
     router bf16 [E, H]; gate_up bf16 [E, 2 I, H] with row 2 j = gate_j, 2 j + 1 =
     up_j; down bf16 [E, H, I].  Weights are quantized once; workspaces for up to
-    max_tokens tokens are kept."""
+    max_tokens tokens are kept, so that a call given its output allocates nothing
+    (and can be captured in a CUDA graph)."""
 
     def __init__(self, router, gate_up, down, top_k, max_tokens):
         self.E, two_i, self.H = gate_up.shape
@@ -42,6 +43,7 @@ class Fp8MoeLayer:
         self.w2, self.s2 = self._weight(down)
         T, R = max_tokens, max_tokens * top_k
         new = lambda *s, dtype=torch.float32: torch.empty(s, dtype=dtype, device="cuda")  # noqa: E731
+        self.logits = new(T, self.E, dtype=router.dtype)
         self.ids, self.weights, self.dst = _i32(T, top_k), new(T, top_k), _i32(T, top_k)
         self.offsets, self.experts, self.src = _i32(self.E + 1), _i32(self.E), _i32(R)
         self.a, self.sa = new(R, self.H, dtype=F8), new(R, _blocks(self.H))
@@ -57,11 +59,12 @@ class Fp8MoeLayer:
         moeq.quantize_fp8_block_weight(w, q, s)
         return q, s
 
+    @torch.no_grad()
     def __call__(self, x, out=None):
         T, R = x.shape[0], x.shape[0] * self.k
         out = torch.empty_like(x) if out is None else out
         ids, w, dst = self.ids[:T], self.weights[:T], self.dst[:T]
-        logits = x @ self.router.t()
+        logits = torch.mm(x, self.router.t(), out=self.logits[:T])
         moeq.gate_topk(logits, ids, w)
         moeq.route_topk(ids, self.offsets, self.experts, self.src, dst_info=dst)
         moeq.quantize_fp8_block_topk(x, dst, self.a[:R], self.sa[:R])
