@@ -463,7 +463,8 @@ moeq_status moeq_dispatch_mxfp4(const void *tokens, int64_t token_stride, int64_
  * A logit of -inf (a masked expert) or NaN is never chosen; a token with fewer
  * than top_k others gets id -1 and weight 0 in the places left over, which
  * moeq_route_topk drops (setting MOEQ_DEVERR_BAD_EXPERT).  A NaN or +inf logit
- * makes the token's weights NaN.
+ * makes all weights of a token that has a choice NaN, in the places left over too;
+ * a token without a choice has weights 0.
  * 1 <= top_k <= num_experts; num_experts <= 1024 and top_k <= 32 (else
  * MOEQ_ERR_UNSUPPORTED). */
 moeq_status moeq_gate_topk(moeq_dtype dtype, const void *logits, int64_t logit_stride,
@@ -476,6 +477,8 @@ moeq_status moeq_gate_topk(moeq_dtype dtype, const void *logits, int64_t logit_s
  * i_r = j of scale * d_weights_r,
  *   normalize == 0:  d_logits = p * (g - <p, g>)
  *   normalize != 0:  d_logits_{i_r} = scale * q_r * (d_weights_r - <q, d_weights>), 0 elsewhere.
+ * A token without a choice gets 0; a NaN or +inf logit makes a token's gradient NaN
+ * (with normalize that of the chosen).
  *   logits, topk_ids  as given to and returned by moeq_gate_topk: a token's ids are
  *               distinct (an id of -1 is skipped; any other id outside the experts too,
  *               and sets MOEQ_DEVERR_BAD_EXPERT).
