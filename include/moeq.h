@@ -570,8 +570,13 @@ moeq_status moeq_quantize_fp8_block_weight(const void *w, int64_t num_experts, i
  *   c         bf16 [total_tokens, N]
  *   a         E4M3 [total_tokens, K];  a_scales fp32 [total_tokens, ceil(K / 128)]
  *   b         E4M3 [num_experts, N, K];  b_scales fp32 [num_experts, ceil(N / 128), ceil(K / 128)]
+ * The product of the two scales is rounded to fp32 first: below 2^-126 it loses bits, and
+ * from 2^128 on it is infinite (NaN times a zero sum) though the term may not be.
  * K % 16 == 0, N % 8 == 0.  The activations' gradient is the same call on the
- * transposed weights. */
+ * transposed weights: b [num_experts, K, N] and b_scales [num_experts, ceil(K / 128),
+ * ceil(N / 128)] are the same codes and scales with their last two axes exchanged
+ * (the caller's copy), a and a_scales the quantized gradient of c, and N is the
+ * reduction (N % 16 == 0, K % 8 == 0). */
 moeq_status moeq_grouped_matmul_fp8_block(void *c, const uint8_t *a, const uint8_t *b,
                                           const float *a_scales, const float *b_scales,
                                           const uint32_t *a_offsets, const int32_t *expert_ids,
