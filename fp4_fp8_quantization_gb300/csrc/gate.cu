@@ -18,7 +18,12 @@
 // shortened for it, and a token whose choice the shortened ones do not decide
 // is chosen again from the whole ones.  Sums are fp32 in a fixed order.
 // Bound by the integer and selection instructions of the rounds (65537 tokens x
-// 128, top-8, fp32: forward 18.7 us, gradient 10.6 us, 5.6 and 10.5 of memory).  The
+// 128, top-8, fp32: forward 18.8 us over all experts, 17.4 over the chosen,
+// gradient 10.6 us, 5.6 and 10.5 of memory; bf16 forward 16.1 and 14.7, 3.1 of
+// memory).  Equal fp32 logits are not decided by shortened images either: of
+// logits upcast from bf16 about every third token ties, 30.8 us for the 17.4.
+// With 513 to 1024 experts of 16 bits some of a lane's 32 images spill (148 bytes
+// a thread): 8192 x 1024 13.7 us, x 512 7.8; fp32 20.3 and 9.3.  The
 // lane's sorted images in shared memory instead of registers, so that a round
 // moves one of them: the same there, 0.2 us slower for few tokens.
 #include <cuda_fp16.h>
@@ -446,10 +451,10 @@ cudaError_t run_gate_lanes(const GateParams &p, cudaStream_t s) {
 template <int DT>
 cudaError_t run_gate(const GateParams &p, cudaStream_t s) {
     // many tokens: as few lanes per token as leave each at most 8 logits, so that
-    // the rounds of a warp's tokens are shared.  fp32, top-8, these lanes against
-    // 32: 65536 tokens x 32 experts 6.7 / 17.6 us, x 64 9.3 / 18.2, x 128 19.4 /
-    // 21.1; 16384 x 128 6.7 / 6.5 (bf16 6.0 / 6.1), 8192 x 64 3.5 / 3.8, x 128 5.0 /
-    // 4.4; 4096 x 64 3.1 / 2.7
+    // the rounds of a warp's tokens are shared.  fp32, top-8, normalised, these
+    // lanes against 32: 65536 tokens x 32 experts 6.7 / 17.8 us, x 64 8.5 / 17.9, x
+    // 128 17.4 / 20.3; 16384 x 128 6.2 / 6.3 (bf16 5.5 / 5.7), 8192 x 64 3.2 / 3.7, x
+    // 128 5.1 / 4.3; 4096 x 64 3.0 / 2.6
     if (p.num_tokens >= 8192 && p.top_k <= 8) {
         if (p.E <= 32) return run_gate_lanes<DT, 4, 8>(p, s);
         if (p.E <= 64) return run_gate_lanes<DT, 8, 8>(p, s);

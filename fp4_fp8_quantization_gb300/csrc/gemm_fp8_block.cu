@@ -24,10 +24,15 @@
 // into the SM (70 bytes a cycle; more requests or reads of them slow it at once,
 // below), and the two accumulators' chain of MMAs, commit, 560 cycles of loads
 // and sums, and release.  Above that is the power limit: 65536 x 7168 x 4096,
-// 64 experts, 1.46 ms a single launch (2.64 PFLOP/s), 1.62 back to back at about
-// 1.5 GHz (2.37); the rowwise-scaled GEMM on the same operands 1.33 and 1.54.
+// 64 experts, 1.43 to 1.54 ms a single launch (2.7 to 2.5 PFLOP/s), 1.62 to 1.72
+// back to back at about 1.5 GHz (2.4 to 2.2); the rowwise-scaled GEMM on the same
+// operands 1.33 and 1.54.
 // With few rows the stream of the weights: 512 rows over 256 experts, K 7168, N
-// 4096, 0.93 ms, 103 % of the copy rate.
+// 4096, 0.93 ms, 103 % of the copy rate.  With sizes that end inside tiles
+// (11996 rows over 48 experts, K 2480, N 1880: 99 us, 44 of memory), the whole
+// tiles that a group's last rows and the last columns cost (the MMA's N and the
+// weights' box are a tile's, 2048 columns for 1880), rows that start inside lines
+// (K 2560: 74), and seven waves for 6.2 of tiles dealt out by number.
 // What did not help: 64-column tensor-memory loads, polling waits, a second
 // issuing warp (all within 1 %), the scales brought to shared memory by the two
 // idle warps (10 % slower: the wait for them joins each block's chain), CTAs of
@@ -623,11 +628,14 @@ enum Form { kSmallTile = 0, kLargeTileByTensor = 1, kLargeTile = 2 };
 // its stages hold two K blocks, so that the waits of the issuing and summing
 // warps, which bound so small a block, are paid once for both (2 to 15 % of the
 // times below).  The choice compares, per K block and in ns, the full waves of
-// tiles, each at the rate of memory or of one CTA's loop (430 and 330 ns measured
-// on streams that leave SMs idle, one block per stage), and the last partial one
-// at the latter.  Measured with K 4096, N 1536 (small against large tiles): 8
-// rows over 8 experts 13.7 / 18.8 us, 16 over 16 27.2 / 22.9, 32 over 29 35.5 /
-// 43.5, 4096 over 128 131 / 142, 8192 over 128 160 / 146, 512 over 8 14.0 / 19.8.
+// tiles, each at the rate of memory or of one CTA's loop, and the last partial one
+// at the latter.  430 is the large tile's loop on streams that leave SMs idle
+// (380 to 440 by the slope of K 4096, 8192 and 16384), 330 the small one's with one
+// block per stage; with two it takes 200 to 270, so that the rule leans to the
+// large tile where the two are close.  Measured with K 4096, N 1536 (small against
+// large tiles): 8 rows over 8 experts 13.6 / 17.9 us, 16 over 16 24.2 / 22.0, 32 over
+// 29 35.4 / 41.6, 4096 over 128 131 / 139, 8192 over 128 146 / 144, 512 over 8 14.0 /
+// 19.2; the rule takes the smaller of each two.
 cudaError_t launch_gemm_fp8_block(const GemmBlockArgs &a, cudaStream_t s) {
     const int64_t T = a.groups.total_rows, g = std::min<int64_t>(a.groups.num_groups, T);
     const int64_t sms = sm_count();
