@@ -610,10 +610,13 @@ moeq_status moeq_gate_topk(moeq_dtype dtype, const void *logits, int64_t logit_s
     return cuda_status(moeq::launch_gate(a, stream));
 }
 
-moeq_status moeq_gate_topk_grad(moeq_dtype dtype, const void *logits, int64_t logit_stride,
-                                int64_t num_tokens, int32_t num_experts, int32_t top_k,
-                                int32_t normalize, float scale, const int32_t *topk_ids,
-                                const float *d_weights, void *d_logits, moeq_stream_t stream) {
+// chosen: 0 the softmax's gradient over all experts or the choices, 1 that of the
+// chosen logits only with sigmoid scores, 2 with softmax scores.
+static moeq_status gate_grad_call(moeq_dtype dtype, const void *logits, int64_t logit_stride,
+                                  int64_t num_tokens, int32_t num_experts, int32_t top_k,
+                                  int32_t normalize, float scale, const int32_t *topk_ids,
+                                  const float *d_weights, void *d_logits, int chosen,
+                                  moeq_stream_t stream) {
     const moeq_status st =
         gate_args_ok(dtype, logits, logit_stride, num_tokens, num_experts, top_k);
     if (st != MOEQ_OK) return st;
@@ -636,7 +639,57 @@ moeq_status moeq_gate_topk_grad(moeq_dtype dtype, const void *logits, int64_t lo
     a.d_weights = d_weights;
     a.d_logits = d_logits;
     a.err = err;
-    return cuda_status(moeq::launch_gate(a, stream));
+    return cuda_status(chosen ? moeq::launch_gate_chosen_grad(a, chosen == 1, stream)
+                              : moeq::launch_gate(a, stream));
+}
+
+moeq_status moeq_gate_topk_grad(moeq_dtype dtype, const void *logits, int64_t logit_stride,
+                                int64_t num_tokens, int32_t num_experts, int32_t top_k,
+                                int32_t normalize, float scale, const int32_t *topk_ids,
+                                const float *d_weights, void *d_logits, moeq_stream_t stream) {
+    return gate_grad_call(dtype, logits, logit_stride, num_tokens, num_experts, top_k, normalize,
+                          scale, topk_ids, d_weights, d_logits, 0, stream);
+}
+
+moeq_status moeq_gate_group_topk_grad(moeq_dtype dtype, const void *logits, int64_t logit_stride,
+                                      int64_t num_tokens, int32_t num_experts, moeq_score score,
+                                      int32_t top_k, int32_t normalize, float scale,
+                                      const int32_t *topk_ids, const float *d_weights,
+                                      void *d_logits, moeq_stream_t stream) {
+    if (score != MOEQ_SCORE_SOFTMAX && score != MOEQ_SCORE_SIGMOID) return MOEQ_ERR_INVALID_ARG;
+    const int chosen = score == MOEQ_SCORE_SIGMOID ? 1 : normalize ? 2 : 0;
+    return gate_grad_call(dtype, logits, logit_stride, num_tokens, num_experts, top_k, normalize,
+                          scale, topk_ids, d_weights, d_logits, chosen, stream);
+}
+
+moeq_status moeq_gate_group_topk(moeq_dtype dtype, const void *logits, int64_t logit_stride,
+                                 int64_t num_tokens, int32_t num_experts, const float *bias,
+                                 moeq_score score, int32_t num_groups, int32_t topk_groups,
+                                 moeq_group_score group_score, int32_t top_k, int32_t normalize,
+                                 float scale, int32_t *topk_ids, float *weights,
+                                 moeq_stream_t stream) {
+    if ((score != MOEQ_SCORE_SOFTMAX && score != MOEQ_SCORE_SIGMOID) ||
+        (group_score != MOEQ_GROUP_MAX && group_score != MOEQ_GROUP_TOP2) || num_groups < 1 ||
+        topk_groups < 1 || topk_groups > num_groups || num_experts % num_groups)
+        return MOEQ_ERR_INVALID_ARG;
+    const moeq_status st =
+        gate_args_ok(dtype, logits, logit_stride, num_tokens, num_experts, top_k);
+    if (st != MOEQ_OK) return st;
+    const int32_t size = num_experts / num_groups;
+    if (top_k > topk_groups * size) return MOEQ_ERR_INVALID_ARG;
+    int32_t lanes = 1;
+    while (lanes < num_groups) lanes *= 2;
+    if (num_groups > moeq::kMaxExpertGroups || size > 1024 / lanes) return MOEQ_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return MOEQ_OK;
+    if (!topk_ids || !weights || !aligned16(topk_ids) || !aligned16(weights) || !aligned16(bias))
+        return MOEQ_ERR_INVALID_ARG;
+    uint32_t *err = device_error_ptr();
+    if (!err) return cuda_status(cudaErrorInvalidDevice);
+    const moeq::GateScoredArgs a{(int)dtype, logits, logit_stride, num_tokens, num_experts, top_k,
+                                 bias, score == MOEQ_SCORE_SIGMOID,
+                                 group_score == MOEQ_GROUP_TOP2, num_groups, topk_groups,
+                                 normalize != 0, scale, topk_ids, weights, err};
+    return cuda_status(moeq::launch_gate_scored(a, stream));
 }
 
 // Common checks of the calls between tokens and their rows.

@@ -170,6 +170,29 @@ struct GateArgs {
 };
 cudaError_t launch_gate(const GateArgs &a, cudaStream_t s);
 
+// The gradient of the router's weights that reaches the chosen logits only:
+// sigmoid scores, or the softmax over the choices (GateArgs.normalize).
+cudaError_t launch_gate_chosen_grad(const GateArgs &a, bool sigmoid, cudaStream_t s);
+
+// The router with scores, a balance bias (or null) and groups of experts.
+struct GateScoredArgs {
+    int dtype;
+    const void *logits;
+    int64_t stride, num_tokens;
+    int32_t num_experts, top_k;
+    const float *bias;
+    bool sigmoid, top2;
+    int32_t groups, topk_groups;
+    int normalize;
+    float scale;
+    int32_t *ids;
+    float *weights;
+    uint32_t *err;
+};
+// Returns cudaErrorNotSupported for groups that do not fit a warp's lanes.
+cudaError_t launch_gate_scored(const GateScoredArgs &a, cudaStream_t s);
+constexpr int kMaxExpertGroups = 32;
+
 // 1 x 128 block quantization of rows, routed tokens (dst) or SwiGLU rows.
 struct Fp8BlockArgs {
     const void *in;

@@ -20,6 +20,8 @@ _LIB_PATH = os.environ.get("MOEQ_LIB") or os.path.join(
 _lib = None
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # moeq_dtype
+SCORES = {"softmax": 0, "sigmoid": 1}                              # moeq_score
+GROUP_SCORES = {"max": 0, "top2": 1}                               # moeq_group_score
 FORMATS = {"nvfp4": 0, "mxfp4": 1, "mxfp8": 2}
 STATUS = {0: "MOEQ_OK", 1: "MOEQ_ERR_INVALID_ARG", 2: "MOEQ_ERR_UNSUPPORTED",
           3: "MOEQ_ERR_CUDA", 4: "MOEQ_ERR_DEVICE"}
@@ -60,6 +62,10 @@ _SIGNATURES = {
                             _P, _I32, _P],
     "moeq_gate_topk": [_I32, _P, _I64, _I64, _I32, _I32, _I32, _F, _P, _P, _P],
     "moeq_gate_topk_grad": [_I32, _P, _I64, _I64, _I32, _I32, _I32, _F, _P, _P, _P, _P],
+    "moeq_gate_group_topk": [_I32, _P, _I64, _I64, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32,
+                             _F, _P, _P, _P],
+    "moeq_gate_group_topk_grad": [_I32, _P, _I64, _I64, _I32, _I32, _I32, _I32, _F, _P, _P, _P,
+                                  _P],
     "moeq_permute_topk": [_I32, _P, _I64, _I64, _I64, _P, _I32, _P, _P, _I64, _P],
     "moeq_permute_topk_grad": [_I32, _P, _I64, _I64, _I64, _P, _I32, _P, _P, _P, _I64, _P, _P],
     "moeq_combine_topk": [_I32, _P, _I64, _I64, _I64, _P, _I32, _P, _P, _P],
@@ -470,6 +476,62 @@ def gate_topk_grad(logits, topk_ids, d_weights, d_logits, normalize=True, scale=
           bool(normalize), scale, _ptr(topk_ids, torch.int32, "topk_ids"),
           _shaped(d_weights, (T, k), torch.float32, "d_weights"),
           _shaped(d_logits, (T, E), logits.dtype, "d_logits"), _stream(stream))
+
+
+def _one_of(names, name, what):
+    code = names.get(name)
+    if code is None:
+        raise ValueError(f"{what}: {name!r}, expected one of {tuple(names)}")
+    return code
+
+
+def _on_current_device(*tensors):
+    """The calls launch on the current device: every tensor lives there."""
+    at = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != at:
+            raise ValueError(f"a tensor on {t.device}: expected the current device, cuda:{at}")
+
+
+def gate_group_topk(logits, topk_ids, weights, bias=None, score="sigmoid", num_groups=1,
+                    topk_groups=None, group_score="top2", normalize=True, scale=1.0, stream=None):
+    """The router with scores ("sigmoid" or "softmax" of the logits), a balance
+    bias (fp32 [num_experts] or None: added to the scores for the choice, not in
+    the weights) and groups: of num_groups groups of consecutive experts the
+    topk_groups (None: all) of the largest value are kept, the value being the
+    best score with bias ("max") or the sum of the best two ("top2").  topk_ids
+    (int32 [num_tokens, top_k], out) are the best experts of those, the best
+    first, ties to the lowest index; weights (fp32, out) their scores, divided by
+    their sum (normalize), times scale.  logits bf16 / fp16 / fp32 [num_tokens,
+    num_experts], -inf for a masked expert; id -1 and weight 0 where none is left."""
+    p = _rows_of(logits, "logits")
+    T, E = logits.shape
+    k = _choices(topk_ids, T)
+    ids = _ptr(topk_ids, torch.int32, "topk_ids")
+    w = _shaped(weights, (T, k), torch.float32, "weights")
+    b = _shaped(bias, (E,), torch.float32, "bias", True)
+    _on_current_device(logits, topk_ids, weights, bias)
+    _call("moeq_gate_group_topk", DTYPES[logits.dtype], p, _row_stride(logits), T, E, b,
+          _one_of(SCORES, score, "score"), num_groups,
+          num_groups if topk_groups is None else topk_groups,
+          _one_of(GROUP_SCORES, group_score, "group_score"), k, bool(normalize), scale, ids, w,
+          _stream(stream))
+
+
+def gate_group_topk_grad(logits, topk_ids, d_weights, d_logits, score="sigmoid", normalize=True,
+                         scale=1.0, stream=None):
+    """Gradient of gate_group_topk's weights, the choice taken as fixed: d_logits
+    (out, the logits' dtype, contiguous) from d_weights fp32 [num_tokens, top_k]
+    and the logits and topk_ids of the forward call."""
+    p = _rows_of(logits, "logits")
+    T, E = logits.shape
+    k = _choices(topk_ids, T)
+    ids = _ptr(topk_ids, torch.int32, "topk_ids")
+    dw = _shaped(d_weights, (T, k), torch.float32, "d_weights")
+    dx = _shaped(d_logits, (T, E), logits.dtype, "d_logits")
+    _on_current_device(logits, topk_ids, d_weights, d_logits)
+    _call("moeq_gate_group_topk_grad", DTYPES[logits.dtype], p, _row_stride(logits), T, E,
+          _one_of(SCORES, score, "score"), k, bool(normalize), scale, ids, dw, dx, _stream(stream))
 
 
 def permute_topk(tokens, dst_info, rows, weights=None, stream=None):

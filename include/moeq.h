@@ -488,6 +488,52 @@ moeq_status moeq_gate_topk_grad(moeq_dtype dtype, const void *logits, int64_t lo
                                 int32_t normalize, float scale, const int32_t *topk_ids,
                                 const float *d_weights, void *d_logits, moeq_stream_t stream);
 
+/* The router with scores, a balance bias and groups of experts.  With x a token's
+ * logits, s_j = sigmoid(x_j) or the softmax of x, c_j = s_j + bias_j:
+ *   the experts are num_groups groups of consecutive ones; a group's value is its
+ *   largest c (MOEQ_GROUP_MAX), or the sum of its two largest (MOEQ_GROUP_TOP2; of one
+ *   usable expert alone, that one's); of the topk_groups groups of the largest values
+ *   (ties: the lowest index) the top_k experts of the largest c (ties: the lowest
+ *   index) are chosen, the largest first;
+ *   normalize == 0:  w_r = scale * s_{i_r}
+ *   normalize != 0:  w_r = scale * s_{i_r} / sum over the choices of s  (0 where it is 0)
+ * The bias decides the choice and does not enter the weights; without one (NULL) c is
+ * ordered as the logits are.  The order is that of c in 64 bits, whatever its fp32
+ * rounding; weights are fp32, from s within 4 ulp (sigmoid) or as in moeq_gate_topk.
+ *   logits      dtype [num_tokens, num_experts], row stride logit_stride elements.
+ *   bias        fp32 [num_experts] or NULL.
+ *   topk_ids    int32 [num_tokens, top_k] (out);  weights fp32 [num_tokens, top_k] (out).
+ * A logit of -inf or NaN, and with a bias one whose c is (a bias of -inf or NaN), is never
+ * chosen; places left over get id -1 and weight 0.  A NaN logit makes all weights of a
+ * token that has a choice NaN; for a softmax a +inf logit does too, and such a token's
+ * choice goes by its logits, without the bias.
+ * num_groups divides num_experts; 1 <= topk_groups <= num_groups; 1 <= top_k <=
+ * topk_groups * (num_experts / num_groups).  num_experts <= 1024, top_k <= 32,
+ * num_groups <= 32 and, with P the power of two from num_groups on, at most 32
+ * experts for each of the 32 / P lanes that a group has, num_experts / num_groups <=
+ * 1024 / P (else MOEQ_ERR_UNSUPPORTED). */
+typedef enum { MOEQ_SCORE_SOFTMAX = 0, MOEQ_SCORE_SIGMOID = 1 } moeq_score;
+typedef enum { MOEQ_GROUP_MAX = 0, MOEQ_GROUP_TOP2 = 1 } moeq_group_score;
+moeq_status moeq_gate_group_topk(moeq_dtype dtype, const void *logits, int64_t logit_stride,
+                                 int64_t num_tokens, int32_t num_experts, const float *bias,
+                                 moeq_score score, int32_t num_groups, int32_t topk_groups,
+                                 moeq_group_score group_score, int32_t top_k, int32_t normalize,
+                                 float scale, int32_t *topk_ids, float *weights,
+                                 moeq_stream_t stream);
+
+/* Gradient of moeq_gate_group_topk's weights (the choice is taken as fixed; the bias has
+ * none): with q = w / scale and g_r = scale * d_weights_r,
+ *   sigmoid, normalize == 0:  d_logits_{i_r} = g_r * s (1 - s)
+ *   sigmoid, normalize != 0:  d_logits_{i_r} = q_r * (g_r - <q, g>) * (1 - s)
+ *   softmax, normalize != 0:  d_logits_{i_r} = q_r * (g_r - <q, g>)
+ * and 0 elsewhere: only the chosen logits are read.  Softmax without normalize is
+ * moeq_gate_topk_grad.  Arguments as there. */
+moeq_status moeq_gate_group_topk_grad(moeq_dtype dtype, const void *logits, int64_t logit_stride,
+                                      int64_t num_tokens, int32_t num_experts, moeq_score score,
+                                      int32_t top_k, int32_t normalize, float scale,
+                                      const int32_t *topk_ids, const float *d_weights,
+                                      void *d_logits, moeq_stream_t stream);
+
 /* Tokens sorted by expert: rows[dst_info[t, j]] = weights[t, j] * tokens[t].
  *   tokens    dtype [num_tokens, hidden], row stride token_stride elements.
  *   dst_info  int32 [num_tokens, top_k] (from moeq_route_topk): the row of each choice,
