@@ -820,6 +820,65 @@ moeq_status moeq_quantize_fp8_block_weight(const void *w, int64_t num_experts, i
         moeq::launch_fp8_block_weight(w, num_experts, N, K, out, scales, err, stream));
 }
 
+static moeq_status norm_sizes_ok(int64_t rows, int64_t K) {
+    if (rows < 0 || K <= 0 || K % 8) return MOEQ_ERR_INVALID_ARG;
+    if (rows >= (int64_t)1 << 31 || K > moeq::kNormMaxCols) return MOEQ_ERR_UNSUPPORTED;
+    return MOEQ_OK;
+}
+
+// A strided matrix of 16-byte vectors; one that may be absent.
+static bool rows_ok(const void *p, int64_t stride, int64_t K, bool required) {
+    return p ? aligned16(p) && stride >= K && stride % 8 == 0 : !required;
+}
+
+moeq_status moeq_add_rms_norm(moeq_dtype dtype, const void *x, int64_t x_stride,
+                              const void *residual, int64_t residual_stride, int64_t rows,
+                              int64_t K, const void *weight, float eps, void *h, void *y,
+                              uint8_t *q, float *scales, int32_t row_scales, float *rstd,
+                              moeq_stream_t stream) {
+    if (!dtype_ok(dtype) || !(eps >= 0.0f)) return MOEQ_ERR_INVALID_ARG;
+    const moeq_status st = norm_sizes_ok(rows, K);
+    if (st != MOEQ_OK) return st;
+    if (rows == 0) return MOEQ_OK;
+    if (!rows_ok(x, x_stride, K, true) || !rows_ok(residual, residual_stride, K, false) ||
+        !weight || !aligned16(weight) || !aligned16(h) || !aligned16(y) || !aligned16(q) ||
+        !aligned16(scales) || !aligned16(rstd))
+        return MOEQ_ERR_INVALID_ARG;
+    if (!h != !residual || !q != !scales || (q && K % 16) || (!y && !q && !rstd))
+        return MOEQ_ERR_INVALID_ARG;
+    uint32_t *err = device_error_ptr();
+    if (!err) return cuda_status(cudaErrorInvalidDevice);
+    const moeq::NormArgs a{(int)dtype, x, residual, weight, x_stride, residual_stride, rows, K,
+                           eps, h, y, q, scales, row_scales != 0, rstd, err};
+    return cuda_status(moeq::launch_norm(a, stream));
+}
+
+int64_t moeq_add_rms_norm_grad_workspace(int64_t rows, int64_t K) {
+    if (norm_sizes_ok(rows, K) != MOEQ_OK) return -1;
+    return rows ? moeq::norm_grad_parts(rows, K) * K * 4 : 0;
+}
+
+moeq_status moeq_add_rms_norm_grad(moeq_dtype dtype, const void *d_y, int64_t d_y_stride,
+                                   const void *d_h, int64_t d_h_stride, const void *h,
+                                   int64_t h_stride, int64_t rows, int64_t K, const void *weight,
+                                   const float *rstd, void *d_x, float *d_weight, void *workspace,
+                                   moeq_stream_t stream) {
+    if (!dtype_ok(dtype)) return MOEQ_ERR_INVALID_ARG;
+    const moeq_status st = norm_sizes_ok(rows, K);
+    if (st != MOEQ_OK) return st;
+    if (rows == 0 && !d_weight) return MOEQ_OK;
+    if (rows > 0 && (!rows_ok(d_y, d_y_stride, K, true) || !rows_ok(d_h, d_h_stride, K, false) ||
+        !rows_ok(h, h_stride, K, true) || !weight || !aligned16(weight) || !rstd ||
+        !aligned16(rstd) || !d_x || !aligned16(d_x) || (d_weight && !workspace)))
+        return MOEQ_ERR_INVALID_ARG;
+    if (!aligned16(d_weight) || !aligned16(workspace)) return MOEQ_ERR_INVALID_ARG;
+    uint32_t *err = device_error_ptr();
+    if (!err) return cuda_status(cudaErrorInvalidDevice);
+    const moeq::NormGradArgs a{(int)dtype, d_y, d_h, h, weight, d_y_stride, d_h_stride, h_stride,
+                               rows, K, rstd, d_x, d_weight, static_cast<float *>(workspace), err};
+    return cuda_status(moeq::launch_norm_grad(a, stream));
+}
+
 moeq_status moeq_grouped_matmul_fp8_block(void *c, const uint8_t *a, const uint8_t *b,
                                           const float *a_scales, const float *b_scales,
                                           const uint32_t *a_offsets, const int32_t *expert_ids,

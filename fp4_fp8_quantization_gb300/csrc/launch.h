@@ -209,6 +209,35 @@ cudaError_t launch_fp8_block(const Fp8BlockArgs &a, cudaStream_t s);
 cudaError_t launch_fp8_block_weight(const void *w, int64_t E, int64_t N, int64_t K, uint8_t *out,
                                     float *scales, uint32_t *err, cudaStream_t s);
 
+// Residual addition, root-mean-square norm and 8-bit output; its gradient.
+// Strides in elements; res null: h is x and is not written.
+struct NormArgs {
+    int dtype;
+    const void *x, *res, *w;
+    int64_t x_stride, res_stride, rows, K;
+    float eps;
+    void *h, *y;
+    uint8_t *q;
+    float *scales;
+    bool row_scales;
+    float *rstd;
+    uint32_t *err;
+};
+cudaError_t launch_norm(const NormArgs &a, cudaStream_t s);
+
+struct NormGradArgs {
+    int dtype;
+    const void *dy, *dh, *h, *w;
+    int64_t dy_stride, dh_stride, h_stride, rows, K;
+    const float *rstd;
+    void *dx;
+    float *d_weight, *workspace;  // workspace: norm_grad_parts(rows, K) rows of K
+    uint32_t *err;
+};
+int64_t norm_grad_parts(int64_t rows, int64_t K);
+cudaError_t launch_norm_grad(const NormGradArgs &a, cudaStream_t s);
+constexpr int64_t kNormMaxCols = 16384;
+
 // Maximum number of groups the GEMM scheduler accepts.
 constexpr int kMaxGroups = 1024;
 

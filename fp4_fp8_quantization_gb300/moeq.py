@@ -74,6 +74,11 @@ _SIGNATURES = {
     "moeq_quantize_fp8_block_topk": [_P, _I64, _I64, _I64, _P, _I32, _P, _P, _I64, _P],
     "moeq_swiglu_quantize_fp8_block": [_P, _I64, _I64, _P, _P, _P],
     "moeq_quantize_fp8_block_weight": [_P, _I64, _I64, _I64, _P, _P, _P],
+    "moeq_add_rms_norm": [_I32, _P, _I64, _P, _I64, _I64, _I64, _P, _F, _P, _P, _P, _P, _I32, _P,
+                          _P],
+    "moeq_add_rms_norm_grad_workspace": [_I64, _I64],
+    "moeq_add_rms_norm_grad": [_I32, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P,
+                               _P],
     "moeq_grouped_matmul_fp8_block": [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32,
                                       _I32, _P],
     "moeq_get_device_error": [_P, _U32P],
@@ -105,6 +110,7 @@ def lib():
             f.restype = ctypes.c_int
         L.moeq_status_string.restype = ctypes.c_char_p
         L.moeq_dispatch_scale_rows.restype = ctypes.c_int64
+        L.moeq_add_rms_norm_grad_workspace.restype = ctypes.c_int64
         _lib = L
     return _lib
 
@@ -646,6 +652,75 @@ def quantize_fp8_block_weight(w, out, scales, stream=None):
           _shaped(out, (E, N, K), _U8, "out"),
           _shaped(scales, (E, _blocks128(N), _blocks128(K)), torch.float32,
                   "scales"), _stream(stream))
+
+
+def _workspace(workspace, need, like):
+    """Pointer of a workspace of at least `need` bytes: the caller's, or a new
+    one (freed in stream order by PyTorch's allocator)."""
+    if need < 0:
+        raise ValueError("sizes that the call does not take")
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    if workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace: {need} bytes expected")
+    return workspace, _ptr(workspace, None, "workspace")
+
+
+def add_rms_norm(x, weight, y=None, residual=None, h=None, q=None, scales=None, rstd=None,
+                 eps=1e-6, stream=None):
+    """h = x + residual (out, the new residual stream; without a residual h is x
+    and is not given); y (out) = h / rms(h) * weight, and / or the same in E4M3:
+    q (out, uint8 / float8_e4m3fn [rows, K]) with scales (out) fp32 [rows,
+    ceil(K / 128)] or, one for each row, [rows].  rstd (out, fp32 [rows]) is
+    1 / rms, for the gradient.  x, residual, h, y [rows, K] and weight [K] of one
+    type, bf16 / fp16 / fp32; h and y may be x or residual themselves."""
+    p = _rows_of(x, "x")
+    n, k = x.shape
+    dt = x.dtype
+    pr = None if residual is None else _rows_of(residual, "residual", (n, k), dt)
+    pw = _shaped(weight, (k,), dt, "weight")
+    ph = _shaped(h, (n, k), dt, "h", True)
+    py = _shaped(y, (n, k), dt, "y", True)
+    pq = _shaped(q, (n, k), _U8, "q", True)
+    by_row = scales is not None and scales.dim() == 1
+    ps = _shaped(scales, (n,) if by_row else (n, _blocks128(k)), torch.float32, "scales", True)
+    pu = _shaped(rstd, (n,), torch.float32, "rstd", True)
+    _on_current_device(x, weight, y, residual, h, q, scales, rstd)
+    _call("moeq_add_rms_norm", DTYPES[dt], p, _row_stride(x), pr,
+          k if residual is None else _row_stride(residual), n, k, pw, eps, ph, py, pq, ps, by_row,
+          pu, _stream(stream))
+
+
+def add_rms_norm_grad_workspace(rows, K):
+    """Bytes of the workspace that add_rms_norm_grad takes for d_weight."""
+    return lib().moeq_add_rms_norm_grad_workspace(rows, K)
+
+
+def add_rms_norm_grad(d_y, h, weight, rstd, d_x, d_weight=None, d_h=None, workspace=None,
+                      stream=None):
+    """Gradient of add_rms_norm: d_x (out, x's and the residual's alike) from d_y,
+    the forward call's h (x where there was no residual) and rstd, plus d_h, what
+    reaches h along the residual stream; d_weight (out, fp32 [K]).  workspace:
+    add_rms_norm_grad_workspace(rows, K) bytes, needed with d_weight; without
+    one it is allocated, on the current stream (so give it with another)."""
+    p = _rows_of(d_y, "d_y")
+    n, k = d_y.shape
+    dt = d_y.dtype
+    ph = _rows_of(h, "h", (n, k), dt)
+    pd = None if d_h is None else _rows_of(d_h, "d_h", (n, k), dt)
+    pw = _shaped(weight, (k,), dt, "weight")
+    pu = _shaped(rstd, (n,), torch.float32, "rstd")
+    px = _shaped(d_x, (n, k), dt, "d_x")
+    pg = _shaped(d_weight, (k,), torch.float32, "d_weight", True)
+    ws = None
+    if d_weight is not None:
+        if workspace is None and stream is not None:
+            raise ValueError("workspace: required with a stream")
+        workspace, ws = _workspace(workspace, add_rms_norm_grad_workspace(n, k), d_y)
+    _on_current_device(d_y, h, weight, rstd, d_x, d_weight, d_h, workspace)
+    _call("moeq_add_rms_norm_grad", DTYPES[dt], p, _row_stride(d_y), pd,
+          k if d_h is None else _row_stride(d_h), ph, _row_stride(h), n, k, pw, pu, px, pg, ws,
+          _stream(stream))
 
 
 def grouped_matmul_fp8_block(c, a, b, a_scales, b_scales, a_offsets, expert_ids,

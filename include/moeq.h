@@ -608,6 +608,53 @@ moeq_status moeq_swiglu_quantize_fp8_block(const void *y, int64_t rows, int64_t 
 moeq_status moeq_quantize_fp8_block_weight(const void *w, int64_t num_experts, int64_t N, int64_t K,
                                            uint8_t *out, float *scales, moeq_stream_t stream);
 
+/* ---- before a layer: the residual's addition, the root-mean-square norm and FP8
+ *
+ * For each row, of one dtype throughout:
+ *   h = x + residual, rounded to the dtype (the new residual stream; without a
+ *       residual h is x and is not written)
+ *   rstd = 1 / sqrt(mean of h^2 + eps),  v = (h * rstd) * weight
+ *   y = v, rounded to the dtype;  q, scales = v in E4M3 by the rule of
+ *       moeq_quantize_fp8_block, from fp32 (not from y)
+ * fp32 throughout, the squares' sum too (squares past its range give an infinite sum).
+ *   x, residual dtype [rows, K], row strides x_stride, residual_stride elements.
+ *   weight      dtype [K].
+ *   h, y        dtype [rows, K] (out); h required with a residual and only then.
+ *   q           E4M3 [rows, K] (out);  scales (out) fp32 [rows, ceil(K / 128)], or, with
+ *               row_scales != 0, one for each row, fp32 [rows] (the operands of
+ *               moeq_grouped_matmul_fp8_block and moeq_grouped_matmul_rowwise_fp8).
+ *   rstd        fp32 [rows] (out), for the gradient.
+ * y, q with scales, and rstd may be NULL, not all of them.  h and y may be x's or the
+ * residual's own buffer (the same rows at the same stride); other overlaps are not allowed.
+ * K and the strides are multiples of 8, with q K of 16; K <= 16384 (else
+ * MOEQ_ERR_UNSUPPORTED); eps >= 0. */
+moeq_status moeq_add_rms_norm(moeq_dtype dtype, const void *x, int64_t x_stride,
+                              const void *residual, int64_t residual_stride, int64_t rows,
+                              int64_t K, const void *weight, float eps, void *h, void *y,
+                              uint8_t *q, float *scales, int32_t row_scales, float *rstd,
+                              moeq_stream_t stream);
+
+/* Gradient of moeq_add_rms_norm (of x and of the residual alike; the quantization's is
+ * that of v, d_y).  With u = rstd, g = weight * d_y and d_h the gradient that reaches h
+ * by itself, along the residual stream:
+ *   d_x = u * (g - h * u^2 * mean(g * h)) + d_h;  d_weight = sum over the rows of d_y * h * u
+ * fp32; d_weight's sums run in an order that the sizes alone give.
+ *   d_y, d_h, h dtype [rows, K], rows strided; d_h NULL: none.
+ *   rstd        fp32 [rows], from the forward call.
+ *   d_x         dtype [rows, K] (out; may be d_y's, d_h's or h's own buffer, at stride K).
+ *   d_weight    fp32 [K] (out) or NULL.  With it, workspace: device memory of
+ *               moeq_add_rms_norm_grad_workspace(rows, K) bytes that no other call in
+ *               flight uses (two captured graphs that share one do not run at once).
+ * rows == 0: d_weight is 0. */
+moeq_status moeq_add_rms_norm_grad(moeq_dtype dtype, const void *d_y, int64_t d_y_stride,
+                                   const void *d_h, int64_t d_h_stride, const void *h,
+                                   int64_t h_stride, int64_t rows, int64_t K, const void *weight,
+                                   const float *rstd, void *d_x, float *d_weight, void *workspace,
+                                   moeq_stream_t stream);
+
+/* Bytes of that workspace (-1: sizes that the call refuses).  Host only. */
+int64_t moeq_add_rms_norm_grad_workspace(int64_t rows, int64_t K);
+
 /* Grouped FP8 matmul with a scale for each block of 128:
  *   c[t, n] = bf16( sum over kb of (a_scales[t, kb] * b_scales[e, n / 128, kb])
  *                   * sum over k in block kb of a[t, k] * b[e, n, k] ),  e = expert_ids[g]

@@ -48,3 +48,46 @@ def test_binding_refuses_host_tensors():
         moeq.gate_group_topk(x, ids, torch.zeros(4, 2))
     with pytest.raises(ValueError):
         moeq.gate_group_topk_grad(x, ids, torch.zeros(4, 2), x)
+
+
+def test_norm_refusals(lib):  # noqa: F811
+    call = _caller(lib.moeq_add_rms_norm, dict(
+        dt=0, x=FAKE, xs=64, r=FAKE, rs=64, R=8, K=64, w=FAKE, eps=1e-6, h=FAKE, y=FAKE, q=FAKE,
+        s=FAKE, by_row=0, u=FAKE, st=None))
+    assert call(dt=3) == BAD and call(R=-1) == BAD and call(K=0) == BAD and call(K=68, xs=72, rs=72) == BAD
+    assert call(K=56) == BAD                               # codes of a K that is no multiple of 16
+    assert call(eps=-1.0) == BAD and call(eps=float("nan")) == BAD
+    assert call(xs=56) == BAD and call(xs=68) == BAD and call(rs=60) == BAD
+    for p in ("x", "r", "w", "h", "y", "q", "s", "u"):
+        assert call(**{p: ODD}) == BAD
+    for p in ("x", "w", "h", "q", "s", "r"):               # h goes with a residual, scales with codes
+        assert call(**{p: None}) == BAD
+    assert call(y=None, q=None, s=None, u=None) == BAD     # nothing to compute
+    assert call(K=16392, xs=16392, rs=16392) == UNSUPPORTED and call(R=1 << 31) == UNSUPPORTED
+    assert call(R=0, x=None, w=None, r=None, h=None) == OK
+
+
+def test_norm_grad_refusals(lib):  # noqa: F811
+    call = _caller(lib.moeq_add_rms_norm_grad, dict(
+        dt=0, dy=FAKE, dys=64, dh=FAKE, dhs=64, h=FAKE, hs=64, R=8, K=64, w=FAKE, u=FAKE, dx=FAKE,
+        dw=FAKE, ws=FAKE, st=None))
+    assert call(dt=3) == BAD and call(R=-1) == BAD and call(K=0) == BAD and call(K=60) == BAD
+    for p in ("dy", "dh", "h", "w", "u", "dx", "dw", "ws"):
+        assert call(**{p: ODD}) == BAD
+    for p in ("dy", "h", "w", "u", "dx", "ws"):
+        assert call(**{p: None}) == BAD
+    for p in ("dys", "dhs", "hs"):
+        assert call(**{p: 56}) == BAD and call(**{p: 68}) == BAD
+    assert call(K=16392, dys=16392, dhs=16392, hs=16392) == UNSUPPORTED
+    assert call(R=0, dw=None, dy=None, h=None, w=None, u=None, dx=None, ws=None) == OK
+    size = lib.moeq_add_rms_norm_grad_workspace
+    assert size(-1, 64) == -1 and size(8, 60) == -1 and size(8, 1 << 20) == -1
+    assert size(0, 64) == 0 and size(1, 4096) == 4096 * 4 and size(1 << 30, 4096) == 304 * 4096 * 4
+
+
+def test_norm_binding_refuses_host_tensors():
+    x = torch.zeros(4, 64)
+    with pytest.raises(ValueError):
+        moeq.add_rms_norm(x, x[0], y=x)
+    with pytest.raises(ValueError):
+        moeq.add_rms_norm_grad(x, x, x[0], x[:, 0], x)
