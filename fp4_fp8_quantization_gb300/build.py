@@ -15,7 +15,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoeq.so")
 SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "layout.cu", "route.cu", "gate.cu", "gate_group.cu",
-           "rows.cu", "norm.cu", "fp8_block.cu", "gemm_fp8_block.cu"]
+           "rows.cu", "norm.cu", "fp8_block.cu", "gemm_fp8_block.cu",
+           "epilogue_grad.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-fmad=false", "-Xcompiler", "-fPIC",

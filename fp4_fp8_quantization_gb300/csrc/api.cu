@@ -879,6 +879,32 @@ moeq_status moeq_add_rms_norm_grad(moeq_dtype dtype, const void *d_y, int64_t d_
     return cuda_status(moeq::launch_norm_grad(a, stream));
 }
 
+static moeq_status matmul_fp8_block_call(moeq::GemmBlockArgs ga, const uint32_t *a_offsets,
+                                         const int32_t *expert_ids, int64_t total_tokens,
+                                         int32_t num_experts, int32_t num_active_experts,
+                                         moeq_stream_t stream) {
+    const int64_t N = ga.N, K = ga.K;
+    if (!groups_ok(a_offsets, expert_ids, num_experts, num_active_experts))
+        return MOEQ_ERR_INVALID_ARG;
+    if (total_tokens < 0 || N <= 0 || K <= 0 || K % 16 || N % 8) return MOEQ_ERR_INVALID_ARG;
+    if (total_tokens >= (int64_t)1 << 31 || N >= (int64_t)1 << 31 || K >= (int64_t)1 << 31 ||
+        num_active_experts > moeq::kMaxGroups)
+        return MOEQ_ERR_UNSUPPORTED;
+    if (!ga.b || !ga.b_scales || !aligned16(ga.b) || !aligned16(ga.b_scales) ||
+        !aligned16(ga.bias))
+        return MOEQ_ERR_INVALID_ARG;
+    if (num_active_experts == 0 || total_tokens == 0) return MOEQ_OK;
+    if (!ga.c || !ga.a || !ga.a_scales || !aligned16(ga.c) || !aligned16(ga.a) ||
+        !aligned16(ga.a_scales) || !aligned16(ga.residual) || !aligned16(ga.z))
+        return MOEQ_ERR_INVALID_ARG;
+    uint32_t *err = device_error_ptr();
+    if (!err) return cuda_status(cudaErrorInvalidDevice);
+    ga.groups = make_groups(a_offsets, nullptr, expert_ids, num_active_experts, num_experts,
+                            total_tokens, 0);
+    ga.err = err;
+    return cuda_status(moeq::launch_gemm_fp8_block(ga, stream));
+}
+
 moeq_status moeq_grouped_matmul_fp8_block(void *c, const uint8_t *a, const uint8_t *b,
                                           const float *a_scales, const float *b_scales,
                                           const uint32_t *a_offsets, const int32_t *expert_ids,
@@ -886,21 +912,7 @@ moeq_status moeq_grouped_matmul_fp8_block(void *c, const uint8_t *a, const uint8
                                           int32_t num_experts, int32_t max_tokens_per_expert,
                                           int32_t num_active_experts, moeq_stream_t stream) {
     (void)max_tokens_per_expert;
-    if (!groups_ok(a_offsets, expert_ids, num_experts, num_active_experts))
-        return MOEQ_ERR_INVALID_ARG;
-    if (total_tokens < 0 || N <= 0 || K <= 0 || K % 16 || N % 8) return MOEQ_ERR_INVALID_ARG;
-    if (total_tokens >= (int64_t)1 << 31 || N >= (int64_t)1 << 31 || K >= (int64_t)1 << 31 ||
-        num_active_experts > moeq::kMaxGroups)
-        return MOEQ_ERR_UNSUPPORTED;
-    if (!b || !b_scales || !aligned16(b) || !aligned16(b_scales)) return MOEQ_ERR_INVALID_ARG;
-    if (num_active_experts == 0 || total_tokens == 0) return MOEQ_OK;
-    if (!c || !a || !a_scales || !aligned16(c) || !aligned16(a) || !aligned16(a_scales))
-        return MOEQ_ERR_INVALID_ARG;
-    uint32_t *err = device_error_ptr();
-    if (!err) return cuda_status(cudaErrorInvalidDevice);
     moeq::GemmBlockArgs ga = {};
-    ga.groups = make_groups(a_offsets, nullptr, expert_ids, num_active_experts, num_experts,
-                            total_tokens, 0);
     ga.N = N;
     ga.K = K;
     ga.a = a;
@@ -908,8 +920,88 @@ moeq_status moeq_grouped_matmul_fp8_block(void *c, const uint8_t *a, const uint8
     ga.a_scales = a_scales;
     ga.b_scales = b_scales;
     ga.c = c;
-    ga.err = err;
-    return cuda_status(moeq::launch_gemm_fp8_block(ga, stream));
+    return matmul_fp8_block_call(ga, a_offsets, expert_ids, total_tokens, num_experts,
+                                 num_active_experts, stream);
+}
+
+static bool activation_ok(int act) { return act >= MOEQ_ACT_NONE && act <= MOEQ_ACT_GELU_TANH; }
+
+moeq_status moeq_grouped_matmul_fp8_block_epilogue(
+    void *c, const uint8_t *a, const uint8_t *b, const float *a_scales, const float *b_scales,
+    const float *bias, moeq_activation activation, const void *residual, void *z,
+    const uint32_t *a_offsets, const int32_t *expert_ids, int64_t total_tokens, int64_t N,
+    int64_t K, int32_t num_experts, int32_t max_tokens_per_expert, int32_t num_active_experts,
+    moeq_stream_t stream) {
+    (void)max_tokens_per_expert;
+    if (!activation_ok(activation)) return MOEQ_ERR_INVALID_ARG;
+    if (z && (z == c || z == residual)) return MOEQ_ERR_INVALID_ARG;
+    moeq::GemmBlockArgs ga = {};
+    ga.N = N;
+    ga.K = K;
+    ga.a = a;
+    ga.b = b;
+    ga.a_scales = a_scales;
+    ga.b_scales = b_scales;
+    ga.c = c;
+    ga.bias = bias;
+    ga.act = activation;
+    ga.residual = residual;
+    ga.z = z;
+    return matmul_fp8_block_call(ga, a_offsets, expert_ids, total_tokens, num_experts,
+                                 num_active_experts, stream);
+}
+
+static moeq_status epilogue_grad_sizes_ok(int64_t rows, int64_t N, int32_t groups) {
+    if (rows < 0 || N <= 0 || N % 8 || groups < 0) return MOEQ_ERR_INVALID_ARG;
+    if (rows >= (int64_t)1 << 31 || N >= (int64_t)1 << 31 || groups > moeq::kMaxGroups)
+        return MOEQ_ERR_UNSUPPORTED;
+    return MOEQ_OK;
+}
+
+int64_t moeq_grouped_epilogue_grad_workspace(int64_t total_tokens, int64_t N,
+                                             int32_t num_active_experts) {
+    if (epilogue_grad_sizes_ok(total_tokens, N, num_active_experts) != MOEQ_OK) return -1;
+    return moeq::epilogue_grad_table_bytes(num_active_experts) +
+           moeq::epilogue_grad_tiles(total_tokens, num_active_experts) * N * 4;
+}
+
+moeq_status moeq_grouped_epilogue_grad(const void *d_c, int64_t d_c_stride, const void *z,
+                                       moeq_activation activation, uint8_t *q, float *scales,
+                                       void *d_z, float *d_bias, const uint32_t *a_offsets,
+                                       const int32_t *expert_ids, int64_t total_tokens, int64_t N,
+                                       int32_t num_experts, int32_t num_active_experts,
+                                       void *workspace, moeq_stream_t stream) {
+    if (!groups_ok(a_offsets, expert_ids, num_experts, num_active_experts) ||
+        !activation_ok(activation))
+        return MOEQ_ERR_INVALID_ARG;
+    const moeq_status st = epilogue_grad_sizes_ok(total_tokens, N, num_active_experts);
+    if (st != MOEQ_OK) return st;
+    if (num_experts > 65535) return MOEQ_ERR_UNSUPPORTED;
+    if (!aligned16(d_bias) || !aligned16(workspace) || (d_bias && !workspace))
+        return MOEQ_ERR_INVALID_ARG;
+    const bool work = total_tokens > 0 && num_active_experts > 0;
+    if (work && (!d_c || !aligned16(d_c) || d_c_stride < N || d_c_stride % 8 || !aligned16(z) ||
+                 !z != (activation == MOEQ_ACT_NONE) || !aligned16(q) || !aligned16(scales) ||
+                 !q != !scales || (q && N % 16) || !aligned16(d_z) || (!q && !d_z && !d_bias)))
+        return MOEQ_ERR_INVALID_ARG;
+    if (!work && !d_bias) return MOEQ_OK;
+    uint32_t *err = device_error_ptr();
+    if (!err) return cuda_status(cudaErrorInvalidDevice);
+    moeq::EpilogueGradArgs g = {};
+    g.groups = make_groups(a_offsets, nullptr, expert_ids, num_active_experts, num_experts,
+                           total_tokens, 0);
+    g.N = N;
+    g.dc = d_c;
+    g.z = z;
+    g.dc_stride = d_c_stride;
+    g.act = activation;
+    g.q = q;
+    g.scales = scales;
+    g.dz = d_z;
+    g.d_bias = d_bias;
+    g.workspace = workspace;
+    g.err = err;
+    return cuda_status(moeq::launch_epilogue_grad(g, stream));
 }
 
 }  // extern "C"

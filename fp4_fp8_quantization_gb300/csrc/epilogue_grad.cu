@@ -1,0 +1,243 @@
+// Gradient of the block product's epilogue c = act(z) + residual, z = product +
+// bias[e], over ragged groups:
+//
+//   d_z = d_c act'(z)   as E4M3 codes with a scale for each 1 x 128 block, ready for
+//                       the product with the transposed weights, and / or as bf16
+//   d_bias[e] = sum over the rows of expert e of d_z (fp32, before any rounding)
+//
+// One pass: 4 bytes read and 1 (or 3) written per element.  A CTA takes tiles of
+// kRows rows of one group by 256 columns, a warp a row at a time, 16 lanes a
+// block; each thread sums its 8 columns over its rows, the warps join in shared
+// memory, and a tile leaves one row of partial sums.  A second kernel adds an
+// expert's rows of them in the order of groups and tiles: no atomics, the same
+// bits every time.
+#include <algorithm>
+
+#include "activation.cuh"
+#include "common.cuh"
+#include "fp8_block.cuh"
+#include "launch.h"
+#include "tensormap.h"
+
+namespace moeq {
+
+namespace {
+
+constexpr int kRows = kEpilogueGradRows;
+constexpr int kWarps = 8;
+constexpr int kCols = 256;  // of a CTA: 32 lanes of 8
+
+struct EpilogueGradParams {
+    const uint16_t *dc, *z;
+    int64_t dc_stride, rows, N;
+    int act;
+    const uint32_t *offsets;
+    const int32_t *expert_ids;
+    int num_groups, num_experts;
+    uint8_t *q;
+    float *scales;
+    uint16_t *dz;
+    float *part;       // [tiles][N], or null
+    uint32_t *tiles;   // [groups + 1] tiles before each group, with part
+    int64_t max_tiles;
+    uint32_t *err;
+};
+
+__global__ void __launch_bounds__(kWarps * 32) epilogue_grad_kernel(EpilogueGradParams p) {
+    // tiles before each group
+    __shared__ uint32_t prefix[kMaxGroups + 1];
+    __shared__ float sums[kWarps][kCols];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.num_groups;
+    const bool first = blockIdx.x == 0 && blockIdx.y == 0;
+    for (int g = threadIdx.x; g < G; g += blockDim.x) {
+        const uint32_t r0 = __ldg(p.offsets + g), r1 = __ldg(p.offsets + g + 1);
+        const int e = __ldg(p.expert_ids + g);
+        uint32_t n = 0;
+        if (r1 < r0 || (int64_t)r1 > p.rows) {
+            if (first) set_error(p.err, MOEQ_DEVERR_BAD_OFFSETS);
+        } else if (e < 0 || e >= p.num_experts) {
+            if (first) set_error(p.err, MOEQ_DEVERR_BAD_EXPERT);
+        } else {
+            n = (r1 - r0 + kRows - 1) / kRows;
+        }
+        prefix[g + 1] = n;
+    }
+    if (threadIdx.x == 0) prefix[0] = 0;
+    __syncthreads();
+    if (warp == 0) {  // inclusive prefix over prefix[1 .. G]
+        uint32_t carry = 0;
+        for (int base = 0; base < G; base += 32) {
+            const int g = base + lane;
+            uint32_t v = g < G ? prefix[g + 1] : 0u;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t t = __shfl_up_sync(0xFFFFFFFFu, v, o);
+                if (lane >= o) v += t;
+            }
+            if (g < G) prefix[g + 1] = carry + v;
+            carry += __shfl_sync(0xFFFFFFFFu, v, 31);
+        }
+    }
+    __syncthreads();
+    if (first && p.part)
+        for (int g = threadIdx.x; g <= G; g += blockDim.x) {
+            uint32_t *o = p.tiles + g;
+            if (store_fits(o, 4, p.tiles, (int64_t)(G + 1) * 4, p.err)) *o = prefix[g];
+        }
+    // groups that overlap can have more tiles than the workspace has rows
+    uint32_t total = prefix[G];
+    if ((int64_t)total > p.max_tiles) {
+        if (first && threadIdx.x == 0) set_error(p.err, MOEQ_DEVERR_BAD_OFFSETS);
+        total = (uint32_t)p.max_tiles;
+    }
+    const int64_t n = (int64_t)blockIdx.x * kCols + lane * 8, NB = (p.N + 127) / 128;
+    const bool in_n = n < p.N;
+    const float c1 = sigma_c1(p.act), c3 = sigma_c3(p.act);
+    for (uint32_t t = blockIdx.y; t < total; t += gridDim.y) {
+        int lo = 0, hi = G;  // the last group that begins at or before tile t
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (prefix[mid] <= t) lo = mid; else hi = mid;
+        }
+        const int64_t r0 = (int64_t)__ldg(p.offsets + lo) + (int64_t)(t - prefix[lo]) * kRows;
+        const int rows = (int)min((int64_t)kRows, (int64_t)__ldg(p.offsets + lo + 1) - r0);
+        float sum[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+        constexpr int U = 4;  // rows of a warp whose loads are in flight together
+        for (int base = warp; base < rows; base += U * kWarps) {
+            uint4 dc[U], zv[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int64_t r = r0 + base + j * kWarps;
+                dc[j] = zv[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (base + j * kWarps < rows && in_n) {
+                    dc[j] = ld_stream(p.dc + r * p.dc_stride + n);
+                    if (p.z) zv[j] = ld_stream(p.z + r * p.N + n);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int64_t r = r0 + base + j * kWarps;
+                if (base + j * kWarps >= rows) break;
+                float x[8];
+                unpack8(dc[j], x);
+                if (p.z) {
+                    float z[8];
+                    unpack8(zv[j], z);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        x[i] = __fmul_rn(x[i], act_slope(z[i], p.act, c1, c3));
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[i] = __fadd_rn(sum[i], x[i]);
+                if (p.q) {
+                    float m = amax8(x);
+#pragma unroll
+                    for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                    const float s = block_scale(m);
+                    if (in_n) {
+                        uint8_t *out = p.q + r * p.N + n;
+                        float *scale = p.scales + r * NB + n / 128;
+                        if (store_fits(out, 8, p.q, p.rows * p.N, p.err))
+                            *reinterpret_cast<uint2 *>(out) = codes8(x, __fdiv_rn(1.0f, s));
+                        if ((lane & 15) == 0 &&
+                            store_fits(scale, 4, p.scales, p.rows * NB * 4, p.err))
+                            *scale = s;
+                    }
+                }
+                if (p.dz && in_n) {
+                    uint16_t *out = p.dz + r * p.N + n;
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        w[i] = f32_to_bf16_bits(x[2 * i]) | (f32_to_bf16_bits(x[2 * i + 1]) << 16);
+                    if (store_fits(out, 16, p.dz, p.rows * p.N * 2, p.err))
+                        st_global_v4(out, w[0], w[1], w[2], w[3]);
+                }
+            }
+        }
+        if (!p.part) continue;
+        __syncthreads();  // the sums of the tile before have been read
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sums[warp][lane * 8 + i] = sum[i];
+        __syncthreads();
+        const int64_t col = (int64_t)blockIdx.x * kCols + threadIdx.x;
+        float v = sums[0][threadIdx.x];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) v = __fadd_rn(v, sums[w][threadIdx.x]);
+        float *out = p.part + (int64_t)t * p.N + col;
+        if (col < p.N && store_fits(out, 4, p.part, p.max_tiles * p.N * 4, p.err)) *out = v;
+    }
+}
+
+// d_bias[e] from the tiles' sums: 32 columns a CTA, its warps take an expert's tiles
+// in turn and join.
+__global__ void __launch_bounds__(1024) bias_grad_kernel(const float *part, const uint32_t *tiles,
+                                                         int64_t max_tiles,
+                                                         const int32_t *expert_ids, int G,
+                                                         int64_t N, float *d_bias, int E,
+                                                         uint32_t *err) {
+    __shared__ float sums[32][33];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int64_t n = (int64_t)blockIdx.x * 32 + lane;
+    const int e = blockIdx.y;
+    float v = 0.0f;
+    for (int base = 0; base < G; base += 32) {
+        const int g = base + lane;
+        uint32_t mine = __ballot_sync(0xFFFFFFFFu, g < G && __ldg(expert_ids + g) == e);
+        for (; mine; mine &= mine - 1) {
+            const int at = base + __ffs((int)mine) - 1;
+            const int64_t t0 = __ldg(tiles + at), t1 = min((int64_t)__ldg(tiles + at + 1), max_tiles);
+            if (n < N) {
+#pragma unroll 4
+                for (int64_t t = t0 + warp; t < t1; t += warps)
+                    v = __fadd_rn(v, __ldg(part + t * N + n));
+            }
+        }
+    }
+    sums[warp][lane] = v;
+    __syncthreads();
+    if (warp == 0) {
+        for (int w = 1; w < warps; ++w) v = __fadd_rn(v, sums[w][lane]);
+        float *out = d_bias + (int64_t)e * N + n;
+        if (n < N && store_fits(out, 4, d_bias, (int64_t)E * N * 4, err)) *out = v;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_epilogue_grad(const EpilogueGradArgs &a, cudaStream_t s) {
+    const int64_t tiles = epilogue_grad_tiles(a.groups.total_rows, a.groups.num_groups);
+    // the sums' place: the table of tiles, then the sums, 16-byte aligned
+    uint32_t *table = static_cast<uint32_t *>(a.workspace);
+    float *part = a.d_bias ? reinterpret_cast<float *>(
+                                 static_cast<uint8_t *>(a.workspace) +
+                                 epilogue_grad_table_bytes(a.groups.num_groups))
+                           : nullptr;
+    const EpilogueGradParams p{static_cast<const uint16_t *>(a.dc),
+                               static_cast<const uint16_t *>(a.z), a.dc_stride,
+                               a.groups.total_rows, a.N, a.act, a.groups.row_offsets,
+                               a.groups.expert_ids, a.groups.num_groups, a.groups.num_experts, a.q,
+                               a.scales, static_cast<uint16_t *>(a.dz), part, table, tiles, a.err};
+    if (tiles > 0) {
+        const dim3 grid((unsigned)((a.N + kCols - 1) / kCols),
+                        (unsigned)std::min<int64_t>(tiles, 65535));
+        const cudaError_t e = launch_pdl(epilogue_grad_kernel, grid, kWarps * 32, 0, s, p);
+        if (e != cudaSuccess) return e;
+    }
+    if (!a.d_bias) return cudaSuccess;
+    // many warps where there are few CTAs
+    const int64_t cols = (a.N + 31) / 32, ctas = cols * a.groups.num_experts;
+    const unsigned threads = ctas < 4 * sm_count() ? 1024 : 256;
+    return launch_pdl(bias_grad_kernel, dim3((unsigned)cols, (unsigned)a.groups.num_experts),
+                      threads, 0, s, (const float *)part, (const uint32_t *)table, tiles,
+                      a.groups.expert_ids, tiles > 0 ? a.groups.num_groups : 0, a.N, a.d_bias,
+                      a.groups.num_experts, a.err);
+}
+
+}  // namespace moeq

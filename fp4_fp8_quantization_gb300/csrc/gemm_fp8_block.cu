@@ -47,6 +47,7 @@
 // 96 (one token, 8 experts, N 1536) 13.8 -> 18.8.
 #include <algorithm>
 
+#include "activation.cuh"
 #include "common.cuh"
 #include "launch.h"
 #include "tensormap.h"
@@ -110,6 +111,11 @@ struct BlockGemmParams {
     const float *a_scales, *b_scales;
     uint16_t *c;
     uint32_t *err;
+    // the epilogue's
+    const float *bias;
+    const uint16_t *residual;
+    uint16_t *z;
+    int act;
 };
 
 // A value that every lane of the (converged) warp holds, in a form the
@@ -125,6 +131,37 @@ __device__ __forceinline__ uint32_t bf16x2(F2 v) {
     return b;
 }
 
+__device__ __forceinline__ F2 bf16x2_values(uint32_t w) {
+    return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// A load that may see an earlier tile's store (c over the residual).
+__device__ __forceinline__ uint4 ld_global_v4(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
+// The activation of 32 values.
+__device__ __forceinline__ void activate16(F2 *v, int act) {
+    if (act == MOEQ_ACT_NONE) return;
+    if (act == MOEQ_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = f2(act_relu(f2_lo(v[i])), act_relu(f2_hi(v[i])));
+    } else if (act == MOEQ_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = f2(act_gelu(f2_lo(v[i])), act_gelu(f2_hi(v[i])));
+    } else {
+        const float c1 = sigma_c1(act), c3 = sigma_c3(act);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            v[i] = f2(act_sigma(f2_lo(v[i]), c1, c3), act_sigma(f2_hi(v[i]), c1, c3));
+    }
+}
+
 // Waits for the thread's tensor-memory loads; r is written by them.
 __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -136,7 +173,8 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
                    "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
-template <class C>
+// EPI: z = sum + bias[e], c = bf16(act(z) + residual), z stored too where asked.
+template <class C, bool EPI>
 __global__ void __launch_bounds__(C::THREADS, 1)
     gemm_fp8_block_kernel(const __grid_constant__ CUtensorMap tmA,
                           const __grid_constant__ CUtensorMap tmA32,
@@ -340,7 +378,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // the last row takes that row's, its sums are dropped)
         struct Part {
             int row, nvalid, ncol;
-            const float *sa, *sb;
+            const float *sa, *sb, *bias;
             __device__ bool work(int N) const { return nvalid > 0 && ncol < N; }
         };
         auto part_of = [&](uint32_t t) {
@@ -352,6 +390,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             w.ncol = tl.nb * C::BN + cgrp * C::COLS_W;
             w.sa = p.a_scales + (int64_t)(w.row + max(0, min(lane, w.nvalid - 1))) * KB;
             w.sb = p.b_scales + ((int64_t)e * NBLK + min(w.ncol / 128, NBLK - 1)) * KB;
+            w.bias = EPI && p.bias ? p.bias + (int64_t)e * p.N : nullptr;
             return w;
         };
         // each lane polls by itself: where the barrier completes while another
@@ -508,29 +547,86 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             // whose 16-byte pieces are XOR-swizzled by row pair, free of bank
             // conflicts), stored with four lanes per row
             const int k = lane & 3, lrow = lane >> 2;
-            uint16_t *out = p.c + (int64_t)(cur.row + lrow) * p.N + cur.ncol + k * 8;
+            const int64_t at = (int64_t)(cur.row + lrow) * p.N + cur.ncol + k * 8;
+            auto own = [&](int j) {  // piece j of the lane's own row
+                return sbuf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4);
+            };
+            auto stage = [&](const F2 *v) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    st_shared_v4(own(j), bf16x2(v[4 * j]), bf16x2(v[4 * j + 1]),
+                                 bf16x2(v[4 * j + 2]), bf16x2(v[4 * j + 3]));
+            };
+            auto piece = [&](int i) {  // of row lrow + 8 i
+                const int rr = lrow + 8 * i;
+                return sbuf + rr * 64 + ((k ^ ((rr >> 1) & 3)) << 4);
+            };
+            auto store = [&](uint16_t *base, int ch, bool in_n) {
+                uint16_t *out = base + at + ch * 32;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 v = ld_shared_v4(piece(i));
+                    uint16_t *o = out + (int64_t)(8 * i) * p.N;
+                    if (lrow + 8 * i < cur.nvalid && in_n &&
+                        store_fits(o, 16, base, p.total_rows * p.N * 2, p.err))
+                        st_global_v4(o, v.x, v.y, v.z, v.w);
+                }
+            };
 #pragma unroll
             for (int ch = 0; ch < C::CHUNKS_W; ++ch) {
                 const int nc = cur.ncol + ch * 32;
                 if (nc >= p.N) break;
-                __syncwarp();  // the last chunk has been read
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const F2 *v = acc + ch * 16 + j * 4;
-                    st_shared_v4(sbuf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), bf16x2(v[0]),
-                                 bf16x2(v[1]), bf16x2(v[2]), bf16x2(v[3]));
-                }
-                __syncwarp();
                 const bool in_n = nc + k * 8 < p.N;  // N is a multiple of 8
+                F2 *v = acc + ch * 16;
+                if constexpr (EPI) {
+                    // the residual's loads are in flight during the activation
+                    uint4 res[4];
+                    if (p.residual) {
+                        const uint16_t *src = p.residual + at + ch * 32;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int rr = lrow + 8 * i;
-                    const uint4 v = ld_shared_v4(sbuf + rr * 64 + ((k ^ ((rr >> 1) & 3)) << 4));
-                    uint16_t *o = out + (int64_t)(8 * i) * p.N + ch * 32;
-                    if (rr < cur.nvalid && in_n &&
-                        store_fits(o, 16, p.c, p.total_rows * p.N * 2, p.err))
-                        st_global_v4(o, v.x, v.y, v.z, v.w);
+                        for (int i = 0; i < 4; ++i) {
+                            res[i] = make_uint4(0u, 0u, 0u, 0u);
+                            if (lrow + 8 * i < cur.nvalid && in_n)
+                                res[i] = ld_global_v4(src + (int64_t)(8 * i) * p.N);
+                        }
+                    }
+                    if (cur.bias) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (nc + 4 * j < p.N) {
+                                const float4 b =
+                                    __ldg(reinterpret_cast<const float4 *>(cur.bias + nc) + j);
+                                v[2 * j] = add2(v[2 * j], f2(b.x, b.y));
+                                v[2 * j + 1] = add2(v[2 * j + 1], f2(b.z, b.w));
+                            }
+                    }
+                    if (p.z) {
+                        __syncwarp();  // the last chunk has been read
+                        stage(v);
+                        __syncwarp();
+                        store(p.z, ch, in_n);
+                    }
+                    activate16(v, p.act);
+                    if (p.residual) {
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            st_shared_v4(piece(i), res[i].x, res[i].y, res[i].z, res[i].w);
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint4 w = ld_shared_v4(own(j));
+                            v[4 * j] = add2(v[4 * j], bf16x2_values(w.x));
+                            v[4 * j + 1] = add2(v[4 * j + 1], bf16x2_values(w.y));
+                            v[4 * j + 2] = add2(v[4 * j + 2], bf16x2_values(w.z));
+                            v[4 * j + 3] = add2(v[4 * j + 3], bf16x2_values(w.w));
+                        }
+                    }
                 }
+                __syncwarp();  // the last chunk has been read
+                stage(v);
+                __syncwarp();
+                store(p.c, ch, in_n);
             }
         }
         if (C::ASYNC && lane == 0) bulk_wait_all();
@@ -556,7 +652,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
 }
 
-template <class C>
+template <class C, bool EPI = false>
 cudaError_t run_block_gemm(const GemmBlockArgs &a, cudaStream_t s) {
     const int64_t T = a.groups.total_rows;
     // the whole-block map of A is of the 128-row tiles, the output's of the
@@ -587,8 +683,10 @@ cudaError_t run_block_gemm(const GemmBlockArgs &a, cudaStream_t s) {
         return cudaErrorInvalidValue;
     const BlockGemmParams p{a.groups.row_offsets, a.groups.expert_ids, a.groups.num_groups,
                             a.groups.num_experts, T, (int)a.N, (int)a.K, a.a_scales, a.b_scales,
-                            static_cast<uint16_t *>(a.c), a.err};
-    auto kern = gemm_fp8_block_kernel<C>;
+                            static_cast<uint16_t *>(a.c), a.err, a.bias,
+                            static_cast<const uint16_t *>(a.residual),
+                            static_cast<uint16_t *>(a.z), a.act};
+    auto kern = gemm_fp8_block_kernel<C, EPI>;
     static std::atomic<int> attr_done[kMaxDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -655,9 +753,14 @@ cudaError_t launch_gemm_fp8_block(const GemmBlockArgs &a, cudaStream_t s) {
 #ifdef MOEQ_FP8_BLOCK_TILE
     tile = MOEQ_FP8_BLOCK_TILE;  // test builds: one form for every size
 #endif
-    if (tile == kSmallTile) return run_block_gemm<BlockCfg<64, 128, 4, 8, false, 2>>(a, s);
+    using Small = BlockCfg<64, 128, 4, 8, false, 2>;
+    using Large = BlockCfg<128, 256, 4, 8, false, 1>;
+    if (a.bias || a.act != MOEQ_ACT_NONE || a.residual || a.z)
+        return tile == kSmallTile ? run_block_gemm<Small, true>(a, s)
+                                  : run_block_gemm<Large, true>(a, s);
+    if (tile == kSmallTile) return run_block_gemm<Small>(a, s);
     if (tile == kLargeTileByTensor) return run_block_gemm<BlockCfg<128, 256, 3, 8, true, 1>>(a, s);
-    return run_block_gemm<BlockCfg<128, 256, 4, 8, false, 1>>(a, s);
+    return run_block_gemm<Large>(a, s);
 }
 
 }  // namespace moeq

@@ -131,8 +131,36 @@ struct GemmBlockArgs {
     const float *a_scales, *b_scales;
     void *c;
     uint32_t *err;
+    // the epilogue (moeq_activation; null: none of it)
+    const float *bias;
+    int act;
+    const void *residual;
+    void *z;
 };
 cudaError_t launch_gemm_fp8_block(const GemmBlockArgs &a, cudaStream_t s);
+
+// Gradient of that epilogue.
+struct EpilogueGradArgs {
+    GroupArgs groups;
+    int64_t N;
+    const void *dc, *z;
+    int64_t dc_stride;
+    int act;
+    uint8_t *q;
+    float *scales;
+    void *dz;
+    float *d_bias;
+    void *workspace;
+    uint32_t *err;
+};
+cudaError_t launch_epilogue_grad(const EpilogueGradArgs &a, cudaStream_t s);
+// Its workspace: a table of tiles for each group, then one row of N sums for each
+// tile of kEpilogueGradRows rows of a group.
+constexpr int kEpilogueGradRows = 128;
+inline int64_t epilogue_grad_tiles(int64_t rows, int64_t groups) {
+    return rows && groups ? rows / kEpilogueGradRows + (groups < rows ? groups : rows) : 0;
+}
+inline int64_t epilogue_grad_table_bytes(int64_t groups) { return (groups + 4) / 4 * 16; }
 
 // Tokens to rows (spread) or rows to tokens, and the dots of the weights'
 // gradient where d_weights is given.  Sizes and strides in elements.

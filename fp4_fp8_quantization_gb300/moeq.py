@@ -22,6 +22,7 @@ _lib = None
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # moeq_dtype
 SCORES = {"softmax": 0, "sigmoid": 1}                              # moeq_score
 GROUP_SCORES = {"max": 0, "top2": 1}                               # moeq_group_score
+ACTIVATIONS = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}   # moeq_activation
 FORMATS = {"nvfp4": 0, "mxfp4": 1, "mxfp8": 2}
 STATUS = {0: "MOEQ_OK", 1: "MOEQ_ERR_INVALID_ARG", 2: "MOEQ_ERR_UNSUPPORTED",
           3: "MOEQ_ERR_CUDA", 4: "MOEQ_ERR_DEVICE"}
@@ -81,6 +82,11 @@ _SIGNATURES = {
                                _P],
     "moeq_grouped_matmul_fp8_block": [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32,
                                       _I32, _P],
+    "moeq_grouped_matmul_fp8_block_epilogue": [_P, _P, _P, _P, _P, _P, _I32, _P, _P, _P, _P, _I64,
+                                               _I64, _I64, _I32, _I32, _I32, _P],
+    "moeq_grouped_epilogue_grad": [_P, _I64, _P, _I32, _P, _P, _P, _P, _P, _P, _I64, _I64, _I32,
+                                   _I32, _P, _P],
+    "moeq_grouped_epilogue_grad_workspace": [_I64, _I64, _I32],
     "moeq_get_device_error": [_P, _U32P],
     "moeq_clear_device_error": [_P],
     "moeq_last_cuda_error": [],
@@ -111,6 +117,7 @@ def lib():
         L.moeq_status_string.restype = ctypes.c_char_p
         L.moeq_dispatch_scale_rows.restype = ctypes.c_int64
         L.moeq_add_rms_norm_grad_workspace.restype = ctypes.c_int64
+        L.moeq_grouped_epilogue_grad_workspace.restype = ctypes.c_int64
         _lib = L
     return _lib
 
@@ -741,6 +748,68 @@ def grouped_matmul_fp8_block(c, a, b, a_scales, b_scales, a_offsets, expert_ids,
                   "b_scales"),
           _ptr(a_offsets, _U32, "a_offsets"), _ptr(expert_ids, torch.int32, "expert_ids"), T, N, K,
           E, max_tokens_per_expert, G, _stream(stream))
+
+
+def grouped_matmul_fp8_block_epilogue(c, a, b, a_scales, b_scales, a_offsets, expert_ids,
+                                      bias=None, activation=None, residual=None, z=None,
+                                      max_tokens_per_expert=0, num_active_experts=None,
+                                      stream=None):
+    """grouped_matmul_fp8_block with an epilogue: c = act(product + bias of the
+    row's expert) + residual, rounded once.  bias fp32 [E, N]; activation None,
+    "relu", "silu", "gelu" or "gelu_tanh"; residual bf16 [rows, N] (may be c
+    itself); z (out, bf16 [rows, N]) is the product with bias, for the gradient."""
+    G = expert_ids.numel() if num_active_experts is None else num_active_experts
+    E, N, K = b.shape
+    if expert_ids.numel() < G or a_offsets.numel() < G + 1:
+        raise ValueError(f"a_offsets, expert_ids: too short for {G} groups")
+    T = a.shape[0]
+    bf16, f32 = torch.bfloat16, torch.float32
+    args = (_shaped(c, (T, N), bf16, "c"), _shaped(a, (T, K), _U8, "a"), _ptr(b, _U8, "b"),
+            _shaped(a_scales, (T, _blocks128(K)), f32, "a_scales"),
+            _shaped(b_scales, (E, _blocks128(N), _blocks128(K)), f32, "b_scales"),
+            _shaped(bias, (E, N), f32, "bias", True),
+            _one_of(ACTIVATIONS, activation, "activation"),
+            _shaped(residual, (T, N), bf16, "residual", True), _shaped(z, (T, N), bf16, "z", True),
+            _ptr(a_offsets, _U32, "a_offsets"), _ptr(expert_ids, torch.int32, "expert_ids"))
+    _on_current_device(c, a, b, a_scales, b_scales, a_offsets, expert_ids, bias, residual, z)
+    _call("moeq_grouped_matmul_fp8_block_epilogue", *args, T, N, K, E, max_tokens_per_expert, G,
+          _stream(stream))
+
+
+def grouped_epilogue_grad_workspace(rows, N, num_active_experts):
+    """Bytes of the workspace that grouped_epilogue_grad takes for d_bias."""
+    return lib().moeq_grouped_epilogue_grad_workspace(rows, N, num_active_experts)
+
+
+def grouped_epilogue_grad(d_c, a_offsets, expert_ids, num_experts, z=None, activation=None, q=None,
+                          scales=None, d_z=None, d_bias=None, workspace=None,
+                          num_active_experts=None, stream=None):
+    """Gradient of grouped_matmul_fp8_block_epilogue's epilogue: d_z = d_c *
+    act'(z) as q (out, uint8 / float8_e4m3fn [rows, N]) with scales (out, fp32
+    [rows, ceil(N / 128)]) and / or as d_z (out, bf16), and d_bias (out, fp32
+    [num_experts, N]), its sums over each expert's rows.  d_c bf16 [rows, N]; z
+    as the forward call saved it, with an activation.  workspace:
+    grouped_epilogue_grad_workspace(rows, N, groups) bytes, needed with d_bias;
+    without one it is allocated, on the current stream (so give it with another)."""
+    G = expert_ids.numel() if num_active_experts is None else num_active_experts
+    if expert_ids.numel() < G or a_offsets.numel() < G + 1:
+        raise ValueError(f"a_offsets, expert_ids: too short for {G} groups")
+    p = _rows_of(d_c, "d_c", dtype=torch.bfloat16)
+    T, N = d_c.shape
+    bf16, f32 = torch.bfloat16, torch.float32
+    args = (p, _row_stride(d_c), _shaped(z, (T, N), bf16, "z", True),
+            _one_of(ACTIVATIONS, activation, "activation"), _shaped(q, (T, N), _U8, "q", True),
+            _shaped(scales, (T, _blocks128(N)), f32, "scales", True),
+            _shaped(d_z, (T, N), bf16, "d_z", True),
+            _shaped(d_bias, (num_experts, N), f32, "d_bias", True),
+            _ptr(a_offsets, _U32, "a_offsets"), _ptr(expert_ids, torch.int32, "expert_ids"))
+    ws = None
+    if d_bias is not None:
+        if workspace is None and stream is not None:
+            raise ValueError("workspace: required with a stream")
+        workspace, ws = _workspace(workspace, grouped_epilogue_grad_workspace(T, N, G), d_c)
+    _on_current_device(d_c, a_offsets, expert_ids, z, q, scales, d_z, d_bias, workspace)
+    _call("moeq_grouped_epilogue_grad", *args, T, N, num_experts, G, ws, _stream(stream))
 
 
 def get_device_error(stream=None):

@@ -677,6 +677,57 @@ moeq_status moeq_grouped_matmul_fp8_block(void *c, const uint8_t *a, const uint8
                                           int32_t num_experts, int32_t max_tokens_per_expert,
                                           int32_t num_active_experts, moeq_stream_t stream);
 
+/* The same product with an epilogue:
+ *   z[t, n] = sum (as above, fp32) + bias[e, n],  c[t, n] = bf16(act(z) + residual[t, n])
+ * fp32 up to the one rounding, act one of
+ *   relu max(z, 0);  silu z sigma(z);  gelu z Phi(z), Phi the normal distribution within
+ *   2^-23;  gelu_tanh z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3)))
+ *   bias        fp32 [num_experts, N] or NULL.
+ *   residual    bf16 [total_tokens, N] or NULL; may be c itself.
+ *   z           bf16 [total_tokens, N] (out) or NULL: z rounded, for the gradient; c is
+ *               computed from fp32 z.  No other output or input of the call.
+ * Rows outside the groups are not written.  One group of all rows and one expert make it a
+ * plain product; the other arguments are as above. */
+typedef enum {
+    MOEQ_ACT_NONE = 0,
+    MOEQ_ACT_RELU = 1,
+    MOEQ_ACT_SILU = 2,
+    MOEQ_ACT_GELU = 3,
+    MOEQ_ACT_GELU_TANH = 4
+} moeq_activation;
+moeq_status moeq_grouped_matmul_fp8_block_epilogue(
+    void *c, const uint8_t *a, const uint8_t *b, const float *a_scales, const float *b_scales,
+    const float *bias, moeq_activation activation, const void *residual, void *z,
+    const uint32_t *a_offsets, const int32_t *expert_ids, int64_t total_tokens, int64_t N,
+    int64_t K, int32_t num_experts, int32_t max_tokens_per_expert, int32_t num_active_experts,
+    moeq_stream_t stream);
+
+/* Gradient of that epilogue, from d_c and the saved z:
+ *   d_z = d_c * act'(z);  d_bias[e] = sum over the rows of e's groups of d_z
+ * fp32; d_z leaves as E4M3 codes q with a scale per 1 x 128 block (the rule of
+ * moeq_quantize_fp8_block, from fp32; the operand of the activations' gradient, above) and
+ * / or as bf16 d_z (for the weights'); the residual's gradient is d_c itself.  The bias's
+ * sums run in an order that the groups give: the same bits every time.
+ *   d_c         bf16 [total_tokens, N], row stride d_c_stride elements (a multiple of 8).
+ *   z           bf16 [total_tokens, N]; NULL with MOEQ_ACT_NONE and only then.
+ *   q           E4M3 [total_tokens, N] (out) and scales fp32 [total_tokens,
+ *               ceil(N / 128)] (out), or both NULL;  d_z bf16 [total_tokens, N] (out) or NULL.
+ *   d_bias      fp32 [num_experts, N] (out) or NULL; an expert without rows gets 0.  With
+ *               it, workspace: device memory of moeq_grouped_epilogue_grad_workspace(...)
+ *               bytes that no other call in flight uses.
+ * Rows outside the groups are not written and not summed.  N % 8 == 0, with q N % 16 == 0;
+ * num_experts <= 65535 (else MOEQ_ERR_UNSUPPORTED). */
+moeq_status moeq_grouped_epilogue_grad(const void *d_c, int64_t d_c_stride, const void *z,
+                                       moeq_activation activation, uint8_t *q, float *scales,
+                                       void *d_z, float *d_bias, const uint32_t *a_offsets,
+                                       const int32_t *expert_ids, int64_t total_tokens, int64_t N,
+                                       int32_t num_experts, int32_t num_active_experts,
+                                       void *workspace, moeq_stream_t stream);
+
+/* Bytes of that workspace (-1: sizes that the call refuses).  Host only. */
+int64_t moeq_grouped_epilogue_grad_workspace(int64_t total_tokens, int64_t N,
+                                             int32_t num_active_experts);
+
 /* Reads the sticky device error word of the current device (MOEQ_DEVERR_*
  * bits) after synchronising `stream`.  Returns MOEQ_ERR_DEVICE when any bit
  * is set, MOEQ_OK otherwise. */

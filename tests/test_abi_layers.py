@@ -91,3 +91,48 @@ def test_norm_binding_refuses_host_tensors():
         moeq.add_rms_norm(x, x[0], y=x)
     with pytest.raises(ValueError):
         moeq.add_rms_norm_grad(x, x, x[0], x[:, 0], x)
+
+
+def test_epilogue_gemm_refusals(lib):  # noqa: F811
+    call = _caller(lib.moeq_grouped_matmul_fp8_block_epilogue, dict(
+        c=FAKE, a=FAKE, b=FAKE, sa=FAKE, sb=FAKE, bias=FAKE, act=2, res=FAKE, z=0x20000, ro=FAKE,
+        ids=FAKE, T=64, N=72, K=144, E=2, mt=8, G=2, st=None))
+    assert call(K=136) == BAD and call(N=68) == BAD and call(K=0) == BAD and call(T=-1) == BAD
+    assert call(E=0) == BAD and call(G=-1) == BAD and call(ro=None) == BAD and call(ids=None) == BAD
+    assert call(act=5) == BAD and call(act=-1) == BAD
+    for p in ("c", "a", "b", "sa", "sb"):
+        assert call(**{p: None}) == BAD
+    for p in ("c", "a", "b", "sa", "sb", "bias", "res", "z"):
+        assert call(**{p: ODD}) == BAD
+    assert call(z=FAKE) == BAD                             # c itself
+    assert call(G=1025) == UNSUPPORTED and call(T=1 << 31) == UNSUPPORTED
+    assert call(G=0) == OK and call(T=0, a=None, c=None, sa=None, res=None, z=None) == OK
+
+
+def test_epilogue_grad_refusals(lib):  # noqa: F811
+    call = _caller(lib.moeq_grouped_epilogue_grad, dict(
+        dc=FAKE, dcs=64, z=FAKE, act=2, q=FAKE, s=FAKE, dz=FAKE, db=FAKE, ro=FAKE, ids=FAKE, T=8,
+        N=64, E=2, G=2, ws=FAKE, st=None))
+    assert call(T=-1) == BAD and call(N=0) == BAD and call(N=68) == BAD and call(E=0) == BAD
+    assert call(N=56) == BAD                               # codes of an N that is no multiple of 16
+    assert call(dcs=56) == BAD and call(dcs=68) == BAD and call(act=5) == BAD and call(act=-1) == BAD
+    for p in ("dc", "z", "q", "s", "dz", "db", "ws"):
+        assert call(**{p: ODD}) == BAD
+    for p in ("dc", "z", "q", "s", "ws", "ro", "ids"):
+        assert call(**{p: None}) == BAD
+    assert call(act=0) == BAD                              # z without an activation
+    assert call(q=None, s=None, dz=None, db=None) == BAD   # nothing to compute
+    assert call(G=1025) == UNSUPPORTED and call(T=1 << 31) == UNSUPPORTED and call(E=65536) == UNSUPPORTED
+    assert call(T=0, db=None, dc=None, z=None, q=None, s=None) == OK
+    size = lib.moeq_grouped_epilogue_grad_workspace
+    assert size(-1, 64, 2) == -1 and size(8, 60, 2) == -1 and size(8, 64, 1025) == -1
+    assert size(8, 64, 2) == 16 + 2 * 64 * 4 and size(1000, 64, 3) == 16 + 10 * 64 * 4
+    assert size(0, 64, 4) == 32
+
+
+def test_epilogue_binding_refuses_host_tensors():
+    x, ids = torch.zeros(4, 64), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        moeq.grouped_matmul_fp8_block_epilogue(x, x, torch.zeros(1, 8, 64), x, x, ids, ids[:1])
+    with pytest.raises(ValueError):
+        moeq.grouped_epilogue_grad(x.bfloat16(), ids, ids[:1], 1, d_z=x)
