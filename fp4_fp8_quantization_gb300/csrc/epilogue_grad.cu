@@ -27,10 +27,16 @@ constexpr int kRows = kEpilogueGradRows;
 constexpr int kWarps = 8;
 constexpr int kCols = 256;  // of a CTA: 32 lanes of 8
 
+__device__ __forceinline__ void pairs8(const uint4 &u, F2 (&x)[4]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        x[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+
 struct EpilogueGradParams {
     const uint16_t *dc, *z;
     int64_t dc_stride, rows, N;
-    int act;
     const uint32_t *offsets;
     const int32_t *expert_ids;
     int num_groups, num_experts;
@@ -43,7 +49,20 @@ struct EpilogueGradParams {
     uint32_t *err;
 };
 
-__global__ void __launch_bounds__(kWarps * 32) epilogue_grad_kernel(EpilogueGradParams p) {
+// The largest of 4 rows' m over the 16 lanes of a block: lane l of them gets that of
+// row l / 4 (each step sends the rows that the other half of the lanes keeps).
+__device__ __forceinline__ float rows_amax(const float (&m)[4], int lane) {
+    constexpr unsigned kAll = 0xFFFFFFFFu;
+    const bool b3 = lane & 8, b2 = lane & 4;
+    const float k0 = fmaxf(b3 ? m[2] : m[0], __shfl_xor_sync(kAll, b3 ? m[0] : m[2], 8));
+    const float k1 = fmaxf(b3 ? m[3] : m[1], __shfl_xor_sync(kAll, b3 ? m[1] : m[3], 8));
+    float k = fmaxf(b2 ? k1 : k0, __shfl_xor_sync(kAll, b2 ? k0 : k1, 4));
+    k = fmaxf(k, __shfl_xor_sync(kAll, k, 2));
+    return fmaxf(k, __shfl_xor_sync(kAll, k, 1));
+}
+
+template <int ACT>
+__global__ void __launch_bounds__(kWarps * 32, 2) epilogue_grad_kernel(EpilogueGradParams p) {
     // tiles before each group
     __shared__ uint32_t prefix[kMaxGroups + 1];
     __shared__ float sums[kWarps][kCols];
@@ -94,7 +113,6 @@ __global__ void __launch_bounds__(kWarps * 32) epilogue_grad_kernel(EpilogueGrad
     }
     const int64_t n = (int64_t)blockIdx.x * kCols + lane * 8, NB = (p.N + 127) / 128;
     const bool in_n = n < p.N;
-    const float c1 = sigma_c1(p.act), c3 = sigma_c3(p.act);
     for (uint32_t t = blockIdx.y; t < total; t += gridDim.y) {
         int lo = 0, hi = G;  // the last group that begins at or before tile t
         while (hi - lo > 1) {
@@ -103,10 +121,10 @@ __global__ void __launch_bounds__(kWarps * 32) epilogue_grad_kernel(EpilogueGrad
         }
         const int64_t r0 = (int64_t)__ldg(p.offsets + lo) + (int64_t)(t - prefix[lo]) * kRows;
         const int rows = (int)min((int64_t)kRows, (int64_t)__ldg(p.offsets + lo + 1) - r0);
-        float sum[8];
+        F2 sum[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
-        constexpr int U = 4;  // rows of a warp whose loads are in flight together
+        for (int i = 0; i < 4; ++i) sum[i] = f2s(0.0f);
+        constexpr int U = 4;  // rows of a warp that are worked on together
         for (int base = warp; base < rows; base += U * kWarps) {
             uint4 dc[U], zv[U];
 #pragma unroll
@@ -115,45 +133,64 @@ __global__ void __launch_bounds__(kWarps * 32) epilogue_grad_kernel(EpilogueGrad
                 dc[j] = zv[j] = make_uint4(0u, 0u, 0u, 0u);
                 if (base + j * kWarps < rows && in_n) {
                     dc[j] = ld_stream(p.dc + r * p.dc_stride + n);
-                    if (p.z) zv[j] = ld_stream(p.z + r * p.N + n);
+                    if (ACT != MOEQ_ACT_NONE) zv[j] = ld_stream(p.z + r * p.N + n);
                 }
+            }
+            F2 x[U][4];
+            float m[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                pairs8(dc[j], x[j]);
+                if constexpr (ACT != MOEQ_ACT_NONE) {
+                    F2 z[4];
+                    pairs8(zv[j], z);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[j][i] = mul2(x[j][i], slope2<ACT>(z[i]));
+                }
+                m[j] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sum[i] = add2(sum[i], x[j][i]);
+                    m[j] = fmaxf(fmaxf(m[j], fabsf(f2_lo(x[j][i]))), fabsf(f2_hi(x[j][i])));
+                }
+            }
+            float inv = 0.0f;  // of row (lane / 4) % 4
+            if (p.q) {
+                const float s = block_scale(rows_amax(m, lane));
+                inv = __frcp_rn(s);
+                const int j = (lane >> 2) & 3;
+                const int64_t r = r0 + base + j * kWarps;
+                // 128-column blocks: the lanes 0 and 16 begin one
+                const int64_t at = (int64_t)blockIdx.x * (kCols / 128) + (lane >> 4);
+                float *scale = p.scales + r * NB + at;
+                if ((lane & 3) == 0 && base + j * kWarps < rows && at < NB &&
+                    store_fits(scale, 4, p.scales, p.rows * NB * 4, p.err))
+                    *scale = s;
             }
 #pragma unroll
             for (int j = 0; j < U; ++j) {
                 const int64_t r = r0 + base + j * kWarps;
-                if (base + j * kWarps >= rows) break;
-                float x[8];
-                unpack8(dc[j], x);
-                if (p.z) {
-                    float z[8];
-                    unpack8(zv[j], z);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        x[i] = __fmul_rn(x[i], act_slope(z[i], p.act, c1, c3));
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sum[i] = __fadd_rn(sum[i], x[i]);
+                const float rj = __shfl_sync(0xFFFFFFFFu, inv, (lane & 16) | (j << 2));
+                if (base + j * kWarps >= rows || !in_n) continue;
                 if (p.q) {
-                    float m = amax8(x);
+                    uint32_t w[4];
 #pragma unroll
-                    for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-                    const float s = block_scale(m);
-                    if (in_n) {
-                        uint8_t *out = p.q + r * p.N + n;
-                        float *scale = p.scales + r * NB + n / 128;
-                        if (store_fits(out, 8, p.q, p.rows * p.N, p.err))
-                            *reinterpret_cast<uint2 *>(out) = codes8(x, __fdiv_rn(1.0f, s));
-                        if ((lane & 15) == 0 &&
-                            store_fits(scale, 4, p.scales, p.rows * NB * 4, p.err))
-                            *scale = s;
+                    for (int i = 0; i < 4; ++i) {
+                        const F2 y = mul2(x[j][i], f2s(rj));
+                        w[i] = e4m3x2(f2_lo(y), f2_hi(y));
                     }
+                    uint8_t *out = p.q + r * p.N + n;
+                    if (store_fits(out, 8, p.q, p.rows * p.N, p.err))
+                        *reinterpret_cast<uint2 *>(out) =
+                            make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
                 }
-                if (p.dz && in_n) {
-                    uint16_t *out = p.dz + r * p.N + n;
+                if (p.dz) {
                     uint32_t w[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        w[i] = f32_to_bf16_bits(x[2 * i]) | (f32_to_bf16_bits(x[2 * i + 1]) << 16);
+                        w[i] = f32_to_bf16_bits(f2_lo(x[j][i])) |
+                               (f32_to_bf16_bits(f2_hi(x[j][i])) << 16);
+                    uint16_t *out = p.dz + r * p.N + n;
                     if (store_fits(out, 16, p.dz, p.rows * p.N * 2, p.err))
                         st_global_v4(out, w[0], w[1], w[2], w[3]);
                 }
@@ -162,7 +199,10 @@ __global__ void __launch_bounds__(kWarps * 32) epilogue_grad_kernel(EpilogueGrad
         if (!p.part) continue;
         __syncthreads();  // the sums of the tile before have been read
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sums[warp][lane * 8 + i] = sum[i];
+        for (int i = 0; i < 4; ++i) {
+            sums[warp][lane * 8 + 2 * i] = f2_lo(sum[i]);
+            sums[warp][lane * 8 + 2 * i + 1] = f2_hi(sum[i]);
+        }
         __syncthreads();
         const int64_t col = (int64_t)blockIdx.x * kCols + threadIdx.x;
         float v = sums[0][threadIdx.x];
@@ -213,7 +253,7 @@ __global__ void __launch_bounds__(1024) bias_grad_kernel(const float *part, cons
 
 cudaError_t launch_epilogue_grad(const EpilogueGradArgs &a, cudaStream_t s) {
     const int64_t tiles = epilogue_grad_tiles(a.groups.total_rows, a.groups.num_groups);
-    // the sums' place: the table of tiles, then the sums, 16-byte aligned
+    // its parts: the table of tiles, then the sums, 16-byte aligned
     uint32_t *table = static_cast<uint32_t *>(a.workspace);
     float *part = a.d_bias ? reinterpret_cast<float *>(
                                  static_cast<uint8_t *>(a.workspace) +
@@ -221,13 +261,19 @@ cudaError_t launch_epilogue_grad(const EpilogueGradArgs &a, cudaStream_t s) {
                            : nullptr;
     const EpilogueGradParams p{static_cast<const uint16_t *>(a.dc),
                                static_cast<const uint16_t *>(a.z), a.dc_stride,
-                               a.groups.total_rows, a.N, a.act, a.groups.row_offsets,
+                               a.groups.total_rows, a.N, a.groups.row_offsets,
                                a.groups.expert_ids, a.groups.num_groups, a.groups.num_experts, a.q,
                                a.scales, static_cast<uint16_t *>(a.dz), part, table, tiles, a.err};
     if (tiles > 0) {
         const dim3 grid((unsigned)((a.N + kCols - 1) / kCols),
                         (unsigned)std::min<int64_t>(tiles, 65535));
-        const cudaError_t e = launch_pdl(epilogue_grad_kernel, grid, kWarps * 32, 0, s, p);
+        auto *kern = a.act == MOEQ_ACT_RELU   ? epilogue_grad_kernel<MOEQ_ACT_RELU>
+                     : a.act == MOEQ_ACT_SILU ? epilogue_grad_kernel<MOEQ_ACT_SILU>
+                     : a.act == MOEQ_ACT_GELU ? epilogue_grad_kernel<MOEQ_ACT_GELU>
+                     : a.act == MOEQ_ACT_GELU_TANH
+                         ? epilogue_grad_kernel<MOEQ_ACT_GELU_TANH>
+                         : epilogue_grad_kernel<MOEQ_ACT_NONE>;
+        const cudaError_t e = launch_pdl(kern, grid, kWarps * 32, 0, s, p);
         if (e != cudaSuccess) return e;
     }
     if (!a.d_bias) return cudaSuccess;

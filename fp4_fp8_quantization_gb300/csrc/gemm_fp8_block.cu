@@ -146,20 +146,16 @@ __device__ __forceinline__ uint4 ld_global_v4(const void *p) {
 }
 
 // The activation of 32 values.
+template <int ACT>
+__device__ __forceinline__ void activate16(F2 *v) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = activate2<ACT>(v[i]);
+}
 __device__ __forceinline__ void activate16(F2 *v, int act) {
-    if (act == MOEQ_ACT_NONE) return;
-    if (act == MOEQ_ACT_RELU) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = f2(act_relu(f2_lo(v[i])), act_relu(f2_hi(v[i])));
-    } else if (act == MOEQ_ACT_GELU) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = f2(act_gelu(f2_lo(v[i])), act_gelu(f2_hi(v[i])));
-    } else {
-        const float c1 = sigma_c1(act), c3 = sigma_c3(act);
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            v[i] = f2(act_sigma(f2_lo(v[i]), c1, c3), act_sigma(f2_hi(v[i]), c1, c3));
-    }
+    if (act == MOEQ_ACT_RELU) activate16<MOEQ_ACT_RELU>(v);
+    if (act == MOEQ_ACT_SILU) activate16<MOEQ_ACT_SILU>(v);
+    if (act == MOEQ_ACT_GELU) activate16<MOEQ_ACT_GELU>(v);
+    if (act == MOEQ_ACT_GELU_TANH) activate16<MOEQ_ACT_GELU_TANH>(v);
 }
 
 // Waits for the thread's tensor-memory loads; r is written by them.
