@@ -18,12 +18,13 @@
 //
 // The row of a token is in the registers of L lanes, a power of two of them for
 // each group (lane and index order are expert order), read once.  Keys are the
-// bits of max c - c with the lane and index in the low bits: those of the best
+// bits of max c - c with the lane and index in the low bits (of 16-bit logits without
+// a bias: their whole images): those of the best
 // values, close to the maximum, keep most of their digits, so that a round of the
 // choice is one integer minimum over the lanes.  Scores next to one another are
-// decided in 64 bits: c in fp32 is off by a bound known beforehand, and a token
+// decided as 64 bits would: c in fp32 is off by a bound known beforehand, and a token
 // in which two values that the choice depends on are closer than that (about one
-// in a thousand) is chosen again from 64-bit scores.
+// in a thousand) is chosen again from scores that are sums of two floats.
 #include <algorithm>
 
 #include "common.cuh"
@@ -41,7 +42,7 @@ struct ScoredParams {
     const uint8_t *logits;
     int64_t stride;  // bytes
     int64_t num_tokens;
-    int E, top_k;
+    int dt, E, top_k;
     const float *bias;  // null: none
     int sigmoid, top2, normalize;
     int groups, topk_groups;
@@ -53,18 +54,37 @@ struct ScoredParams {
     uint32_t *err;
 };
 
-// 1 / (1 + exp(-x)) within 4e-7: exp is within 2 + 1.2 |x| ulp of 2^-23, which
-// s (1 - s) turns into 8e-8 at most; the sum and the quotient (2 ulp) add 3e-7 s.
-__device__ __forceinline__ float score_fast(float x) {
-    return __fdividef(1.0f, __fadd_rn(1.0f, __expf(-x)));
+// exp and sigma of fp32 by 2^x and 1 / x of the hardware, results below 2^-126 as 0.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
 
+// 1 / (1 + exp(-x)) within kScoreTol: exp is within 2^-22 + |x| 2^-23 relative, which
+// s (1 - s) turns into 8e-8 at most; the sum and the quotient add 2e-7 s.
+__device__ __forceinline__ float score_fast(float x) {
+    return rcp_fast(__fadd_rn(1.0f, exp2_fast(__fmul_rn(x, -kLog2e))));
+}
 constexpr float kScoreTol = 4e-7f;
 
-// A softmax's p, relative: exp's 2 + 1.2 |d| ulp (at most 2 ulp of the largest p),
-// the total's own error, the mean of its terms' (ln 1024 bounds the mean of |d|) and
-// (32 + 5) 2^-24 of its sums, and the product's: 4e-6 of the largest p.
+// exp(x - m), x <= m, within 2^-22 + |x - m| 2^-22 relative (the difference and its
+// product are rounded).
+__device__ __forceinline__ float exp_fast(float x, float m) {
+    return exp2_fast(__fmul_rn(__fadd_rn(x, -m), kLog2e));
+}
+// A softmax's p, in units of the largest one: 2 2^-22 of it for exp, and relative the
+// total's own error, the mean of its terms' (ln 1024 bounds the mean of |x - m|), (32 + 5)
+// 2^-24 of its sums and 2^-22 of the quotient: 4.9e-6.
 constexpr float kSoftmaxTol = 5e-6f;
+// without the total, exp alone
+constexpr float kExpTol = 6e-7f;
 
 // sigmoid(x) for the weights: within a few ulp of either end.
 __device__ __forceinline__ float sigmoid_exact(float x) {
@@ -77,6 +97,15 @@ __device__ __forceinline__ uint32_t lanes_min(uint32_t v) {
     if constexpr (L == 32) return __reduce_min_sync(0xFFFFFFFFu, v);
 #pragma unroll
     for (int o = L / 2; o; o >>= 1) v = min(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
+
+// The largest of the lanes' floats, none a NaN.
+template <int L>
+__device__ __forceinline__ float lanes_top(float v) {
+    if constexpr (L == 32) return key_value(lanes_max<L>(order_key(v)));
+#pragma unroll
+    for (int o = L / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
     return v;
 }
 
@@ -100,93 +129,255 @@ __device__ __forceinline__ Place place_of(const ScoredParams &p, int sub) {
     return a;
 }
 
-// Best two of pairs (a >= b) and (c >= d).
+// The best two of a >= b and c >= d.
 template <class T>
 __device__ __forceinline__ void best_two(T &a, T &b, T c, T d) {
-    b = a < c ? (a > d ? a : d) : (b > c ? b : c);
+    const T lo = a < c ? a : c, hi = b > d ? b : d;
     a = a > c ? a : c;
+    b = lo > hi ? lo : hi;
 }
 
-template <class T>
-__device__ __forceinline__ T group_value(T a, T b, bool sum, T none) {
-    return sum && b > none ? a + b : a;
+// What follows down to the kernel runs for one token in a thousand.  Fetching its
+// instructions is much of what it costs, so that loops stay loops; 64-bit floats, which
+// this machine takes some 90 cycles for, are left out (with them a pair of values took
+// 13500 cycles and the groups 80000).
+
+// A value as the sum of two floats, the second below half a unit of the first.
+struct Pair {
+    float hi, lo;
+};
+
+__device__ __forceinline__ Pair quick_sum(float a, float b) {  // |a| >= |b|
+    const float s = __fadd_rn(a, b);
+    return {s, __fadd_rn(b, -__fadd_rn(s, -a))};
+}
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), v = __fadd_rn(s, -a);
+    return {s, __fadd_rn(__fadd_rn(a, -__fadd_rn(s, -v)), __fadd_rn(b, -v))};
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+    const Pair s = two_sum(a.hi, b.hi);
+    return quick_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
+}
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+    const float p = __fmul_rn(a.hi, b.hi);
+    const float e = __fmaf_rn(a.hi, b.hi, -p);
+    return quick_sum(p, __fadd_rn(e, __fmaf_rn(a.hi, b.lo, __fmul_rn(a.lo, b.hi))));
+}
+// 1 / d by a Newton step from 2^-23, with the step's square
+__device__ __forceinline__ Pair reciprocal(Pair d) {
+    const float r = rcp_fast(d.hi);
+    const float e = __fmaf_rn(-d.lo, r, __fmaf_rn(-d.hi, r, 1.0f));
+    return quick_sum(r, __fmul_rn(r, __fmaf_rn(e, e, e)));
 }
 
-// The choice from 64-bit scores, for a warp with a token that 32 bits do not
-// decide; lane r of each token gets choice r (-1: none left).
-__device__ __noinline__ int choose_64(const ScoredParams &p, const uint8_t *row, int dt, int lane,
-                                      int L) {
+// exp(x), x <= 0, within 2^-45: 2^n e^f with n = x / ln 2 to the nearest, ln 2 in three
+// parts of which the first leaves n times it exact, and the Taylor series of e^f, |f| <=
+// 0.35, to the 13th power.
+__device__ __noinline__ Pair exp_pair(Pair x) {
+    const float n = rintf(__fmul_rn(x.hi, kLog2e));
+    if (!(n >= -126.0f)) return {0.0f, 0.0f};
+    Pair f = two_sum(__fmaf_rn(n, -0x1.62ep-1f, x.hi), x.lo);
+    f = add(f, mul({-n, 0.0f}, {0x1.0bfbe8p-15f, 0x1.cf79acp-40f}));
+    Pair p = {1.0f, 0.0f};
+#pragma unroll 1
+    for (float k = 13.0f; k > 0.0f; k -= 1.0f)
+        p = add({1.0f, 0.0f}, mul(mul(p, f), reciprocal({k, 0.0f})));
+    const float scale = __uint_as_float((uint32_t)((int)n + 127) << 23);
+    return {__fmul_rn(p.hi, scale), __fmul_rn(p.lo, scale)};
+}
+
+// Integers that order as values do; 0 stands for none.  The second part is rounded to
+// what 64-bit floats keep beside the first, so that what they cannot tell apart is equal.
+__device__ __forceinline__ uint64_t pair_key(Pair v) {
+    const float unit =
+        __fmul_rn(__uint_as_float(__float_as_uint(v.hi) & 0x7F800000u), 1.5f * 0x1p-29f);
+    const float lo = __fadd_rn(__fadd_rn(v.lo, unit), -unit);
+    return ((uint64_t)order_key(v.hi) << 32) | order_key(lo);
+}
+__device__ __forceinline__ uint64_t float_key(float v) {
+    return v > -kInf ? ((uint64_t)order_key(v) << 32) | 0x80000000u : 0u;
+}
+__device__ __forceinline__ float key_hi(uint64_t k) { return key_value((uint32_t)(k >> 32)); }
+__device__ __forceinline__ Pair key_pair(uint64_t k) { return {key_hi(k), key_value((uint32_t)k)}; }
+
+// What the calls below know of a token: its largest logit, whether its order is that of
+// the logits (no bias, or no softmax), and the bound of the scores' errors, doubled.
+struct Token {
+    float m;
+    bool plain;
+    float tol;
+};
+
+// The sum of exp(x - m) over a token's logits.
+__device__ __noinline__ Pair total_pair(const ScoredParams &p, const uint8_t *row, int lane, int L,
+                                        float m) {
+    const Place a = place_of(p, lane % L);
+    Pair total = {0.0f, 0.0f};
+#pragma unroll 1
+    for (int i = 0; i < a.n; ++i) {
+        const float x = load_any(row, a.j0 + i, p.dt);
+        if (x > -kInf) total = add(total, exp_pair(two_sum(x, -m)));
+    }
+#pragma unroll 1
+    for (int o = L / 2; o; o >>= 1)
+        total = add(total, {__shfl_xor_sync(0xFFFFFFFFu, total.hi, o),
+                            __shfl_xor_sync(0xFFFFFFFFu, total.lo, o)});
+    return total;
+}
+
+// The key of c from a logit and its bias; of a softmax with its total.
+__device__ __noinline__ uint64_t value_key(bool sigmoid, float x, float b, float m, Pair total) {
+    // sigma by e = exp(-|x|): 1 / (1 + e) or e / (1 + e)
+    const Pair e = exp_pair(sigmoid ? Pair{-fabsf(x), 0.0f} : two_sum(x, -m));
+    const Pair r = reciprocal(sigmoid ? add({1.0f, 0.0f}, e) : total);
+    return pair_key(add(sigmoid && x >= 0.0f ? r : mul(e, r), {b, 0.0f}));
+}
+
+// Keys of a lane's values in fp32 (none for what is never chosen) and which of them are
+// final.  scored: c, or the sums' terms; else the logits.
+__device__ __noinline__ uint32_t first_keys(const ScoredParams &p, const uint8_t *row, Place a,
+                                            Token k, bool bias, bool scored, float total,
+                                            uint64_t *c) {
+    uint32_t known = scored ? 0u : 0xFFFFFFFFu;
+#pragma unroll 1
+    for (int i = 0; i < a.n; ++i) {
+        const float x = load_any(row, a.j0 + i, p.dt);
+        float v = x;
+        if (scored) v = p.sigmoid ? score_fast(x) : __fdividef(exp_fast(x, k.m), total);
+        if (bias) v = __fadd_rn(v, __ldg(p.bias + a.j0 + i));
+        c[i] = x > -kInf ? float_key(v) : 0u;
+        if (!(fabsf(v) < 1e30f)) known |= 1u << i;
+    }
+    return known;
+}
+
+__device__ __forceinline__ uint64_t shfl_xor_key(uint64_t k, int o) {
+    return __shfl_xor_sync(0xFFFFFFFFu, (unsigned long long)k, o);
+}
+
+// The groups chosen, for a warp with a token whose fp32 values do not decide them:
+// whether the lane's is.  Where the border between the chosen and the others depends
+// on two values that are closer than their errors, what they sum is computed as pairs,
+// and the groups are ranked again.
+__device__ __noinline__ bool groups_again(const ScoredParams &p, const uint8_t *row, int lane,
+                                          int L, Token k) {
     constexpr unsigned kAll = 0xFFFFFFFFu;
-    const double none = -__longlong_as_double(0x7FF0000000000000ll);
     const int sub = lane % L;
     const Place a = place_of(p, sub);
-    double c[kMaxPerLane];
-    float m = -kInf;
-    int bad = 0;
-    for (int i = 0; i < a.n; ++i) {
-        const float x = load_any(row, a.j0 + i, dt);
-        bad |= x != x;
-        m = fmaxf(m, x);
-        c[i] = x > -kInf ? (double)x : none;
-    }
-    for (int o = L / 2; o; o >>= 1) {
-        m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-        bad |= __shfl_xor_sync(kAll, bad, o);
-    }
-    const bool plain = !p.sigmoid && (bad || m == kInf);  // no softmax: by the logits
-    double total = 0.0;
-    if (!p.sigmoid) {
-        for (int i = 0; i < a.n; ++i)
-            if (c[i] > none) total += exp(c[i] - (double)m);
-        for (int o = L / 2; o; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
-    }
-    const bool by_score = !plain && (p.bias || (p.groups > 1 && p.top2));
-    double g1 = none, g2 = none;
-    for (int i = 0; i < a.n; ++i) {
-        double v = c[i];
-        if (by_score && c[i] > none) {
-            v = p.sigmoid ? 1.0 / (1.0 + exp(-c[i])) : exp(c[i] - (double)m) / total;
-            if (p.bias) {
-                v += (double)__ldg(p.bias + a.j0 + i);
-                c[i] = v = v > none ? v : none;
-            }
-        }
-        best_two(g1, g2, v, none);
-    }
-    if (p.groups > 1) {
+    const bool bias = p.bias && !k.plain, sums = p.top2 && !k.plain, scored = bias || sums;
+    // the sums of exps are compared without the total that all share
+    Pair total = {1.0f, 0.0f};
+    if (!p.sigmoid && p.bias) total = total_pair(p, row, lane, L, k.m);
+    uint64_t c[kMaxPerLane];
+    uint32_t known = first_keys(p, row, a, k, bias, scored, total.hi, c);
+#pragma unroll 1
+    for (;;) {
+        uint64_t g1 = 0u, g2 = 0u;
+#pragma unroll 1
+        for (int i = 0; i < a.n; ++i) best_two(g1, g2, c[i], (uint64_t)0u);
+#pragma unroll 1
         for (int o = (1 << p.lane_shift) / 2; o; o >>= 1) {
-            const double b1 = __shfl_xor_sync(kAll, g1, o), b2 = __shfl_xor_sync(kAll, g2, o);
+            const uint64_t b1 = shfl_xor_key(g1, o), b2 = shfl_xor_key(g2, o);
             best_two(g1, g2, b1, b2);
         }
-        const double v = group_value(g1, g2, p.top2 && !plain, none);
+        const bool two = sums && g2 != 0u;
+        uint64_t v = g1;
+        if (two && key_hi(g1) < kInf) v = pair_key(add(key_pair(g1), key_pair(g2)));
         int rank = 0;
+        float edge = 0.0f, next = 0.0f;  // the last value that is chosen, the first that is not
+#pragma unroll 1
         for (int h = 0; h < p.groups; ++h) {
-            const double u = __shfl_sync(kAll, v, h << p.lane_shift, L);
+            const uint64_t u = __shfl_sync(kAll, (unsigned long long)v, h << p.lane_shift, L);
             rank += u > v || (u == v && h < a.group);
         }
-        if (rank >= p.topk_groups)
-            for (int i = 0; i < a.n; ++i) c[i] = none;
-    }
-    int id = -1;
-    uint32_t taken = 0u;
-    for (int r = 0; r < p.top_k; ++r) {
-        double best = none;
-        int at = 0x7FFFFFFF;
-        for (int i = 0; i < a.n; ++i)
-            if (!((taken >> i) & 1u) && c[i] > best) {
-                best = c[i];
-                at = a.j0 + i;
+#pragma unroll 1
+        for (int h = 0; h < p.groups; ++h) {
+            const float u = __shfl_sync(kAll, key_hi(v), h << p.lane_shift, L);
+            const int r = __shfl_sync(kAll, rank, h << p.lane_shift, L);
+            if (r == p.topk_groups - 1) edge = u;
+            if (r == p.topk_groups) next = u;
+        }
+        const float low = key_hi(two ? g2 : g1), value = key_hi(v);
+        const float size = __fadd_rn(fabsf(key_hi(g1)), two ? fabsf(low) : 0.0f);
+        const float near = __fmaf_rn(1e-6f, size, 2.0f * k.tol);
+        const bool open = scored && g1 != 0u && p.topk_groups < p.groups &&
+                          (rank < p.topk_groups ? value - next <= near : edge - value <= near);
+        const float from = __fmaf_rn(-1e-6f, fabsf(low), low - k.tol);
+        bool more = false;
+#pragma unroll 1
+        for (int i = 0; open && i < a.n; ++i)
+            if (!((known >> i) & 1u) && c[i] != 0u && key_hi(c[i]) >= from) {
+                c[i] = value_key(p.sigmoid, load_any(row, a.j0 + i, p.dt),
+                                 bias ? __ldg(p.bias + a.j0 + i) : 0.0f, k.m, total);
+                known |= 1u << i;
+                more = true;
             }
-        for (int o = L / 2; o; o >>= 1) {
-            const double v = __shfl_xor_sync(kAll, best, o);
-            const int j = __shfl_xor_sync(kAll, at, o);
-            if (v > best || (v == best && j < at)) {
-                best = v;
-                at = j;
+        if (!__any_sync(kAll, more)) return rank < p.topk_groups;
+    }
+}
+
+// The choice from all of a token's values, for a warp with one that the kept keys do not
+// decide; lane r of each token gets choice r (-1: none left).  in: whether the lane's
+// group is chosen.  Values in fp32, those near the one that is chosen as pairs too.
+__device__ __noinline__ int choose_again(const ScoredParams &p, const uint8_t *row, int lane, int L,
+                                         bool in, Token k) {
+    constexpr unsigned kAll = 0xFFFFFFFFu;
+    const int sub = lane % L;
+    const Place a = place_of(p, sub);
+    const bool bias = p.bias && !k.plain;
+    Pair total = {1.0f, 0.0f};
+    if (!p.sigmoid && p.bias) total = total_pair(p, row, lane, L, k.m);
+    uint64_t c[kMaxPerLane];
+    uint32_t known = first_keys(p, row, a, k, bias, bias, total.hi, c);
+    int id = -1;
+#pragma unroll 1
+    for (int r = 0; r < p.top_k; ++r) {
+        uint64_t best;
+        int at;
+#pragma unroll 1
+        for (;;) {
+            best = 0u;
+            at = 0x7FFFFFFF;
+#pragma unroll 1
+            for (int i = 0; in && i < a.n; ++i)
+                if (c[i] > best) {
+                    best = c[i];
+                    at = a.j0 + i;
+                }
+#pragma unroll 1
+            for (int o = L / 2; o; o >>= 1) {
+                const uint64_t v = shfl_xor_key(best, o);
+                const int j = __shfl_xor_sync(kAll, at, o);
+                if (v > best || (v == best && j < at)) {
+                    best = v;
+                    at = j;
+                }
+            }
+            const float hi = key_hi(best);
+            const float from = __fmaf_rn(-1e-6f, fabsf(hi), hi - k.tol);
+            uint32_t todo = 0u;
+            int count = 0;
+#pragma unroll 1
+            for (int i = 0; bias && in && i < a.n; ++i)
+                if (c[i] != 0u && key_hi(c[i]) >= from) {
+                    ++count;
+                    todo |= 1u << i;
+                }
+#pragma unroll 1
+            for (int o = L / 2; o; o >>= 1) count += __shfl_xor_sync(kAll, count, o);
+            todo = count > 1 ? todo & ~known : 0u;
+            if (!__any_sync(kAll, todo != 0u)) break;
+            known |= todo;
+#pragma unroll 1
+            for (; todo; todo &= todo - 1) {
+                const int i = __ffs((int)todo) - 1;
+                c[i] = value_key(p.sigmoid, load_any(row, a.j0 + i, p.dt), __ldg(p.bias + a.j0 + i),
+                                 k.m, total);
             }
         }
-        if (at >= a.j0 && at < a.j0 + a.n) taken |= 1u << (at - a.j0);
-        if (sub == r) id = best > none ? at : -1;
+        if (in && at >= a.j0 && at < a.j0 + a.n) c[at - a.j0] = 0u;
+        if (sub == r) id = best != 0u ? at : -1;
     }
     return id;
 }
@@ -209,10 +400,11 @@ __device__ __forceinline__ void merge_step(uint32_t (&key)[NV]) {
     }
 }
 
-template <int DT, int NV, int L>
+
+template <int NV, int L, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(kWarps * 32) gate_scored_kernel(ScoredParams p) {
     constexpr unsigned kAll = 0xFFFFFFFFu;
-    constexpr uint32_t kIdx = (uint32_t)(L * NV) - 1u, kNoKey = 0xFFFFFFFFu;
+    constexpr uint32_t kIdx = (uint32_t)(L * NV) - 1u;
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, sub = lane % L;
@@ -223,76 +415,107 @@ __global__ void __launch_bounds__(kWarps * 32) gate_scored_kernel(ScoredParams p
     const uint8_t *row = p.logits + t * p.stride;
     const Place a = place_of(p, sub);
     float x[NV];
-    load_row<DT>(row, a.j0 + a.n, a.j0, p.vec, x);
-    // c, -inf for what is never chosen
-    float c[NV], m = -kInf, inv = 0.0f, total = 0.0f;
-    bool nan = false;
+    if (p.dt == MOEQ_FP32)
+        load_row<MOEQ_FP32>(row, a.j0 + a.n, a.j0, p.vec, x);
+    else if (p.dt == MOEQ_BF16)
+        load_row<MOEQ_BF16>(row, a.j0 + a.n, a.j0, p.vec, x);
+    else
+        load_row<MOEQ_FP16>(row, a.j0 + a.n, a.j0, p.vec, x);
+    bool nan = false, masked = false;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         nan |= x[i] != x[i];
-        m = fmaxf(m, x[i]);
+        masked |= !(x[i] > -kInf);
     }
-    bool plain = false;
-    if (!p.sigmoid) {
+    float m = -kInf, total = 0.0f, inv = 0.0f;
+    bool plain = false;  // no softmax: by the logits
+    float e[NV];
+    if constexpr (!SIGMOID) {
 #pragma unroll
-        for (int o = L / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-        if (m > -kInf) {
+        for (int i = 0; i < NV; ++i) m = fmaxf(m, x[i]);
+        m = lanes_top<L>(m);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) total = __fadd_rn(total, exp_diff(x[i], m));
+        for (int i = 0; i < NV; ++i) {
+            e[i] = exp_fast(x[i], m);
+            total = __fadd_rn(total, e[i]);
         }
-        total = lanes_sum<L>(total);
-        inv = __fdividef(1.0f, total);
+        total = m > -kInf ? lanes_sum<L>(total) : 0.0f;
+        inv = rcp_fast(total);
         plain = !(total < kInf);  // NaN: a NaN logit, or m infinite
     }
-    auto score = [&](float v) {
-        return p.sigmoid ? score_fast(v) : __fmul_rn(exp_diff(v, m), inv);
-    };
-    // c of a logit and its bias
+    // c, -inf for what is never chosen
     auto value = [&](float v, float b) {
-        return p.bias && !plain ? __fadd_rn(score(v), b) : v;
+        if constexpr (!BIAS) return v;
+        if constexpr (SIGMOID) return __fadd_rn(score_fast(v), b);
+        return plain ? v : __fadd_rn(__fmul_rn(exp_fast(v, m), inv), b);
     };
-    // how far apart two values are decided: twice the scores' bound, and the
-    // rounding of the sums with the bias (2^-24 each, taken as 2^-22)
-    const float tol =
-        plain ? 0.0f : 2.0f * (p.sigmoid ? kScoreTol : __fmul_rn(kSoftmaxTol, inv));
-    bool unsure = false;
+    float c[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const float b = p.bias && i < a.n ? __ldg(p.bias + a.j0 + i) : 0.0f;
-        const float v = value(x[i], b);
-        c[i] = x[i] > -kInf && v > -kInf ? v : -kInf;
+        const float b = BIAS && i < a.n ? __ldg(p.bias + a.j0 + i) : 0.0f;
+        c[i] = BIAS && !SIGMOID ? (plain ? x[i] : __fadd_rn(__fmul_rn(e[i], inv), b))
+                                : value(x[i], b);
     }
-    if (p.groups > 1) {
-        const bool sum = p.top2 && !plain, scores = sum && !p.bias;
-        float g1 = -kInf, g2 = -kInf;
+    // a NaN bias's too
+    if (BIAS || __any_sync(kAll, masked)) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            best_two(g1, g2, scores && c[i] > -kInf ? score(c[i]) : c[i], -kInf);
+        for (int i = 0; i < NV; ++i) c[i] = x[i] > -kInf && c[i] > -kInf ? c[i] : -kInf;
+    }
+    // How far apart two values are decided: twice the scores' bound, and the rounding of
+    // the sums with the bias (2^-24 each, taken as 2^-22).
+    const float tol = SIGMOID ? 2.0f * kScoreTol : 2.0f * kSoftmaxTol * inv;
+    const bool rounded = BIAS && !plain;
+    bool in = true;  // the lane's group is chosen
+    if (p.groups > 1) {
+        const bool sum = p.top2 && !plain, scores = sum && !BIAS;
+        float g1 = -kInf, g2 = -kInf;
+        if (scores) {  // exp without the total, which all share
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const float v = SIGMOID ? score_fast(c[i]) : e[SIGMOID ? 0 : i];
+                best_two(g1, g2, c[i] > -kInf ? v : -kInf, -kInf);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                g2 = fmaxf(g2, fminf(g1, c[i]));
+                g1 = fmaxf(g1, c[i]);
+            }
+        }
         for (int o = (1 << p.lane_shift) / 2; o; o >>= 1) {
             const float b1 = __shfl_xor_sync(kAll, g1, o), b2 = __shfl_xor_sync(kAll, g2, o);
             best_two(g1, g2, b1, b2);
         }
-        const float v = group_value(g1, g2, sum, -kInf);
-        // twice the error of this group's value, so that of two the larger counts
-        const float size = __fadd_rn(fabsf(g1), sum && g2 > -kInf ? fabsf(g2) : 0.0f);
-        const float near = (sum || p.bias) && !plain
-                               ? __fadd_rn(2.0f * tol, __fmul_rn(size, 0x1p-20f))
-                               : -1.0f;
-        int rank = 0;
-        float above = kInf, below = -kInf;  // the nearest groups' values
-        for (int h = 0; h < p.groups; ++h) {
-            const float u = __shfl_sync(kAll, v, h << p.lane_shift, L);
-            const bool ahead = u > v || (u == v && h < a.group);
-            rank += ahead;
-            if (ahead) above = fminf(above, u);
-            if (!ahead && h != a.group) below = fmaxf(below, u);
+        const bool two = sum && g2 > -kInf;
+        const float v = two ? __fadd_rn(g1, g2) : g1;
+        // groups by their values' images, the lowest of equal ones first
+        uint32_t key = a.group < p.groups ? order_key(v) : 0u, border = 0u;
+        int at = 0;  // the first lane of the group chosen last
+        in = false;
+        for (int r = 0; r < p.topk_groups; ++r) {
+            border = lanes_max<L>(key);
+            const uint32_t has = __ballot_sync(kAll, key == border) >> (lane - sub);
+            at = __ffs((int)has) - 1;
+            if (a.group == at >> p.lane_shift) {
+                in = true;
+                key = 0u;
+            }
         }
-        // only the border between the chosen groups and the others counts
-        if (a.n > 0 && v > -kInf) {
-            if (rank == p.topk_groups) unsure = above - v <= near;
-            if (rank == p.topk_groups - 1) unsure = v - below <= near;
+        if (sum || rounded) {
+            // the border between the last group chosen and the first that is not
+            const uint32_t next = lanes_max<L>(key);
+            const uint32_t has = __ballot_sync(kAll, key == next) >> (lane - sub);
+            const float size = __fadd_rn(fabsf(g1), two ? fabsf(g2) : 0.0f);
+            const float most = fmaxf(__shfl_sync(kAll, size, at, L),
+                                     __shfl_sync(kAll, size, __ffs((int)has) - 1, L));
+            const float bound = BIAS || SIGMOID ? tol : 2.0f * kExpTol;
+            const bool unsure =
+                next > kNegInfKey && !(__fadd_rn(key_value(border), -key_value(next)) >
+                                       __fadd_rn(2.0f * bound, __fmul_rn(most, 0x1p-20f)));
+            if (__any_sync(kAll, unsure))
+                in = groups_again(p, row, lane, L, Token{m, plain, bound});
         }
-        if (rank >= p.topk_groups) {
+        if (!in) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) c[i] = -kInf;
         }
@@ -300,15 +523,24 @@ __global__ void __launch_bounds__(kWarps * 32) gate_scored_kernel(ScoredParams p
     float top = -kInf;
 #pragma unroll
     for (int i = 0; i < NV; ++i) top = fmaxf(top, c[i]);
-#pragma unroll
-    for (int o = L / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+    top = lanes_top<L>(top);
+    // without a bias the images of 16-bit logits are whole in the bits above the index
+    const bool whole = !BIAS && p.dt != MOEQ_FP32;
+    // keys from that of -inf, or of an infinite distance, on stand for no expert
+    const uint32_t none = whole ? ~kNegInfKey >> 1 : 0x7F800000u;
+    // half the distance, which cannot overflow
+    const float half = __fmul_rn(top, 0.5f);
     uint32_t key[NV];
+    if (whole) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        // an infinite c is as far from itself as 0
-        const float d = c[i] == top ? 0.0f : __fadd_rn(top, -c[i]);
-        key[i] = c[i] > -kInf ? (__float_as_uint(d) & ~kIdx) | (uint32_t)(sub * NV + i) : kNoKey;
+        for (int i = 0; i < NV; ++i) key[i] = ~order_key(c[i]) >> 1;
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            key[i] = __float_as_uint(__fmaf_rn(c[i], -0.5f, half)) & 0x7FFFFFFFu;
     }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) key[i] = (key[i] & ~kIdx) | (uint32_t)(sub * NV + i);
     merge_step<NV, 1, 1>(key);
     // a token's best keys, and the one behind them
     __shared__ uint32_t chosen[kWarps][32 / L][L + 1];
@@ -318,73 +550,89 @@ __global__ void __launch_bounds__(kWarps * 32) gate_scored_kernel(ScoredParams p
         const bool own = key[0] == mn;
         if (own) out[r] = mn;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) key[i] = own ? (i + 1 < NV ? key[(i + 1) % NV] : kNoKey) : key[i];
+        for (int i = 0; i < NV; ++i)
+            key[i] = own ? (i + 1 < NV ? key[(i + 1) % NV] : 0x7FFFFFFFu) : key[i];
     }
     __syncwarp();
     auto expert_of = [&](uint32_t k) {
         const Place b = place_of(p, (int)((k & kIdx) / NV));
         return b.j0 + (int)(k & kIdx) % NV;
     };
-    // whether a key that differs from the one behind the choices by its index alone is
-    // left: its c can be above by the width of what the index took
-    const uint32_t last = out[p.top_k];
-    const bool hidden = ((lanes_min<L>(key[0]) ^ last) & ~kIdx) == 0u;
+    const uint32_t rest = lanes_min<L>(key[0]);  // the best key that is left
     int id = -1;
     float v = 0.0f, b = 0.0f, cv = -kInf;
-    if (sub <= p.top_k && out[sub] != kNoKey) {
+    if (sub <= p.top_k && out[sub] < none) {
         id = expert_of(out[sub]);
-        v = load_logit<DT>(row, id);
-        if (p.bias) b = __ldg(p.bias + id);
+        v = load_any(row, id, p.dt);
+        if (BIAS) b = __ldg(p.bias + id);
         cv = value(v, b);
     }
-    float vn = __shfl_down_sync(kAll, v, 1, L), bn = __shfl_down_sync(kAll, b, 1, L);
-    float cn = __shfl_down_sync(kAll, cv, 1, L);
-    if (sub == L - 1 && p.top_k == L) {
-        cn = -kInf;
-        if (last != kNoKey) {
-            const int j = expert_of(last);
-            vn = load_logit<DT>(row, j);
-            if (p.bias) bn = __ldg(p.bias + j);
-            cn = value(vn, bn);
-        }
+    // two neighbours that are not decided (of the same logit and bias the lower index
+    // is first); lane top_k has the one behind the choices
+    const float vn = __shfl_down_sync(kAll, v, 1, L), bn = __shfl_down_sync(kAll, b, 1, L);
+    const float cn = __shfl_down_sync(kAll, cv, 1, L);
+    const float near =
+        rounded ? __fadd_rn(tol, __fmul_rn(fmaxf(fabsf(cv), fabsf(cn)), 0x1p-22f)) : 0.0f;
+    const bool unsure = !whole && sub < p.top_k && sub < L - 1 && cn > -kInf && (v != vn || b != bn) &&
+                        !(__fadd_rn(cv, -cn) > near);
+    // the last choice and what is left, of which a bound is known (an index took the
+    // key's low bits)
+    bool all = !whole && top == kInf;
+    if (!whole && sub == p.top_k - 1 && id >= 0) {
+        uint32_t left = rest;
+        if (p.top_k == L) left = min(left, out[L]);  // no lane has the one behind
+        const float bound = __fadd_rn(top, -2.0f * __uint_as_float(left & ~kIdx));
+        const float slack = __fmul_rn(__fadd_rn(fabsf(top), fabsf(bound)), 0x1p-22f);
+        all |= left < none && !(__fadd_rn(cv, -bound) > __fadd_rn(near, slack));
     }
-    const bool border = sub == p.top_k - 1 && hidden;
-    // the same logit and bias: the lower index is first
-    if (sub < p.top_k && id >= 0 && cn > -kInf && (border || v != vn || b != bn)) {
-        float near = p.bias && !plain
-                         ? __fadd_rn(tol, __fmul_rn(fmaxf(fabsf(cv), fabsf(cn)), 0x1p-22f))
-                         : 0.0f;
-        if (border) near = __fadd_rn(near, __fmul_rn(__fadd_rn(top, -cn), (kIdx + 1u) * 0x1p-22f));
-        unsure |= !(__fadd_rn(cv, -cn) > near);
+    const Token token{m, plain, tol};
+    if (__any_sync(kAll, all)) {
+        id = choose_again(p, row, lane, L, in, token);
+        if (id >= 0) v = load_any(row, id, p.dt);
+    } else if (__any_sync(kAll, unsure)) {
+        // the same choices and the one behind them, their values as pairs
+        uint64_t key64 = float_key(v);
+        if (BIAS) {
+            Pair sum = {1.0f, 0.0f};
+            if (!SIGMOID) sum = total_pair(p, row, lane, L, m);
+            if (!plain) key64 = value_key(SIGMOID, v, b, m, sum);
+        }
+        int rank = 0;
+#pragma unroll 1
+        for (int r = 0; r <= min(p.top_k, L - 1); ++r) {
+            const uint64_t u = __shfl_sync(kAll, (unsigned long long)key64, r, L);
+            const int j = __shfl_sync(kAll, id, r, L);
+            rank += j >= 0 && (u > key64 || (u == key64 && j < id));
+        }
+        if (sub <= p.top_k) out[sub] = 0xFFFFFFFFu;
+        __syncwarp();
+        if (id >= 0) out[rank] = (uint32_t)id;
+        __syncwarp();
+        id = sub < p.top_k ? (int)out[sub] : -1;
+        if (id >= 0) v = load_any(row, id, p.dt);
     }
     if (sub >= p.top_k) id = -1;
-    if (__any_sync(kAll, unsure)) {
-        id = choose_64(p, row, DT, lane, L);
-        if (id >= 0) v = load_logit<DT>(row, id);
-    }
     // the weights
     const bool some = __shfl_sync(kAll, id, 0, L) >= 0;
     float s = 0.0f, sum = 0.0f;
-    if (p.sigmoid) {
+    if (SIGMOID) {
         if (id >= 0) s = sigmoid_exact(v);
         sum = p.normalize ? s : 1.0f;
     } else if (p.normalize) {
         // relative to the largest of the chosen
-        float mc = id >= 0 ? v : -kInf;
-#pragma unroll
-        for (int o = L / 2; o; o >>= 1) mc = fmaxf(mc, __shfl_xor_sync(kAll, mc, o));
+        const float mc = lanes_top<L>(id >= 0 && v == v ? v : -kInf);
         if (id >= 0) s = exp_diff(v, mc);
         sum = s;
     } else {
         if (id >= 0) s = exp_diff(v, m);
+        sum = total;
     }
     if (p.normalize) sum = lanes_sum<L>(sum);
-    if (!p.sigmoid && !p.normalize) sum = total;
-    // a NaN, or an infinity in a softmax, is seen in all of the token's weights
-#pragma unroll
-    for (int o = L / 2; o; o >>= 1) nan |= __shfl_xor_sync(kAll, (int)nan, o) != 0;
     float w = sum > 0.0f ? __fmul_rn(__fdiv_rn(s, sum), p.scale) : 0.0f;
-    if (nan || plain) w = __int_as_float(0x7FFFFFFF);
+    // a NaN, or an infinity in a softmax, is seen in all of the token's weights
+    const uint32_t nans = __ballot_sync(kAll, nan);
+    if (plain || ((nans >> (lane - sub)) & (kAll >> (32 - L))) != 0u)
+        w = __int_as_float(0x7FFFFFFF);
     if (!some) w = 0.0f;
     if (active && sub < p.top_k) {
         int32_t *ids = p.ids + t * p.top_k + sub;
@@ -475,11 +723,15 @@ __global__ void __launch_bounds__(kWarps * 32) gate_chosen_grad_kernel(ChosenGra
         store_logit<DT>(out, id, d);
 }
 
-template <int DT, int NV, int L>
+template <int NV, int L>
 cudaError_t run_lanes(const ScoredParams &p, cudaStream_t s) {
     const int64_t per_cta = kWarps * 32 / L;
-    return launch_pdl(gate_scored_kernel<DT, NV, L>,
-                      (unsigned)((p.num_tokens + per_cta - 1) / per_cta), kWarps * 32, 0, s, p);
+    auto *kern = p.sigmoid ? (p.bias ? gate_scored_kernel<NV, L, true, true>
+                                     : gate_scored_kernel<NV, L, true, false>)
+                           : (p.bias ? gate_scored_kernel<NV, L, false, true>
+                                     : gate_scored_kernel<NV, L, false, false>);
+    return launch_pdl(kern, (unsigned)((p.num_tokens + per_cta - 1) / per_cta), kWarps * 32, 0, s,
+                      p);
 }
 
 // The lanes and logits per lane of a token's groups on L lanes; false where a
@@ -502,15 +754,14 @@ bool lay_out(ScoredParams &p, int L, int size) {
     return true;
 }
 
-template <int DT>
 cudaError_t run_scored(ScoredParams p, cudaStream_t s) {
-    if (!lay_out(p, 32, kSize<DT>)) return cudaErrorNotSupported;
-    return p.per_lane <= 1    ? run_lanes<DT, 1, 32>(p, s)
-           : p.per_lane <= 2  ? run_lanes<DT, 2, 32>(p, s)
-           : p.per_lane <= 4  ? run_lanes<DT, 4, 32>(p, s)
-           : p.per_lane <= 8  ? run_lanes<DT, 8, 32>(p, s)
-           : p.per_lane <= 16 ? run_lanes<DT, 16, 32>(p, s)
-                              : run_lanes<DT, 32, 32>(p, s);
+    if (!lay_out(p, 32, p.dt == MOEQ_FP32 ? 4 : 2)) return cudaErrorNotSupported;
+    return p.per_lane <= 1    ? run_lanes<1, 32>(p, s)
+           : p.per_lane <= 2  ? run_lanes<2, 32>(p, s)
+           : p.per_lane <= 4  ? run_lanes<4, 32>(p, s)
+           : p.per_lane <= 8  ? run_lanes<8, 32>(p, s)
+           : p.per_lane <= 16 ? run_lanes<16, 32>(p, s)
+                              : run_lanes<32, 32>(p, s);
 }
 
 template <int DT>
@@ -533,6 +784,7 @@ cudaError_t launch_gate_scored(const GateScoredArgs &a, cudaStream_t s) {
     p.logits = static_cast<const uint8_t *>(a.logits);
     p.stride = a.stride * size;
     p.num_tokens = a.num_tokens;
+    p.dt = a.dtype;
     p.E = a.num_experts;
     p.top_k = a.top_k;
     p.bias = a.bias;
@@ -545,9 +797,7 @@ cudaError_t launch_gate_scored(const GateScoredArgs &a, cudaStream_t s) {
     p.ids = a.ids;
     p.weights = a.weights;
     p.err = a.err;
-    if (a.dtype == MOEQ_BF16) return run_scored<MOEQ_BF16>(p, s);
-    if (a.dtype == MOEQ_FP16) return run_scored<MOEQ_FP16>(p, s);
-    return run_scored<MOEQ_FP32>(p, s);
+    return run_scored(p, s);
 }
 
 cudaError_t launch_gate_chosen_grad(const GateArgs &a, bool sigmoid, cudaStream_t s) {
