@@ -37,6 +37,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kMaxPerLane = 32;
+constexpr int64_t kManyTokens = 4096;
 
 struct ScoredParams {
     const uint8_t *logits;
@@ -47,7 +48,7 @@ struct ScoredParams {
     int sigmoid, top2, normalize;
     int groups, topk_groups;
     int group_size, lane_shift, per_lane;  // 1 << lane_shift lanes a group, per_lane logits each
-    int vec;                               // a lane's logits are aligned vectors
+    int vec, bias_vec;                     // a lane's logits, biases are aligned vectors
     float scale;
     int32_t *ids;
     float *weights;
@@ -86,10 +87,11 @@ constexpr float kSoftmaxTol = 5e-6f;
 // without the total, exp alone
 constexpr float kExpTol = 6e-7f;
 
-// sigmoid(x) for the weights: within a few ulp of either end.
+// sigmoid(x) for the weights: within 4 ulp at either end (exp 2, the sum half, 1 / x one
+// and the product half).
 __device__ __forceinline__ float sigmoid_exact(float x) {
     const float e = expf(-fabsf(x));
-    return __fdiv_rn(x >= 0.0f ? 1.0f : e, __fadd_rn(1.0f, e));
+    return __fmul_rn(x >= 0.0f ? 1.0f : e, rcp_fast(__fadd_rn(1.0f, e)));
 }
 
 template <int L>
@@ -421,12 +423,9 @@ __global__ void __launch_bounds__(kWarps * 32) gate_scored_kernel(ScoredParams p
         load_row<MOEQ_BF16>(row, a.j0 + a.n, a.j0, p.vec, x);
     else
         load_row<MOEQ_FP16>(row, a.j0 + a.n, a.j0, p.vec, x);
-    bool nan = false, masked = false;
+    bool usable = true;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        nan |= x[i] != x[i];
-        masked |= !(x[i] > -kInf);
-    }
+    for (int i = 0; i < NV; ++i) usable &= x[i] > -kInf;
     float m = -kInf, total = 0.0f, inv = 0.0f;
     bool plain = false;  // no softmax: by the logits
     float e[NV];
@@ -439,7 +438,8 @@ __global__ void __launch_bounds__(kWarps * 32) gate_scored_kernel(ScoredParams p
             e[i] = exp_fast(x[i], m);
             total = __fadd_rn(total, e[i]);
         }
-        total = m > -kInf ? lanes_sum<L>(total) : 0.0f;
+        total = lanes_sum<L>(total);
+        if (!(m > -kInf)) total = 0.0f;
         inv = rcp_fast(total);
         plain = !(total < kInf);  // NaN: a NaN logit, or m infinite
     }
@@ -450,16 +450,42 @@ __global__ void __launch_bounds__(kWarps * 32) gate_scored_kernel(ScoredParams p
         return plain ? v : __fadd_rn(__fmul_rn(exp_fast(v, m), inv), b);
     };
     float c[NV];
+    if constexpr (BIAS) {
+        if (p.bias_vec && a.n == NV) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const float b = BIAS && i < a.n ? __ldg(p.bias + a.j0 + i) : 0.0f;
-        c[i] = BIAS && !SIGMOID ? (plain ? x[i] : __fadd_rn(__fmul_rn(e[i], inv), b))
-                                : value(x[i], b);
+            for (int i = 0; i < NV; i += 4) {
+                const float4 u = __ldg(reinterpret_cast<const float4 *>(p.bias + a.j0 + i));
+                c[i] = u.x;
+                if (i + 3 < NV) {
+                    c[(i + 1) % NV] = u.y;
+                    c[(i + 2) % NV] = u.z;
+                    c[(i + 3) % NV] = u.w;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) c[i] = i < a.n ? __ldg(p.bias + a.j0 + i) : 0.0f;
+        }
+        // a NaN as -inf
+        if constexpr (SIGMOID) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) c[i] = fmaxf(value(x[i], c[i]), -kInf);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                c[i] = fmaxf(plain ? x[i] : __fadd_rn(__fmul_rn(e[i], inv), c[i]), -kInf);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) c[i] = x[i];
     }
-    // a NaN bias's too
-    if (BIAS || __any_sync(kAll, masked)) {
+    bool nan = false;
+    if (__any_sync(kAll, !usable)) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) c[i] = x[i] > -kInf && c[i] > -kInf ? c[i] : -kInf;
+        for (int i = 0; i < NV; ++i) {
+            nan |= x[i] != x[i];
+            c[i] = x[i] > -kInf ? c[i] : -kInf;
+        }
     }
     // How far apart two values are decided: twice the scores' bound, and the rounding of
     // the sums with the bias (2^-24 each, taken as 2^-22).
@@ -501,7 +527,8 @@ __global__ void __launch_bounds__(kWarps * 32) gate_scored_kernel(ScoredParams p
                 key = 0u;
             }
         }
-        if (sum || rounded) {
+        // (the tokens of a warp may differ in plain: what is between lanes runs for all)
+        if (p.top2 || BIAS) {
             // the border between the last group chosen and the first that is not
             const uint32_t next = lanes_max<L>(key);
             const uint32_t has = __ballot_sync(kAll, key == next) >> (lane - sub);
@@ -510,7 +537,7 @@ __global__ void __launch_bounds__(kWarps * 32) gate_scored_kernel(ScoredParams p
                                      __shfl_sync(kAll, size, __ffs((int)has) - 1, L));
             const float bound = BIAS || SIGMOID ? tol : 2.0f * kExpTol;
             const bool unsure =
-                next > kNegInfKey && !(__fadd_rn(key_value(border), -key_value(next)) >
+                (sum || rounded) && next > kNegInfKey && !(__fadd_rn(key_value(border), -key_value(next)) >
                                        __fadd_rn(2.0f * bound, __fmul_rn(most, 0x1p-20f)));
             if (__any_sync(kAll, unsure))
                 in = groups_again(p, row, lane, L, Token{m, plain, bound});
@@ -542,7 +569,9 @@ __global__ void __launch_bounds__(kWarps * 32) gate_scored_kernel(ScoredParams p
 #pragma unroll
     for (int i = 0; i < NV; ++i) key[i] = (key[i] & ~kIdx) | (uint32_t)(sub * NV + i);
     merge_step<NV, 1, 1>(key);
-    // a token's best keys, and the one behind them
+    // a token's best keys, and the one behind them; of a lane's at most as many as that
+    // (top_k <= L) and one are looked at
+    constexpr int kKeep = NV < L + 2 ? NV : L + 2;
     __shared__ uint32_t chosen[kWarps][32 / L][L + 1];
     uint32_t *out = chosen[threadIdx.x >> 5][lane / L];
     for (int r = 0; r <= p.top_k; ++r) {
@@ -550,8 +579,8 @@ __global__ void __launch_bounds__(kWarps * 32) gate_scored_kernel(ScoredParams p
         const bool own = key[0] == mn;
         if (own) out[r] = mn;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            key[i] = own ? (i + 1 < NV ? key[(i + 1) % NV] : 0x7FFFFFFFu) : key[i];
+        for (int i = 0; i < kKeep; ++i)
+            key[i] = own ? (i + 1 < kKeep ? key[(i + 1) % NV] : 0x7FFFFFFFu) : key[i];
     }
     __syncwarp();
     auto expert_of = [&](uint32_t k) {
@@ -734,34 +763,52 @@ cudaError_t run_lanes(const ScoredParams &p, cudaStream_t s) {
                       p);
 }
 
-// The lanes and logits per lane of a token's groups on L lanes; false where a
-// lane would hold more than kMaxPerLane.
-bool lay_out(ScoredParams &p, int L, int size) {
+// The lanes and logits per lane of a token's groups on L lanes, and the registers that
+// a lane needs for them (a power of two); 0 where they do not fit.
+int lay_out(ScoredParams &p, int L) {
+    const int size = p.dt == MOEQ_FP32 ? 4 : 2;
     int lanes = L;  // of a group
     while (lanes > 0 && lanes * p.groups > L) lanes /= 2;
-    if (lanes == 0) return false;
+    if (lanes == 0 || p.top_k > L) return 0;
     p.group_size = p.E / p.groups;
     p.per_lane = (p.group_size + lanes - 1) / lanes;
-    if (p.per_lane > kMaxPerLane) return false;
+    if (p.per_lane > kMaxPerLane) return 0;
     p.lane_shift = 0;
     while ((1 << p.lane_shift) < lanes) ++p.lane_shift;
     int nv = 1;
     while (nv < p.per_lane) nv *= 2;
     if (p.groups == 1) p.per_lane = nv;  // whole vectors
     const int bytes = std::min(nv * size, 16);
-    p.vec = p.per_lane == nv && p.stride % bytes == 0 && p.group_size * size % bytes == 0;
-    if (p.groups == 1) p.vec = p.stride % bytes == 0;
-    return true;
+    const bool whole = p.per_lane == nv;  // lanes begin at multiples of nv in their group
+    p.vec = whole && p.stride % bytes == 0 && (p.groups == 1 || p.group_size * size % bytes == 0);
+    p.bias_vec = whole && nv % 4 == 0 && (p.groups == 1 || p.group_size % 4 == 0);
+    return nv;
 }
 
 cudaError_t run_scored(ScoredParams p, cudaStream_t s) {
-    if (!lay_out(p, 32, p.dt == MOEQ_FP32 ? 4 : 2)) return cudaErrorNotSupported;
-    return p.per_lane <= 1    ? run_lanes<1, 32>(p, s)
-           : p.per_lane <= 2  ? run_lanes<2, 32>(p, s)
-           : p.per_lane <= 4  ? run_lanes<4, 32>(p, s)
-           : p.per_lane <= 8  ? run_lanes<8, 32>(p, s)
-           : p.per_lane <= 16 ? run_lanes<16, 32>(p, s)
-                              : run_lanes<32, 32>(p, s);
+    if (p.num_tokens >= kManyTokens) {
+        ScoredParams q = p;
+        const int nv = lay_out(q, 8);
+        if (nv == 32) return run_lanes<32, 8>(q, s);
+        if (nv == 16) return run_lanes<16, 8>(q, s);
+        if (nv == 8) return run_lanes<8, 8>(q, s);
+        if (nv == 4) return run_lanes<4, 8>(q, s);
+    }
+    if (p.num_tokens >= kManyTokens) {
+        ScoredParams q = p;
+        const int nv = lay_out(q, 16);
+        if (nv == 32) return run_lanes<32, 16>(q, s);
+        if (nv == 16) return run_lanes<16, 16>(q, s);
+        if (nv == 8) return run_lanes<8, 16>(q, s);
+    }
+    const int nv = lay_out(p, 32);
+    return nv == 0    ? cudaErrorNotSupported
+           : nv == 1  ? run_lanes<1, 32>(p, s)
+           : nv == 2  ? run_lanes<2, 32>(p, s)
+           : nv == 4  ? run_lanes<4, 32>(p, s)
+           : nv == 8  ? run_lanes<8, 32>(p, s)
+           : nv == 16 ? run_lanes<16, 32>(p, s)
+                      : run_lanes<32, 32>(p, s);
 }
 
 template <int DT>

@@ -156,6 +156,54 @@ def test_many_tokens_with_ties(T, score):
         assert np.array_equal(ids.cpu().numpy(), np.tile(ref, ((T + 4) // 5, 1))[:T])
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,G,some,k", [(256, 8, 4, 8), (64, 1, 1, 4), (160, 8, 3, 6), (512, 16, 5, 12),
+                                        (128, 4, 2, 16), (40, 2, 1, 3), (256, 1, 1, 8), (250, 5, 3, 9),
+                                        (32, 8, 8, 8), (1024, 32, 9, 17), (9, 1, 1, 2)])
+def test_many_tokens_against_oracle(E, G, some, k, score, dtype):
+    """Fewer lanes for each of many tokens: 47 rows, over and over."""
+    rng = np.random.default_rng(E + k)
+    n, T = 47, 20001
+    x = torch.from_numpy(rng.normal(size=(n, E)) * 1.5).to(dtype)
+    x[::5, 2::3] = float("-inf")
+    x[1, 3], x[2, 4] = float("nan"), float("inf")
+    x[3] = x[3, 0]
+    bias = torch.from_numpy(rng.normal(size=E) * (0.1 if score == "sigmoid" else 1.0 / E)).float()
+    many = x.repeat((T + n - 1) // n, 1)[:T].to(DEV)
+    for b in (None, bias):
+        for group_score in ("top2", "max"):
+            kw = dict(num_groups=G, topk_groups=some, score=score, group_score=group_score)
+            ids, w = _gate(many, k, b, **kw)
+            ref_ids, ref_w = _want(x, k, b, **kw)
+            for a in range(0, T, n):
+                m = min(n, T - a)
+                assert torch.equal(ids[a:a + m], ids[:m])
+                assert torch.equal(w[a:a + m].view(torch.int32), w[:m].view(torch.int32))
+            assert np.array_equal(ids[:n].cpu().numpy(), ref_ids)
+            got, nan = f64(w[:n]), np.isnan(ref_w)
+            assert np.array_equal(np.isnan(got), nan)
+            ref_w = np.where(nan, 0.0, ref_w)
+            rows = np.where(np.isfinite(f64(x)), f64(x), -np.inf)
+            assert np.all(np.abs(np.where(nan, 0.0, got) - ref_w)
+                          <= _rel(rows, k, score) * ref_w + 2.0 ** -120)
+
+
+@pytest.mark.parametrize("E,G,k", [(256, 8, 8), (128, 1, 8), (512, 4, 16)])
+def test_many_tokens_that_fp32_does_not_decide(E, G, k):
+    """As above, a few such tokens among many, and all of them."""
+    rng = np.random.default_rng(E + 1)
+    x = rng.normal(size=(1, E)).astype(np.float32)
+    bias = (1.25 - L.scores(x, "sigmoid")[0]).astype(np.float32)
+    rows = np.concatenate([x, rng.normal(size=(29, E)).astype(np.float32)])
+    kw = dict(num_groups=G, topk_groups=max(1, G // 2))
+    ref, _ = _want(torch.from_numpy(rows), k, torch.from_numpy(bias), **kw)
+    for n in (1, 30):
+        many = torch.from_numpy(rows[:n]).repeat(18000 // n, 1)
+        ids, _ = _gate(many, k, torch.from_numpy(bias), **kw)
+        assert np.array_equal(ids.cpu().numpy(), np.tile(ref[:n], (18000 // n, 1)))
+
+
 def test_rows_without_choices_and_values_that_are_none():
     inf, nan = float("inf"), float("nan")
     low = torch.finfo(torch.float32).min
