@@ -37,7 +37,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kMaxPerLane = 32;
-constexpr int64_t kManyTokens = 4096;
 
 struct ScoredParams {
     const uint8_t *logits;
@@ -173,18 +172,20 @@ __device__ __forceinline__ Pair reciprocal(Pair d) {
     return quick_sum(r, __fmul_rn(r, __fmaf_rn(e, e, e)));
 }
 
-// exp(x), x <= 0, within 2^-45: 2^n e^f with n = x / ln 2 to the nearest, ln 2 in three
+// exp(x), x <= 0, within 2^-44: 2^n e^f with n = x / ln 2 to the nearest, ln 2 in three
 // parts of which the first leaves n times it exact, and the Taylor series of e^f, |f| <=
-// 0.35, to the 13th power.
+// 0.35, to the 13th power (from the 8th on, below 2^-22 of the sum, in fp32).
 __device__ __noinline__ Pair exp_pair(Pair x) {
     const float n = rintf(__fmul_rn(x.hi, kLog2e));
     if (!(n >= -126.0f)) return {0.0f, 0.0f};
     Pair f = two_sum(__fmaf_rn(n, -0x1.62ep-1f, x.hi), x.lo);
     f = add(f, mul({-n, 0.0f}, {0x1.0bfbe8p-15f, 0x1.cf79acp-40f}));
-    Pair p = {1.0f, 0.0f};
+    float q = 1.0f, k = 13.0f;
 #pragma unroll 1
-    for (float k = 13.0f; k > 0.0f; k -= 1.0f)
-        p = add({1.0f, 0.0f}, mul(mul(p, f), reciprocal({k, 0.0f})));
+    for (; k > 7.0f; k -= 1.0f) q = __fmaf_rn(__fmul_rn(q, f.hi), rcp_fast(k), 1.0f);
+    Pair p = {q, 0.0f};
+#pragma unroll 1
+    for (; k > 0.0f; k -= 1.0f) p = add({1.0f, 0.0f}, mul(mul(p, f), reciprocal({k, 0.0f})));
     const float scale = __uint_as_float((uint32_t)((int)n + 127) << 23);
     return {__fmul_rn(p.hi, scale), __fmul_rn(p.lo, scale)};
 }
@@ -317,6 +318,35 @@ __device__ __noinline__ bool groups_again(const ScoredParams &p, const uint8_t *
             }
         if (!__any_sync(kAll, more)) return rank < p.topk_groups;
     }
+}
+
+// The border between two groups, the last that is chosen (side 1) and the first that is
+// not (side 2), where no third is near: whether the second comes first.  The lanes of the
+// two know, by bits of `terms`, which of their values can be among those that count.
+__device__ __noinline__ bool swap_groups(const ScoredParams &p, const uint8_t *row, int lane, int L,
+                                         Token k, int side, uint32_t terms, int one, int other) {
+    constexpr unsigned kAll = 0xFFFFFFFFu;
+    const Place a = place_of(p, lane % L);
+    const bool bias = p.bias && !k.plain;
+    Pair total = {1.0f, 0.0f};
+    if (!p.sigmoid && p.bias) total = total_pair(p, row, lane, L, k.m);
+    uint64_t g1 = 0u, g2 = 0u;
+#pragma unroll 1
+    for (uint32_t todo = side ? terms : 0u; todo; todo &= todo - 1) {
+        const int j = a.j0 + __ffs((int)todo) - 1;
+        const uint64_t c = value_key(p.sigmoid, load_any(row, j, p.dt),
+                                     bias ? __ldg(p.bias + j) : 0.0f, k.m, total);
+        best_two(g1, g2, c, (uint64_t)0u);
+    }
+#pragma unroll 1
+    for (int o = (1 << p.lane_shift) / 2; o; o >>= 1) {
+        const uint64_t b1 = shfl_xor_key(g1, o), b2 = shfl_xor_key(g2, o);
+        best_two(g1, g2, b1, b2);
+    }
+    if (p.top2 && g2 != 0u) g1 = pair_key(add(key_pair(g1), key_pair(g2)));
+    const uint64_t u = __shfl_sync(kAll, (unsigned long long)g1, one, L);
+    const uint64_t v = __shfl_sync(kAll, (unsigned long long)g1, other, L);
+    return v > u || (v == u && other < one);
 }
 
 // The choice from all of a token's values, for a warp with one that the kept keys do not
@@ -528,19 +558,46 @@ __global__ void __launch_bounds__(kWarps * 32) gate_scored_kernel(ScoredParams p
             }
         }
         // (the tokens of a warp may differ in plain: what is between lanes runs for all)
-        if (p.top2 || BIAS) {
+        if (p.topk_groups < p.groups && (p.top2 || BIAS)) {
             // the border between the last group chosen and the first that is not
             const uint32_t next = lanes_max<L>(key);
             const uint32_t has = __ballot_sync(kAll, key == next) >> (lane - sub);
+            const int other = __ffs((int)has) - 1;
             const float size = __fadd_rn(fabsf(g1), two ? fabsf(g2) : 0.0f);
-            const float most = fmaxf(__shfl_sync(kAll, size, at, L),
-                                     __shfl_sync(kAll, size, __ffs((int)has) - 1, L));
+            const float most =
+                fmaxf(__shfl_sync(kAll, size, at, L), __shfl_sync(kAll, size, other, L));
             const float bound = BIAS || SIGMOID ? tol : 2.0f * kExpTol;
+            const float near = __fadd_rn(2.0f * bound, __fmul_rn(most, 0x1p-20f));
+            const float vb = key_value(border), vn = key_value(next);
             const bool unsure =
-                (sum || rounded) && next > kNegInfKey && !(__fadd_rn(key_value(border), -key_value(next)) >
-                                       __fadd_rn(2.0f * bound, __fmul_rn(most, 0x1p-20f)));
-            if (__any_sync(kAll, unsure))
-                in = groups_again(p, row, lane, L, Token{m, plain, bound});
+                (sum || rounded) && next > kNegInfKey && !(__fadd_rn(vb, -vn) > near);
+            if (__any_sync(kAll, unsure)) {
+                // a third one as near, from either side
+                const int side = a.group == at >> p.lane_shift      ? 1
+                                 : a.group == other >> p.lane_shift ? 2
+                                                                    : 0;
+                const float wide = __fmaf_rn(size, 0x1p-19f, 2.0f * near);
+                const bool third = side == 0 && a.n > 0 && v > -kInf && unsure &&
+                                   !((in ? v - vn : vb - v) > wide);
+                const bool huge = unsure && !(most < 1e30f);
+                const Token token{m, plain, bound};
+                if (__any_sync(kAll, third || huge)) {
+                    in = groups_again(p, row, lane, L, token);
+                } else {
+                    uint32_t terms = 0u;
+                    const float low = two ? g2 : g1;
+                    const float from = __fadd_rn(low, -__fmaf_rn(fabsf(low), 0x1p-20f, bound));
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) {
+                        const float u = scores ? (SIGMOID ? score_fast(c[i]) : e[SIGMOID ? 0 : i])
+                                               : c[i];
+                        if (c[i] > -kInf && u >= from) terms |= 1u << i;
+                    }
+                    if (!unsure) terms = 0u;
+                    const bool swap = swap_groups(p, row, lane, L, token, side, terms, at, other);
+                    if (unsure && swap) in = side == 1 ? false : side == 2 ? true : in;
+                }
+            }
         }
         if (!in) {
 #pragma unroll
@@ -587,58 +644,102 @@ __global__ void __launch_bounds__(kWarps * 32) gate_scored_kernel(ScoredParams p
         const Place b = place_of(p, (int)((k & kIdx) / NV));
         return b.j0 + (int)(k & kIdx) % NV;
     };
-    const uint32_t rest = lanes_min<L>(key[0]);  // the best key that is left
+    uint32_t rest = lanes_min<L>(key[0]);  // the best key that is left
     int id = -1;
     float v = 0.0f, b = 0.0f, cv = -kInf;
-    if (sub <= p.top_k && out[sub] < none) {
-        id = expert_of(out[sub]);
-        v = load_any(row, id, p.dt);
-        if (BIAS) b = __ldg(p.bias + id);
-        cv = value(v, b);
-    }
+    auto candidate = [&]() {
+        if (out[sub] < none) {
+            id = expert_of(out[sub]);
+            v = load_any(row, id, p.dt);
+            if (BIAS) b = __ldg(p.bias + id);
+            cv = value(v, b);
+        }
+    };
+    if (sub <= p.top_k) candidate();
     // two neighbours that are not decided (of the same logit and bias the lower index
-    // is first); lane top_k has the one behind the choices
-    const float vn = __shfl_down_sync(kAll, v, 1, L), bn = __shfl_down_sync(kAll, b, 1, L);
-    const float cn = __shfl_down_sync(kAll, cv, 1, L);
+    // is first); lane top_k has the one behind the choices, or, with a choice in each lane,
+    // the last lane looks at it too
+    float vn = __shfl_down_sync(kAll, v, 1, L), bn = __shfl_down_sync(kAll, b, 1, L);
+    float cn = __shfl_down_sync(kAll, cv, 1, L);
+    const bool full = p.top_k == L;
+    int behind = -1;
+    if (full && out[L] < none) behind = expert_of(out[L]);
+    if (full && sub == L - 1) {
+        cn = -kInf;
+        if (behind >= 0) {
+            vn = load_any(row, behind, p.dt);
+            if (BIAS) bn = __ldg(p.bias + behind);
+            cn = value(vn, bn);
+        }
+    }
     const float near =
         rounded ? __fadd_rn(tol, __fmul_rn(fmaxf(fabsf(cv), fabsf(cn)), 0x1p-22f)) : 0.0f;
-    const bool unsure = !whole && sub < p.top_k && sub < L - 1 && cn > -kInf && (v != vn || b != bn) &&
-                        !(__fadd_rn(cv, -cn) > near);
-    // the last choice and what is left, of which a bound is known (an index took the
-    // key's low bits)
-    bool all = !whole && top == kInf;
-    if (!whole && sub == p.top_k - 1 && id >= 0) {
-        uint32_t left = rest;
-        if (p.top_k == L) left = min(left, out[L]);  // no lane has the one behind
+    bool unsure = !whole && sub < p.top_k && cn > -kInf && (v != vn || b != bn) &&
+                  !(__fadd_rn(cv, -cn) > near);
+    // whether what is left may be as good as the last choice: a bound of it is known (an
+    // index took the key's low bits)
+    auto open = [&](uint32_t left) {
         const float bound = __fadd_rn(top, -2.0f * __uint_as_float(left & ~kIdx));
         const float slack = __fmul_rn(__fadd_rn(fabsf(top), fabsf(bound)), 0x1p-22f);
-        all |= left < none && !(__fadd_rn(cv, -bound) > __fadd_rn(near, slack));
-    }
+        return !whole && sub == p.top_k - 1 && id >= 0 && left < none &&
+               !(__fadd_rn(cv, -bound) > __fadd_rn(near, slack));
+    };
+    bool all = !whole && top == kInf;
+    unsure |= open(rest);
     const Token token{m, plain, tol};
-    if (__any_sync(kAll, all)) {
-        id = choose_again(p, row, lane, L, in, token);
-        if (id >= 0) v = load_any(row, id, p.dt);
-    } else if (__any_sync(kAll, unsure)) {
-        // the same choices and the one behind them, their values as pairs
-        uint64_t key64 = float_key(v);
-        if (BIAS) {
-            Pair sum = {1.0f, 0.0f};
-            if (!SIGMOID) sum = total_pair(p, row, lane, L, m);
-            if (!plain) key64 = value_key(SIGMOID, v, b, m, sum);
-        }
-        int rank = 0;
+    if (__any_sync(kAll, unsure | all)) {
+        // more candidates, as many as there are lanes
+        int count = full ? L : p.top_k + 1;
+        if (__any_sync(kAll, open(rest))) {
 #pragma unroll 1
-        for (int r = 0; r <= min(p.top_k, L - 1); ++r) {
-            const uint64_t u = __shfl_sync(kAll, (unsigned long long)key64, r, L);
-            const int j = __shfl_sync(kAll, id, r, L);
-            rank += j >= 0 && (u > key64 || (u == key64 && j < id));
+            for (; count < L; ++count) {
+                const uint32_t mn = lanes_min<L>(key[0]);
+                const bool own = key[0] == mn;
+                if (own) out[count] = mn;
+#pragma unroll
+                for (int i = 0; i < kKeep; ++i)
+                    key[i] = own ? (i + 1 < kKeep ? key[(i + 1) % NV] : 0x7FFFFFFFu) : key[i];
+            }
+            __syncwarp();
+            if (sub > p.top_k) candidate();
+            rest = lanes_min<L>(key[0]);
+            all |= open(rest);
         }
-        if (sub <= p.top_k) out[sub] = 0xFFFFFFFFu;
-        __syncwarp();
-        if (id >= 0) out[rank] = (uint32_t)id;
-        __syncwarp();
-        id = sub < p.top_k ? (int)out[sub] : -1;
-        if (id >= 0) v = load_any(row, id, p.dt);
+        if (__any_sync(kAll, all)) {
+            id = choose_again(p, row, lane, L, in, token);
+        } else {
+            // the candidates by their values as pairs; with a choice in each lane the one
+            // behind them too, which every lane has
+            uint64_t key64 = float_key(v), last = 0u;
+            if (full && behind >= 0) last = float_key(load_any(row, behind, p.dt));
+            if (BIAS) {
+                Pair sum = {1.0f, 0.0f};
+                if (!SIGMOID) sum = total_pair(p, row, lane, L, m);
+                if (!plain) {
+                    key64 = value_key(SIGMOID, v, b, m, sum);
+                    if (full && behind >= 0)
+                        last = value_key(SIGMOID, load_any(row, behind, p.dt),
+                                         __ldg(p.bias + behind), m, sum);
+                }
+            }
+            int rank = behind >= 0 && (last > key64 || (last == key64 && behind < id));
+            int place = 0;  // of the one behind
+#pragma unroll 1
+            for (int r = 0; r < count; ++r) {
+                const uint64_t u = __shfl_sync(kAll, (unsigned long long)key64, r, L);
+                const int j = __shfl_sync(kAll, id, r, L);
+                rank += j >= 0 && (u > key64 || (u == key64 && j < id));
+                place += j >= 0 && (u > last || (u == last && j < behind));
+            }
+            __syncwarp();
+            out[sub] = 0xFFFFFFFFu;
+            __syncwarp();
+            if (id >= 0) out[rank] = (uint32_t)id;
+            if (behind >= 0 && sub == 0) out[place] = (uint32_t)behind;
+            __syncwarp();
+            id = (int)out[sub];
+        }
+        if (sub < p.top_k && id >= 0) v = load_any(row, id, p.dt);
     }
     if (sub >= p.top_k) id = -1;
     // the weights
@@ -786,18 +887,22 @@ int lay_out(ScoredParams &p, int L) {
 }
 
 cudaError_t run_scored(ScoredParams p, cudaStream_t s) {
-    if (p.num_tokens >= kManyTokens) {
-        ScoredParams q = p;
+    // Many tokens: few lanes each, so that what a token costs whatever its experts is
+    // shared by the tokens of a warp.  Forward, sigmoid with bias, bf16, 8 lanes (or 16)
+    // against 32: 65536 tokens x 64 experts, top-8, 14.2 / 36.4 us, x 128, top-4, 17.2 /
+    // 35.5, x 160, 8 groups, 33.3 / 52.6, x 256, 8 groups, 40.2 (45.0) / 51.6, x 512, 16
+    // groups (85.0) / 74.6; 4096 x 64 3.5 / 5.0, x 128 3.8 / 4.5, x 256 6.0 / 6.2; 2048 x
+    // 128 3.2 / 3.4, x 256 4.8 / 4.3
+    ScoredParams q = p;
+    if (p.num_tokens >= 4096) {
         const int nv = lay_out(q, 8);
         if (nv == 32) return run_lanes<32, 8>(q, s);
         if (nv == 16) return run_lanes<16, 8>(q, s);
         if (nv == 8) return run_lanes<8, 8>(q, s);
         if (nv == 4) return run_lanes<4, 8>(q, s);
     }
-    if (p.num_tokens >= kManyTokens) {
-        ScoredParams q = p;
+    if (p.num_tokens >= 8192) {
         const int nv = lay_out(q, 16);
-        if (nv == 32) return run_lanes<32, 16>(q, s);
         if (nv == 16) return run_lanes<16, 16>(q, s);
         if (nv == 8) return run_lanes<8, 16>(q, s);
     }
