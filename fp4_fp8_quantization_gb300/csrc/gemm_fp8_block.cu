@@ -86,7 +86,8 @@ struct BlockCfg {
     static constexpr bool ASYNC = ASYNC_;
     static constexpr int BUF_BYTES = ASYNC ? 32 * COLS_W * 2 : 2048;
     static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SUM_WARPS * BUF_BYTES + 1024;
-    static_assert(SMEM_BYTES + 12 * (kMaxGroups + 1) + 512 <= 227 * 1024, "shared memory per CTA");
+    static_assert(SMEM_BYTES + 12 * (kMaxGroups + 1) + 512 + SUM_WARPS * COLS_W * 4 <= 227 * 1024,
+                  "shared memory per CTA");
     static_assert(!ASYNC || COLS_W % 64 == 0, "boxes of 64 columns");
     // an MMA reads MMA_M rows of A, past a smaller m-block's end whatever is there
     static_assert(B_BYTES + SUM_WARPS * BUF_BYTES >= (MMA_M - BM) * BK, "A reads stay inside");
@@ -133,6 +134,14 @@ __device__ __forceinline__ uint32_t bf16x2(F2 v) {
 
 __device__ __forceinline__ F2 bf16x2_values(uint32_t w) {
     return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// 16 bytes to shared memory, waited for by the thread that asked.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() {
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // A load that may see an earlier tile's store (c over the residual).
@@ -184,6 +193,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // per group: tiles before it, first row, expert
     __shared__ uint32_t prefix[kMaxGroups + 1];
     __shared__ int first_row[kMaxGroups + 1], expert[kMaxGroups];
+    // each sum warp's part of the expert's bias
+    __shared__ __align__(16) float bias_part[EPI ? C::SUM_WARPS : 1][EPI ? C::COLS_W : 4];
 
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -374,7 +385,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // the last row takes that row's, its sums are dropped)
         struct Part {
             int row, nvalid, ncol;
-            const float *sa, *sb, *bias;
+            int expert;
+            const float *sa, *sb;
             __device__ bool work(int N) const { return nvalid > 0 && ncol < N; }
         };
         auto part_of = [&](uint32_t t) {
@@ -386,7 +398,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             w.ncol = tl.nb * C::BN + cgrp * C::COLS_W;
             w.sa = p.a_scales + (int64_t)(w.row + max(0, min(lane, w.nvalid - 1))) * KB;
             w.sb = p.b_scales + ((int64_t)e * NBLK + min(w.ncol / 128, NBLK - 1)) * KB;
-            w.bias = EPI && p.bias ? p.bias + (int64_t)e * p.N : nullptr;
+            w.expert = e;
             return w;
         };
         // each lane polls by itself: where the barrier completes while another
@@ -415,6 +427,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
             cur = nxt;
             const bool work = cur.work(p.N);
+            if constexpr (EPI) {
+                // on its way during the reduction; the last tile's has been read
+                __syncwarp();
+                if (work && p.bias && lane < C::COLS_W / 4 && cur.ncol + lane * 4 < p.N)
+                    copy_async16(smem_u32(&bias_part[warp - C::SUM_WARP0][lane * 4]),
+                                 p.bias + (int64_t)cur.expert * p.N + cur.ncol + lane * 4);
+            }
             F2 acc[C::COLS_W / 2];
 #pragma unroll
             for (int i = 0; i < C::COLS_W / 2; ++i) acc[i] = f2(0.0f, 0.0f);
@@ -568,6 +587,25 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         st_global_v4(o, v.x, v.y, v.z, v.w);
                 }
             };
+            // the residual of a chunk: the next one's is on its way from when this one's is in
+            // the staging buffer (two chunks' in registers spill: 407 -> 480 us below)
+            uint4 res[4];
+            auto residual = [&](int ch) {
+                const uint16_t *src = p.residual + at + ch * 32;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    res[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (lrow + 8 * i < cur.nvalid && cur.ncol + ch * 32 + k * 8 < p.N)
+                        res[i] = ld_global_v4(src + (int64_t)(8 * i) * p.N);
+                }
+            };
+            if constexpr (EPI) {
+                if (p.residual) residual(0);
+                if (p.bias) {
+                    copy_async_wait();
+                    __syncwarp();
+                }
+            }
 #pragma unroll
             for (int ch = 0; ch < C::CHUNKS_W; ++ch) {
                 const int nc = cur.ncol + ch * 32;
@@ -575,26 +613,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const bool in_n = nc + k * 8 < p.N;  // N is a multiple of 8
                 F2 *v = acc + ch * 16;
                 if constexpr (EPI) {
-                    // the residual's loads are in flight during the activation
-                    uint4 res[4];
-                    if (p.residual) {
-                        const uint16_t *src = p.residual + at + ch * 32;
+                    if (p.bias) {  // past N whatever is there
+                        const uint32_t bias_at = smem_u32(&bias_part[warp - C::SUM_WARP0][ch * 32]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            res[i] = make_uint4(0u, 0u, 0u, 0u);
-                            if (lrow + 8 * i < cur.nvalid && in_n)
-                                res[i] = ld_global_v4(src + (int64_t)(8 * i) * p.N);
+                        for (int j = 0; j < 8; ++j) {
+                            const uint4 b = ld_shared_v4(bias_at + j * 16);
+                            v[2 * j] = add2(v[2 * j], f2(__uint_as_float(b.x), __uint_as_float(b.y)));
+                            v[2 * j + 1] =
+                                add2(v[2 * j + 1], f2(__uint_as_float(b.z), __uint_as_float(b.w)));
                         }
-                    }
-                    if (cur.bias) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (nc + 4 * j < p.N) {
-                                const float4 b =
-                                    __ldg(reinterpret_cast<const float4 *>(cur.bias + nc) + j);
-                                v[2 * j] = add2(v[2 * j], f2(b.x, b.y));
-                                v[2 * j + 1] = add2(v[2 * j + 1], f2(b.z, b.w));
-                            }
                     }
                     if (p.z) {
                         __syncwarp();  // the last chunk has been read
@@ -608,6 +635,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             st_shared_v4(piece(i), res[i].x, res[i].y, res[i].z, res[i].w);
+                        if (ch + 1 < C::CHUNKS_W) residual(ch + 1);
                         __syncwarp();
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -626,6 +654,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
         }
         if (C::ASYNC && lane == 0) bulk_wait_all();
+        if constexpr (EPI) copy_async_wait();  // after giving up too
     }
 
     // this CTA's loads, MMAs and stores are all issued
