@@ -498,12 +498,53 @@ def _one_of(names, name, what):
     return code
 
 
-def _on_current_device(*tensors):
-    """The calls launch on the current device: every tensor lives there."""
-    at = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != at:
-            raise ValueError(f"a tensor on {t.device}: expected the current device, cuda:{at}")
+# The checks of the calls below: they launch on the current device, where every
+# tensor lives.  A small call takes little more than its checks, so that what is
+# right is seen in one expression (a host tensor's device is -1) and what is
+# wrong is looked at again for its message.
+
+def _on_current_device(dev):
+    if dev != (_raw_device() if _raw_device is not None else torch.cuda.current_device()):
+        raise ValueError(f"tensors on cuda:{dev}: expected the current device")
+
+
+def _matrix(t, name, dtype=None, shape=None, dev=None):
+    """(pointer, row stride, device) of a 2-D CUDA tensor, as _rows_of."""
+    if (isinstance(t, torch.Tensor) and t.is_contiguous() and t.dim() == 2
+            and (t.dtype in DTYPES if dtype is None else t.dtype is dtype)
+            and (shape is None or t.shape == shape)):
+        at = t.get_device()
+        if at >= 0 and (dev is None or at == dev):
+            return t.data_ptr(), t.shape[1], at
+    p = _rows_of(t, name, shape, dtype)
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
+    return p, _row_stride(t), t.get_device()
+
+
+def _array(t, shape, dtype, dev, name):
+    """Pointer of a contiguous tensor of this shape and dtype (or one of a tuple
+    of dtypes) on device dev."""
+    if (isinstance(t, torch.Tensor) and t.shape == shape and t.get_device() == dev
+            and (t.dtype is dtype or (type(dtype) is tuple and t.dtype in dtype))
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _shaped(t, shape, dtype, name)
+    raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
+
+
+def _groups(a_offsets, expert_ids, num_active_experts, dev):
+    """(pointer, pointer, groups) of a ragged group description."""
+    G = expert_ids.numel() if num_active_experts is None else num_active_experts
+    if expert_ids.numel() < G or a_offsets.numel() < G + 1:
+        raise ValueError(f"a_offsets, expert_ids: too short for {G} groups")
+    return (_array(a_offsets, a_offsets.shape, _U32, dev, "a_offsets"),
+            _array(expert_ids, expert_ids.shape, torch.int32, dev, "expert_ids"), G)
+
+
+def _checked(fn, status):
+    if status != 0:
+        raise MoeqError(fn, status)
 
 
 def gate_group_topk(logits, topk_ids, weights, bias=None, score="sigmoid", num_groups=1,
@@ -517,18 +558,19 @@ def gate_group_topk(logits, topk_ids, weights, bias=None, score="sigmoid", num_g
     first, ties to the lowest index; weights (fp32, out) their scores, divided by
     their sum (normalize), times scale.  logits bf16 / fp16 / fp32 [num_tokens,
     num_experts], -inf for a masked expert; id -1 and weight 0 where none is left."""
-    p = _rows_of(logits, "logits")
+    p, stride, dev = _matrix(logits, "logits")
     T, E = logits.shape
     k = _choices(topk_ids, T)
-    ids = _ptr(topk_ids, torch.int32, "topk_ids")
-    w = _shaped(weights, (T, k), torch.float32, "weights")
-    b = _shaped(bias, (E,), torch.float32, "bias", True)
-    _on_current_device(logits, topk_ids, weights, bias)
-    _call("moeq_gate_group_topk", DTYPES[logits.dtype], p, _row_stride(logits), T, E, b,
-          _one_of(SCORES, score, "score"), num_groups,
-          num_groups if topk_groups is None else topk_groups,
-          _one_of(GROUP_SCORES, group_score, "group_score"), k, bool(normalize), scale, ids, w,
-          _stream(stream))
+    shape = (T, k)
+    ids = _array(topk_ids, shape, torch.int32, dev, "topk_ids")
+    w = _array(weights, shape, torch.float32, dev, "weights")
+    b = None if bias is None else _array(bias, (E,), torch.float32, dev, "bias")
+    _on_current_device(dev)
+    _checked("moeq_gate_group_topk", (_lib or lib()).moeq_gate_group_topk(
+        DTYPES[logits.dtype], p, stride, T, E, b, _one_of(SCORES, score, "score"), num_groups,
+        num_groups if topk_groups is None else topk_groups,
+        _one_of(GROUP_SCORES, group_score, "group_score"), k, bool(normalize), scale, ids, w,
+        _stream(stream)))
 
 
 def gate_group_topk_grad(logits, topk_ids, d_weights, d_logits, score="sigmoid", normalize=True,
@@ -536,15 +578,17 @@ def gate_group_topk_grad(logits, topk_ids, d_weights, d_logits, score="sigmoid",
     """Gradient of gate_group_topk's weights, the choice taken as fixed: d_logits
     (out, the logits' dtype, contiguous) from d_weights fp32 [num_tokens, top_k]
     and the logits and topk_ids of the forward call."""
-    p = _rows_of(logits, "logits")
+    p, stride, dev = _matrix(logits, "logits")
     T, E = logits.shape
     k = _choices(topk_ids, T)
-    ids = _ptr(topk_ids, torch.int32, "topk_ids")
-    dw = _shaped(d_weights, (T, k), torch.float32, "d_weights")
-    dx = _shaped(d_logits, (T, E), logits.dtype, "d_logits")
-    _on_current_device(logits, topk_ids, d_weights, d_logits)
-    _call("moeq_gate_group_topk_grad", DTYPES[logits.dtype], p, _row_stride(logits), T, E,
-          _one_of(SCORES, score, "score"), k, bool(normalize), scale, ids, dw, dx, _stream(stream))
+    shape = (T, k)
+    ids = _array(topk_ids, shape, torch.int32, dev, "topk_ids")
+    dw = _array(d_weights, shape, torch.float32, dev, "d_weights")
+    dx = _array(d_logits, (T, E), logits.dtype, dev, "d_logits")
+    _on_current_device(dev)
+    _checked("moeq_gate_group_topk_grad", (_lib or lib()).moeq_gate_group_topk_grad(
+        DTYPES[logits.dtype], p, stride, T, E, _one_of(SCORES, score, "score"), k, bool(normalize),
+        scale, ids, dw, dx, _stream(stream)))
 
 
 def permute_topk(tokens, dst_info, rows, weights=None, stream=None):
@@ -661,16 +705,19 @@ def quantize_fp8_block_weight(w, out, scales, stream=None):
                   "scales"), _stream(stream))
 
 
-def _workspace(workspace, need, like):
-    """Pointer of a workspace of at least `need` bytes: the caller's, or a new
-    one (freed in stream order by PyTorch's allocator)."""
+def _workspace(workspace, need, stream, like, dev):
+    """(pointer, tensor) of a workspace of at least `need` bytes: the caller's, or
+    a new one (freed in the current stream's order by PyTorch's allocator, so not
+    for another stream)."""
     if need < 0:
         raise ValueError("sizes that the call does not take")
     if workspace is None:
+        if stream is not None:
+            raise ValueError("workspace: required with a stream")
         workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
     if workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace: {need} bytes expected")
-    return workspace, _ptr(workspace, None, "workspace")
+    return _array(workspace, workspace.shape, workspace.dtype, dev, "workspace"), workspace
 
 
 def add_rms_norm(x, weight, y=None, residual=None, h=None, q=None, scales=None, rstd=None,
@@ -681,21 +728,26 @@ def add_rms_norm(x, weight, y=None, residual=None, h=None, q=None, scales=None, 
     ceil(K / 128)] or, one for each row, [rows].  rstd (out, fp32 [rows]) is
     1 / rms, for the gradient.  x, residual, h, y [rows, K] and weight [K] of one
     type, bf16 / fp16 / fp32; h and y may be x or residual themselves."""
-    p = _rows_of(x, "x")
-    n, k = x.shape
+    p, xs, dev = _matrix(x, "x")
+    shape = x.shape
+    n, k = shape
     dt = x.dtype
-    pr = None if residual is None else _rows_of(residual, "residual", (n, k), dt)
-    pw = _shaped(weight, (k,), dt, "weight")
-    ph = _shaped(h, (n, k), dt, "h", True)
-    py = _shaped(y, (n, k), dt, "y", True)
-    pq = _shaped(q, (n, k), _U8, "q", True)
-    by_row = scales is not None and scales.dim() == 1
-    ps = _shaped(scales, (n,) if by_row else (n, _blocks128(k)), torch.float32, "scales", True)
-    pu = _shaped(rstd, (n,), torch.float32, "rstd", True)
-    _on_current_device(x, weight, y, residual, h, q, scales, rstd)
-    _call("moeq_add_rms_norm", DTYPES[dt], p, _row_stride(x), pr,
-          k if residual is None else _row_stride(residual), n, k, pw, eps, ph, py, pq, ps, by_row,
-          pu, _stream(stream))
+    pr, rs = None, k
+    if residual is not None:
+        pr, rs, _ = _matrix(residual, "residual", dt, shape, dev)
+    f32 = torch.float32
+    pw = _array(weight, (k,), dt, dev, "weight")
+    ph = None if h is None else _array(h, shape, dt, dev, "h")
+    py = None if y is None else _array(y, shape, dt, dev, "y")
+    pq = None if q is None else _array(q, shape, _U8, dev, "q")
+    by_row, ps = False, None
+    if scales is not None:
+        by_row = scales.dim() == 1
+        ps = _array(scales, (n,) if by_row else (n, _blocks128(k)), f32, dev, "scales")
+    pu = None if rstd is None else _array(rstd, (n,), f32, dev, "rstd")
+    _on_current_device(dev)
+    _checked("moeq_add_rms_norm", (_lib or lib()).moeq_add_rms_norm(
+        DTYPES[dt], p, xs, pr, rs, n, k, pw, eps, ph, py, pq, ps, by_row, pu, _stream(stream)))
 
 
 def add_rms_norm_grad_workspace(rows, K):
@@ -710,24 +762,24 @@ def add_rms_norm_grad(d_y, h, weight, rstd, d_x, d_weight=None, d_h=None, worksp
     reaches h along the residual stream; d_weight (out, fp32 [K]).  workspace:
     add_rms_norm_grad_workspace(rows, K) bytes, needed with d_weight; without
     one it is allocated, on the current stream (so give it with another)."""
-    p = _rows_of(d_y, "d_y")
-    n, k = d_y.shape
-    dt = d_y.dtype
-    ph = _rows_of(h, "h", (n, k), dt)
-    pd = None if d_h is None else _rows_of(d_h, "d_h", (n, k), dt)
-    pw = _shaped(weight, (k,), dt, "weight")
-    pu = _shaped(rstd, (n,), torch.float32, "rstd")
-    px = _shaped(d_x, (n, k), dt, "d_x")
-    pg = _shaped(d_weight, (k,), torch.float32, "d_weight", True)
-    ws = None
+    p, ys, dev = _matrix(d_y, "d_y")
+    shape = d_y.shape
+    n, k = shape
+    dt, f32 = d_y.dtype, torch.float32
+    ph, hs, _ = _matrix(h, "h", dt, shape, dev)
+    pd, ds = None, k
+    if d_h is not None:
+        pd, ds, _ = _matrix(d_h, "d_h", dt, shape, dev)
+    pw = _array(weight, (k,), dt, dev, "weight")
+    pu = _array(rstd, (n,), f32, dev, "rstd")
+    px = _array(d_x, shape, dt, dev, "d_x")
+    pg = ws = None
     if d_weight is not None:
-        if workspace is None and stream is not None:
-            raise ValueError("workspace: required with a stream")
-        workspace, ws = _workspace(workspace, add_rms_norm_grad_workspace(n, k), d_y)
-    _on_current_device(d_y, h, weight, rstd, d_x, d_weight, d_h, workspace)
-    _call("moeq_add_rms_norm_grad", DTYPES[dt], p, _row_stride(d_y), pd,
-          k if d_h is None else _row_stride(d_h), ph, _row_stride(h), n, k, pw, pu, px, pg, ws,
-          _stream(stream))
+        pg = _array(d_weight, (k,), f32, dev, "d_weight")
+        ws, workspace = _workspace(workspace, add_rms_norm_grad_workspace(n, k), stream, d_y, dev)
+    _on_current_device(dev)
+    _checked("moeq_add_rms_norm_grad", (_lib or lib()).moeq_add_rms_norm_grad(
+        DTYPES[dt], p, ys, pd, ds, ph, hs, n, k, pw, pu, px, pg, ws, _stream(stream)))
 
 
 def grouped_matmul_fp8_block(c, a, b, a_scales, b_scales, a_offsets, expert_ids,
@@ -758,22 +810,28 @@ def grouped_matmul_fp8_block_epilogue(c, a, b, a_scales, b_scales, a_offsets, ex
     row's expert) + residual, rounded once.  bias fp32 [E, N]; activation None,
     "relu", "silu", "gelu" or "gelu_tanh"; residual bf16 [rows, N] (may be c
     itself); z (out, bf16 [rows, N]) is the product with bias, for the gradient."""
-    G = expert_ids.numel() if num_active_experts is None else num_active_experts
-    E, N, K = b.shape
-    if expert_ids.numel() < G or a_offsets.numel() < G + 1:
-        raise ValueError(f"a_offsets, expert_ids: too short for {G} groups")
-    T = a.shape[0]
-    bf16, f32 = torch.bfloat16, torch.float32
-    args = (_shaped(c, (T, N), bf16, "c"), _shaped(a, (T, K), _U8, "a"), _ptr(b, _U8, "b"),
-            _shaped(a_scales, (T, _blocks128(K)), f32, "a_scales"),
-            _shaped(b_scales, (E, _blocks128(N), _blocks128(K)), f32, "b_scales"),
-            _shaped(bias, (E, N), f32, "bias", True),
-            _one_of(ACTIVATIONS, activation, "activation"),
-            _shaped(residual, (T, N), bf16, "residual", True), _shaped(z, (T, N), bf16, "z", True),
-            _ptr(a_offsets, _U32, "a_offsets"), _ptr(expert_ids, torch.int32, "expert_ids"))
-    _on_current_device(c, a, b, a_scales, b_scales, a_offsets, expert_ids, bias, residual, z)
-    _call("moeq_grouped_matmul_fp8_block_epilogue", *args, T, N, K, E, max_tokens_per_expert, G,
-          _stream(stream))
+    pa, _, dev = _matrix(a, "a", a.dtype)
+    T, K = a.shape
+    E, N, _ = b.shape
+    out, bf16, f32 = (T, N), torch.bfloat16, torch.float32
+    if a.dtype not in _U8:
+        raise TypeError(f"a: dtype {a.dtype}, expected one of {_U8}")
+    if not a.is_contiguous():
+        raise ValueError("a: must be contiguous")
+    ro, ids, G = _groups(a_offsets, expert_ids, num_active_experts, dev)
+    pc = _array(c, out, bf16, dev, "c")
+    pb = _array(b, (E, N, K), _U8, dev, "b")
+    kb = _blocks128(K)
+    psa = _array(a_scales, (T, kb), f32, dev, "a_scales")
+    psb = _array(b_scales, (E, _blocks128(N), kb), f32, dev, "b_scales")
+    pv = None if bias is None else _array(bias, (E, N), f32, dev, "bias")
+    pr = None if residual is None else _array(residual, out, bf16, dev, "residual")
+    pz = None if z is None else _array(z, out, bf16, dev, "z")
+    _on_current_device(dev)
+    _checked("moeq_grouped_matmul_fp8_block_epilogue",
+             (_lib or lib()).moeq_grouped_matmul_fp8_block_epilogue(
+                 pc, pa, pb, psa, psb, pv, _one_of(ACTIVATIONS, activation, "activation"), pr, pz,
+                 ro, ids, T, N, K, E, max_tokens_per_expert, G, _stream(stream)))
 
 
 def grouped_epilogue_grad_workspace(rows, N, num_active_experts):
@@ -791,25 +849,24 @@ def grouped_epilogue_grad(d_c, a_offsets, expert_ids, num_experts, z=None, activ
     as the forward call saved it, with an activation.  workspace:
     grouped_epilogue_grad_workspace(rows, N, groups) bytes, needed with d_bias;
     without one it is allocated, on the current stream (so give it with another)."""
-    G = expert_ids.numel() if num_active_experts is None else num_active_experts
-    if expert_ids.numel() < G or a_offsets.numel() < G + 1:
-        raise ValueError(f"a_offsets, expert_ids: too short for {G} groups")
-    p = _rows_of(d_c, "d_c", dtype=torch.bfloat16)
-    T, N = d_c.shape
+    p, cs, dev = _matrix(d_c, "d_c", torch.bfloat16)
+    shape = d_c.shape
+    T, N = shape
     bf16, f32 = torch.bfloat16, torch.float32
-    args = (p, _row_stride(d_c), _shaped(z, (T, N), bf16, "z", True),
-            _one_of(ACTIVATIONS, activation, "activation"), _shaped(q, (T, N), _U8, "q", True),
-            _shaped(scales, (T, _blocks128(N)), f32, "scales", True),
-            _shaped(d_z, (T, N), bf16, "d_z", True),
-            _shaped(d_bias, (num_experts, N), f32, "d_bias", True),
-            _ptr(a_offsets, _U32, "a_offsets"), _ptr(expert_ids, torch.int32, "expert_ids"))
-    ws = None
+    ro, ids, G = _groups(a_offsets, expert_ids, num_active_experts, dev)
+    pz = None if z is None else _array(z, shape, bf16, dev, "z")
+    pq = None if q is None else _array(q, shape, _U8, dev, "q")
+    ps = None if scales is None else _array(scales, (T, _blocks128(N)), f32, dev, "scales")
+    pd = None if d_z is None else _array(d_z, shape, bf16, dev, "d_z")
+    pv = ws = None
     if d_bias is not None:
-        if workspace is None and stream is not None:
-            raise ValueError("workspace: required with a stream")
-        workspace, ws = _workspace(workspace, grouped_epilogue_grad_workspace(T, N, G), d_c)
-    _on_current_device(d_c, a_offsets, expert_ids, z, q, scales, d_z, d_bias, workspace)
-    _call("moeq_grouped_epilogue_grad", *args, T, N, num_experts, G, ws, _stream(stream))
+        pv = _array(d_bias, (num_experts, N), f32, dev, "d_bias")
+        ws, workspace = _workspace(workspace, grouped_epilogue_grad_workspace(T, N, G), stream,
+                                   d_c, dev)
+    _on_current_device(dev)
+    _checked("moeq_grouped_epilogue_grad", (_lib or lib()).moeq_grouped_epilogue_grad(
+        p, cs, pz, _one_of(ACTIVATIONS, activation, "activation"), pq, ps, pd, pv, ro, ids, T, N,
+        num_experts, G, ws, _stream(stream)))
 
 
 def get_device_error(stream=None):
