@@ -962,7 +962,7 @@ int64_t moeq_grouped_epilogue_grad_workspace(int64_t total_tokens, int64_t N,
                                              int32_t num_active_experts) {
     if (epilogue_grad_sizes_ok(total_tokens, N, num_active_experts) != MOEQ_OK) return -1;
     return moeq::epilogue_grad_table_bytes(num_active_experts) +
-           moeq::epilogue_grad_tiles(total_tokens, num_active_experts) * N * 4;
+           moeq::epilogue_grad_tiles(total_tokens, N, num_active_experts) * N * 4;
 }
 
 moeq_status moeq_grouped_epilogue_grad(const void *d_c, int64_t d_c_stride, const void *z,

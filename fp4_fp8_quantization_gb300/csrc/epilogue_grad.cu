@@ -6,7 +6,7 @@
 //   d_bias[e] = sum over the rows of expert e of d_z (fp32, before any rounding)
 //
 // One pass: 4 bytes read and 1 (or 3) written per element.  A CTA takes tiles of
-// kRows rows of one group by 256 columns, a warp a row at a time, 16 lanes a
+// 64 to 256 rows of one group by 256 columns, a warp a row at a time, 16 lanes a
 // block; each thread sums its 8 columns over its rows, the warps join in shared
 // memory, and a tile leaves one row of partial sums.  A second kernel adds an
 // expert's rows of them in the order of groups and tiles: no atomics, the same
@@ -23,7 +23,6 @@ namespace moeq {
 
 namespace {
 
-constexpr int kRows = kEpilogueGradRows;
 constexpr int kWarps = 8;
 constexpr int kCols = 256;  // of a CTA: 32 lanes of 8
 
@@ -37,6 +36,7 @@ __device__ __forceinline__ void pairs8(const uint4 &u, F2 (&x)[4]) {
 struct EpilogueGradParams {
     const uint16_t *dc, *z;
     int64_t dc_stride, rows, N;
+    int tile_rows;
     const uint32_t *offsets;
     const int32_t *expert_ids;
     int num_groups, num_experts;
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) epilogue_grad_kernel(EpilogueG
         } else if (e < 0 || e >= p.num_experts) {
             if (first) set_error(p.err, MOEQ_DEVERR_BAD_EXPERT);
         } else {
-            n = (r1 - r0 + kRows - 1) / kRows;
+            n = (r1 - r0 + p.tile_rows - 1) / p.tile_rows;
         }
         prefix[g + 1] = n;
     }
@@ -119,14 +119,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2) epilogue_grad_kernel(EpilogueG
             const int mid = (lo + hi) >> 1;
             if (prefix[mid] <= t) lo = mid; else hi = mid;
         }
-        const int64_t r0 = (int64_t)__ldg(p.offsets + lo) + (int64_t)(t - prefix[lo]) * kRows;
-        const int rows = (int)min((int64_t)kRows, (int64_t)__ldg(p.offsets + lo + 1) - r0);
+        const int64_t r0 = (int64_t)__ldg(p.offsets + lo) + (int64_t)(t - prefix[lo]) * p.tile_rows;
+        const int rows = (int)min((int64_t)p.tile_rows, (int64_t)__ldg(p.offsets + lo + 1) - r0);
         F2 sum[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[i] = f2s(0.0f);
         constexpr int U = 4;  // rows of a warp that are worked on together
-        for (int base = warp; base < rows; base += U * kWarps) {
-            uint4 dc[U], zv[U];
+        uint4 dc[U], zv[U];
+        auto load = [&](int base) {
 #pragma unroll
             for (int j = 0; j < U; ++j) {
                 const int64_t r = r0 + base + j * kWarps;
@@ -136,6 +136,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) epilogue_grad_kernel(EpilogueG
                     if (ACT != MOEQ_ACT_NONE) zv[j] = ld_stream(p.z + r * p.N + n);
                 }
             }
+        };
+        load(warp);
+        for (int base = warp; base < rows; base += U * kWarps) {
             F2 x[U][4];
             float m[U];
 #pragma unroll
@@ -154,6 +157,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) epilogue_grad_kernel(EpilogueG
                     m[j] = fmaxf(fmaxf(m[j], fabsf(f2_lo(x[j][i]))), fabsf(f2_hi(x[j][i])));
                 }
             }
+            load(base + U * kWarps);  // on their way while these are quantized and stored
             float inv = 0.0f;  // of row (lane / 4) % 4
             if (p.q) {
                 const float s = block_scale(rows_amax(m, lane));
@@ -213,46 +217,54 @@ __global__ void __launch_bounds__(kWarps * 32, 2) epilogue_grad_kernel(EpilogueG
     }
 }
 
-// d_bias[e] from the tiles' sums: 32 columns a CTA, its warps take an expert's tiles
+// d_bias[e] from the tiles' sums: 128 columns a CTA, its warps take an expert's tiles
 // in turn and join.
 __global__ void __launch_bounds__(1024) bias_grad_kernel(const float *part, const uint32_t *tiles,
                                                          int64_t max_tiles,
                                                          const int32_t *expert_ids, int G,
                                                          int64_t N, float *d_bias, int E,
                                                          uint32_t *err) {
-    __shared__ float sums[32][33];
+    __shared__ float4 sums[32][32];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int64_t n = (int64_t)blockIdx.x * 32 + lane;
+    const int64_t n = (int64_t)blockIdx.x * 128 + lane * 4;  // N is a multiple of 8
     const int e = blockIdx.y;
-    float v = 0.0f;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [&](const float4 &u) {
+        v.x = __fadd_rn(v.x, u.x);
+        v.y = __fadd_rn(v.y, u.y);
+        v.z = __fadd_rn(v.z, u.z);
+        v.w = __fadd_rn(v.w, u.w);
+    };
     for (int base = 0; base < G; base += 32) {
         const int g = base + lane;
         uint32_t mine = __ballot_sync(0xFFFFFFFFu, g < G && __ldg(expert_ids + g) == e);
         for (; mine; mine &= mine - 1) {
             const int at = base + __ffs((int)mine) - 1;
-            const int64_t t0 = __ldg(tiles + at), t1 = min((int64_t)__ldg(tiles + at + 1), max_tiles);
+            const int64_t t1 = min((int64_t)__ldg(tiles + at + 1), max_tiles);
             if (n < N) {
 #pragma unroll 4
-                for (int64_t t = t0 + warp; t < t1; t += warps)
-                    v = __fadd_rn(v, __ldg(part + t * N + n));
+                for (int64_t t = (int64_t)__ldg(tiles + at) + warp; t < t1; t += warps)
+                    add(__ldg(reinterpret_cast<const float4 *>(part + t * N + n)));
             }
         }
     }
     sums[warp][lane] = v;
     __syncthreads();
     if (warp == 0) {
-        for (int w = 1; w < warps; ++w) v = __fadd_rn(v, sums[w][lane]);
+        for (int w = 1; w < warps; ++w) add(sums[w][lane]);
         float *out = d_bias + (int64_t)e * N + n;
-        if (n < N && store_fits(out, 4, d_bias, (int64_t)E * N * 4, err)) *out = v;
+        if (n < N && store_fits(out, 16, d_bias, (int64_t)E * N * 4, err))
+            st_global_v4(out, __float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z),
+                         __float_as_uint(v.w));
     }
 }
 
 }  // namespace
 
 cudaError_t launch_epilogue_grad(const EpilogueGradArgs &a, cudaStream_t s) {
-    const int64_t tiles = epilogue_grad_tiles(a.groups.total_rows, a.groups.num_groups);
+    const int64_t tiles = epilogue_grad_tiles(a.groups.total_rows, a.N, a.groups.num_groups);
     // its parts: the table of tiles, then the sums, 16-byte aligned
     uint32_t *table = static_cast<uint32_t *>(a.workspace);
     float *part = a.d_bias ? reinterpret_cast<float *>(
@@ -261,7 +273,9 @@ cudaError_t launch_epilogue_grad(const EpilogueGradArgs &a, cudaStream_t s) {
                            : nullptr;
     const EpilogueGradParams p{static_cast<const uint16_t *>(a.dc),
                                static_cast<const uint16_t *>(a.z), a.dc_stride,
-                               a.groups.total_rows, a.N, a.groups.row_offsets,
+                               a.groups.total_rows, a.N,
+                               (int)epilogue_grad_rows(a.groups.total_rows, a.N),
+                               a.groups.row_offsets,
                                a.groups.expert_ids, a.groups.num_groups, a.groups.num_experts, a.q,
                                a.scales, static_cast<uint16_t *>(a.dz), part, table, tiles, a.err};
     if (tiles > 0) {
@@ -278,8 +292,8 @@ cudaError_t launch_epilogue_grad(const EpilogueGradArgs &a, cudaStream_t s) {
     }
     if (!a.d_bias) return cudaSuccess;
     // many warps where there are few CTAs
-    const int64_t cols = (a.N + 31) / 32, ctas = cols * a.groups.num_experts;
-    const unsigned threads = ctas < 4 * sm_count() ? 1024 : 256;
+    const int64_t cols = (a.N + 127) / 128, ctas = cols * a.groups.num_experts;
+    const unsigned threads = ctas < 2 * sm_count() ? 1024 : 128;
     return launch_pdl(bias_grad_kernel, dim3((unsigned)cols, (unsigned)a.groups.num_experts),
                       threads, 0, s, (const float *)part, (const uint32_t *)table, tiles,
                       a.groups.expert_ids, tiles > 0 ? a.groups.num_groups : 0, a.N, a.d_bias,

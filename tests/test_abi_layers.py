@@ -126,7 +126,8 @@ def test_epilogue_grad_refusals(lib):  # noqa: F811
     assert call(T=0, db=None, dc=None, z=None, q=None, s=None) == OK
     size = lib.moeq_grouped_epilogue_grad_workspace
     assert size(-1, 64, 2) == -1 and size(8, 60, 2) == -1 and size(8, 64, 1025) == -1
-    assert size(8, 64, 2) == 16 + 2 * 64 * 4 and size(1000, 64, 3) == 16 + 10 * 64 * 4
+    assert size(8, 64, 2) == 16 + 2 * 64 * 4 and size(1000, 64, 3) == 16 + (15 + 3) * 64 * 4
+    assert size(1 << 20, 64, 3) == 16 + (4096 + 3) * 64 * 4
     assert size(0, 64, 4) == 32
 
 
