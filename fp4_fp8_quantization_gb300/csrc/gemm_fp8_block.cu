@@ -178,16 +178,28 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
                    "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
-// EPI: z = sum + bias[e], c = bf16(act(z) + residual), z stored too where asked.
+// The residual's tensor map, of the kernels that copy it to the staging buffers.
+template <bool USED>
+struct ResidualMap {
+    CUtensorMap map;
+};
+template <>
+struct ResidualMap<false> {};
+
+// EPI: z = sum + bias[e], c = bf16(act(z) + residual), z stored too where asked (not by
+// the asynchronous form, whose staging buffers hold the residual first and then c).
 template <class C, bool EPI>
 __global__ void __launch_bounds__(C::THREADS, 1)
     gemm_fp8_block_kernel(const __grid_constant__ CUtensorMap tmA,
                           const __grid_constant__ CUtensorMap tmA32,
                           const __grid_constant__ CUtensorMap tmB,
-                          const __grid_constant__ CUtensorMap tmC, const BlockGemmParams p) {
+                          const __grid_constant__ CUtensorMap tmC,
+                          const __grid_constant__ ResidualMap<EPI && C::ASYNC> tmR,
+                          const BlockGemmParams p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full_bar[C::STAGES], done_bar[C::STAGES], tempty_bar[C::NBUF];
     __shared__ uint64_t drain_bar;
+    __shared__ uint64_t res_bar[EPI && C::ASYNC ? C::SUM_WARPS : 1];  // the residual is there
     __shared__ uint32_t tmem_slot, stages_done;
     __shared__ int abort_flag;
     // per group: tiles before it, first row, expert
@@ -213,6 +225,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         for (int b = 0; b < C::NBUF; ++b) mbar_init(&tempty_bar[b], C::SUM_WARPS);
         mbar_init(&drain_bar, 1);
+        if constexpr (EPI && C::ASYNC) {
+            for (int w = 0; w < C::SUM_WARPS; ++w) mbar_init(&res_bar[w], 1);
+        }
         abort_flag = 0;
         stages_done = 0;
         prefix[0] = 0;
@@ -408,7 +423,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_v, p.err));
         };
         int buf = 0, stage = 0;
-        uint32_t phase = 0;
+        uint32_t phase = 0, res_phase = 0;
+        bool res_asked = false;  // a residual's copy is not waited for yet
         bool ok = true;
         Part cur = {}, nxt = {};
         // the scales of the next K block, on their way during this one
@@ -504,6 +520,26 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                                    __uint_as_float(r[ch & 1][2 * i + 1])),
                                                 s2[q], acc[cc * 16 + i]);
                 }
+                if constexpr (EPI && C::ASYNC) {
+                    // the residual into the staging buffer, which the last tile's
+                    // stores have read by now; its rows past the group's are not used
+                    if (kb == 0 && ok && p.residual) {
+                        if (lane == 0) bulk_wait_read_all();
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            const int sw = warp - C::SUM_WARP0;
+                            const int boxes = min(C::COLS_W / 64, (p.N - cur.ncol + 63) / 64);
+                            mbar_arrive_expect_tx(&res_bar[sw], boxes * 4096);
+                            for (int ch = 0; ch < boxes; ++ch)
+                                tma_load_2d(smem + C::STAGES * C::STAGE_BYTES + sw * C::BUF_BYTES +
+                                                ch * 4096,
+                                            &tmR.map, &res_bar[sw], cur.ncol + ch * 64, cur.row,
+                                            policy_evict_first());
+                        }
+                        res_asked = true;
+                    }
+                }
                 if (!ok) {
                     tmem_ld_wait32(r[0]);
                     break;
@@ -511,18 +547,65 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             }
             if (!ok) break;
+            if constexpr (EPI && C::ASYNC) {
+                if (res_asked) {
+                    ok = sums_wait(&res_bar[warp - C::SUM_WARP0], res_phase);
+                    if (!ok) break;
+                    res_phase ^= 1u;
+                    res_asked = false;
+                }
+            }
             // the next tile's place and first scales, while this one is stored
             if (t + gridDim.x < total) {
                 nxt = part_of(t + gridDim.x);
                 first_scales();
             }
             if (!work) continue;
+            // past N whatever is there
+            auto add_bias = [&](F2 *v, int ch) {
+                const uint32_t at = smem_u32(&bias_part[warp - C::SUM_WARP0][ch * 32]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint4 b = ld_shared_v4(at + j * 16);
+                    v[2 * j] = add2(v[2 * j], f2(__uint_as_float(b.x), __uint_as_float(b.y)));
+                    v[2 * j + 1] =
+                        add2(v[2 * j + 1], f2(__uint_as_float(b.z), __uint_as_float(b.w)));
+                }
+            };
+            // 8 columns of the residual
+            auto add_row = [&](F2 *v, const uint4 &w) {
+                v[0] = add2(v[0], bf16x2_values(w.x));
+                v[1] = add2(v[1], bf16x2_values(w.y));
+                v[2] = add2(v[2], bf16x2_values(w.z));
+                v[3] = add2(v[3], bf16x2_values(w.w));
+            };
             if constexpr (C::ASYNC) {
                 // the whole part into the warp's staging buffer, in boxes of 64
                 // columns (rows of 128 bytes in the tensor map's 128-byte swizzle);
                 // the last tile's stores have long read it
-                if (lane == 0) bulk_wait_read_all();
-                __syncwarp();
+                if (!EPI || !p.residual) {
+                    if (lane == 0) bulk_wait_read_all();
+                    __syncwarp();
+                }
+                if constexpr (EPI) {
+                    if (p.bias) {
+                        copy_async_wait();
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int ch = 0; ch < C::CHUNKS_W; ++ch) {
+                        F2 *v = acc + ch * 16;
+                        if (p.bias) add_bias(v, ch);
+                        activate16(v, p.act);
+                        if (p.residual) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                add_row(v + 4 * j,
+                                        ld_shared_v4(sbuf + ch / 2 * 4096 + lane * 128 +
+                                                     (((ch % 2 * 4 + j) ^ (lane & 7)) << 4)));
+                        }
+                    }
+                }
 #pragma unroll
                 for (int ch = 0; ch < C::COLS_W / 64; ++ch)
 #pragma unroll
@@ -613,16 +696,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const bool in_n = nc + k * 8 < p.N;  // N is a multiple of 8
                 F2 *v = acc + ch * 16;
                 if constexpr (EPI) {
-                    if (p.bias) {  // past N whatever is there
-                        const uint32_t bias_at = smem_u32(&bias_part[warp - C::SUM_WARP0][ch * 32]);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const uint4 b = ld_shared_v4(bias_at + j * 16);
-                            v[2 * j] = add2(v[2 * j], f2(__uint_as_float(b.x), __uint_as_float(b.y)));
-                            v[2 * j + 1] =
-                                add2(v[2 * j + 1], f2(__uint_as_float(b.z), __uint_as_float(b.w)));
-                        }
-                    }
+                    if (p.bias) add_bias(v, ch);
                     if (p.z) {
                         __syncwarp();  // the last chunk has been read
                         stage(v);
@@ -638,13 +712,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         if (ch + 1 < C::CHUNKS_W) residual(ch + 1);
                         __syncwarp();
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint4 w = ld_shared_v4(own(j));
-                            v[4 * j] = add2(v[4 * j], bf16x2_values(w.x));
-                            v[4 * j + 1] = add2(v[4 * j + 1], bf16x2_values(w.y));
-                            v[4 * j + 2] = add2(v[4 * j + 2], bf16x2_values(w.z));
-                            v[4 * j + 3] = add2(v[4 * j + 3], bf16x2_values(w.w));
-                        }
+                        for (int j = 0; j < 4; ++j) add_row(v + 4 * j, ld_shared_v4(own(j)));
                     }
                 }
                 __syncwarp();  // the last chunk has been read
@@ -654,7 +722,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
         }
         if (C::ASYNC && lane == 0) bulk_wait_all();
-        if constexpr (EPI) copy_async_wait();  // after giving up too
+        // after giving up too
+        if constexpr (EPI) copy_async_wait();
+        if (EPI && C::ASYNC && res_asked && lane == 0)
+            mbar_drain(&res_bar[warp - C::SUM_WARP0], res_phase);
     }
 
     // this CTA's loads, MMAs and stores are all issued
@@ -706,6 +777,15 @@ cudaError_t run_block_gemm(const GemmBlockArgs &a, cudaStream_t s) {
                     CU_TENSOR_MAP_L2_PROMOTION_NONE,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
+    ResidualMap<EPI && C::ASYNC> tR = {};
+    if constexpr (EPI && C::ASYNC) {
+        if (a.residual &&
+            encode_fn()(&tR.map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(a.residual),
+                        dc, sc, bc, ec, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
     const BlockGemmParams p{a.groups.row_offsets, a.groups.expert_ids, a.groups.num_groups,
                             a.groups.num_experts, T, (int)a.N, (int)a.K, a.a_scales, a.b_scales,
                             static_cast<uint16_t *>(a.c), a.err, a.bias,
@@ -736,7 +816,7 @@ cudaError_t run_block_gemm(const GemmBlockArgs &a, cudaStream_t s) {
     const int64_t tiles = (T / C::BM + std::min<int64_t>(a.groups.num_groups, T)) *
                           ((a.N + C::BN - 1) / C::BN);
     const unsigned grid = (unsigned)std::min<int64_t>(tiles, sm_count());
-    return launch_pdl(kern, grid, C::THREADS, C::SMEM_BYTES, s, tA, tA32, tB, tC, p);
+    return launch_pdl(kern, grid, C::THREADS, C::SMEM_BYTES, s, tA, tA32, tB, tC, tR, p);
 }
 
 // The forms below (the last two 128 x 256, results stored by tensor stores or
@@ -780,11 +860,18 @@ cudaError_t launch_gemm_fp8_block(const GemmBlockArgs &a, cudaStream_t s) {
 #endif
     using Small = BlockCfg<64, 128, 4, 8, false, 2>;
     using Large = BlockCfg<128, 256, 4, 8, false, 1>;
-    if (a.bias || a.act != MOEQ_ACT_NONE || a.residual || a.z)
-        return tile == kSmallTile ? run_block_gemm<Small, true>(a, s)
-                                  : run_block_gemm<Large, true>(a, s);
+    using Async = BlockCfg<128, 256, 3, 8, true, 1>;
+    if (a.bias || a.act != MOEQ_ACT_NONE || a.residual || a.z) {
+        if (tile == kSmallTile) return run_block_gemm<Small, true>(a, s);
+        if (a.z) tile = kLargeTile;  // two results do not fit the staging buffers
+#ifndef MOEQ_FP8_BLOCK_TILE
+        else if (a.residual) tile = kLargeTileByTensor;
+#endif
+        return tile == kLargeTileByTensor ? run_block_gemm<Async, true>(a, s)
+                                          : run_block_gemm<Large, true>(a, s);
+    }
     if (tile == kSmallTile) return run_block_gemm<Small>(a, s);
-    if (tile == kLargeTileByTensor) return run_block_gemm<BlockCfg<128, 256, 3, 8, true, 1>>(a, s);
+    if (tile == kLargeTileByTensor) return run_block_gemm<Async>(a, s);
     return run_block_gemm<Large>(a, s);
 }
 
