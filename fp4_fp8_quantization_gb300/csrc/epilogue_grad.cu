@@ -10,7 +10,13 @@
 // block; each thread sums its 8 columns over its rows, the warps join in shared
 // memory, and a tile leaves one row of partial sums.  A second kernel adds an
 // expert's rows of them in the order of groups and tiles: no atomics, the same
-// bits every time.
+// bits every time.  Four rows of a warp are worked on together, so that their 8 block
+// scales take one division a lane, and the next four's loads are in flight meanwhile.
+//
+// 32768 x 4096 over 64 experts, silu: 130 us without empty tiles (0.76 of the copy rate,
+// of it 8 for the bias's second kernel), 0.59 of DRAM's peak and 0.65 of the issue slots
+// in the profile: instructions and the tiles' beginnings, which nothing overlaps.  4096 x
+// 4096 23, 64 x 4096 7.4 (4.9 without the bias).
 #include <algorithm>
 
 #include "activation.cuh"

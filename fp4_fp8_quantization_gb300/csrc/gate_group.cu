@@ -19,12 +19,20 @@
 // The row of a token is in the registers of L lanes, a power of two of them for
 // each group (lane and index order are expert order), read once.  Keys are the
 // bits of max c - c with the lane and index in the low bits (of 16-bit logits without
-// a bias: their whole images): those of the best
-// values, close to the maximum, keep most of their digits, so that a round of the
-// choice is one integer minimum over the lanes.  Scores next to one another are
-// decided as 64 bits would: c in fp32 is off by a bound known beforehand, and a token
-// in which two values that the choice depends on are closer than that (about one
-// in a thousand) is chosen again from scores that are sums of two floats.
+// a bias: their whole images): those of the best values, close to the maximum, keep
+// most of their digits, so that a round of the choice is one integer minimum over the
+// lanes.  Scores next to one another are decided as 64 bits would: c in fp32 is off by
+// a bound known beforehand, and a token in which two values that the choice depends on
+// are closer than that (about one in a thousand) looks at those again as sums of two
+// floats.
+//
+// Bound by the pipes of integer minima and comparisons and of 2^x and 1 / x: some 385
+// instructions a token of 256 experts, a third of them the lanes' sorts.  65537 x 256,
+// 8 groups of which 4, top-8, sigmoid and bias: forward 49 us fp32, 42 bf16 (10 and 5
+// of memory), gradient 15 (10); 65536 x 128, one group, top-4, 18; 9999 x 160 softmax,
+// 8 groups, top-6, 8.3; 64 x 256 2.9.  A token that is looked at again takes 3 us more
+// (in 64-bit floats 7 to 40), in time with the others'.  More CTAs on an SM by fewer
+// registers: none faster, 8 of them 15 % slower.
 #include <algorithm>
 
 #include "common.cuh"
@@ -802,18 +810,12 @@ __global__ void __launch_bounds__(kWarps * 32) gate_chosen_grad_kernel(ChosenGra
     const uint8_t *in = p.logits + t * p.stride;
     uint8_t *out = p.d_logits + t * p.E * kS;
     const int64_t size = p.num_tokens * p.E * kS;
+    // the zeros leave while the ids are on their way
     int id = -1;
     float g = 0.0f, x = -kInf;
     if (sub < p.top_k) {
         id = __ldg(p.ids + t * p.top_k + sub);
-        if (id < -1 || id >= p.E) {
-            if (active) set_error(p.err, MOEQ_DEVERR_BAD_EXPERT);
-            id = -1;
-        }
-        if (id >= 0) {
-            g = __fmul_rn(__ldg(p.d_weights + t * p.top_k + sub), p.scale);
-            x = load_logit<DT>(in, id);
-        }
+        g = __ldg(p.d_weights + t * p.top_k + sub);
     }
     if (active) {
         if (p.vec) {
@@ -826,6 +828,12 @@ __global__ void __launch_bounds__(kWarps * 32) gate_chosen_grad_kernel(ChosenGra
                     store_logit<DT>(out, j, 0.0f);
         }
     }
+    if (id < -1 || id >= p.E) {
+        if (active) set_error(p.err, MOEQ_DEVERR_BAD_EXPERT);
+        id = -1;
+    }
+    g = id >= 0 ? __fmul_rn(g, p.scale) : 0.0f;
+    if (id >= 0) x = load_logit<DT>(in, id);
     float d = 0.0f;
     if (p.sigmoid) {
         const float s = id >= 0 ? sigmoid_exact(x) : 0.0f;

@@ -45,6 +45,15 @@
 // is what bounds it.  The reduction split over a cluster whose CTAs exchange their
 // sums costs 2 us a tile: 24 tiles of K 4096 10.5 -> 8.1 us, 48 11.2 -> 10.7, but
 // 96 (one token, 8 experts, N 1536) 13.8 -> 18.8.
+//
+// The epilogue (bias, activation, residual; act(z) in paired fp32) runs on the sum
+// warps, between a tile's last block and the next one's first sums: the tensor cores
+// are two blocks ahead and then wait for it.  Its loads come before: the bias by
+// asynchronous copies at the tile's start, the residual into the staging buffers during
+// the reduction, or, with direct stores, a chunk ahead.  16384 x 7168 x 4096, back to
+// back under the power limit: plain 387 us, bias 400, silu 420, gelu_tanh 423, gelu 440,
+// bias and residual 438 (455 without the copies), both 465; the residual's and z's 235
+// MB are 35 us of memory each.
 #include <algorithm>
 
 #include "activation.cuh"
