@@ -844,7 +844,7 @@ moeq_status moeq_add_rms_norm(moeq_dtype dtype, const void *x, int64_t x_stride,
         !weight || !aligned16(weight) || !aligned16(h) || !aligned16(y) || !aligned16(q) ||
         !aligned16(scales) || !aligned16(rstd))
         return MOEQ_ERR_INVALID_ARG;
-    if (!h != !residual || !q != !scales || (q && K % 16) || (!y && !q && !rstd))
+    if (!h != !residual || (h && h == y) || !q != !scales || (q && K % 16) || (!y && !q && !rstd))
         return MOEQ_ERR_INVALID_ARG;
     uint32_t *err = device_error_ptr();
     if (!err) return cuda_status(cudaErrorInvalidDevice);

@@ -499,7 +499,8 @@ moeq_status moeq_gate_topk_grad(moeq_dtype dtype, const void *logits, int64_t lo
  *   normalize != 0:  w_r = scale * s_{i_r} / sum over the choices of s  (0 where it is 0)
  * The bias decides the choice and does not enter the weights; without one (NULL) c is
  * ordered as the logits are.  The order is that of c in 64 bits, whatever its fp32
- * rounding; weights are fp32, from s within 4 ulp (sigmoid) or as in moeq_gate_topk.
+ * rounding (a score below 2^-126 counts as 0); weights are fp32, from s within 4 ulp
+ * (sigmoid) or as in moeq_gate_topk.
  *   logits      dtype [num_tokens, num_experts], row stride logit_stride elements.
  *   bias        fp32 [num_experts] or NULL.
  *   topk_ids    int32 [num_tokens, top_k] (out);  weights fp32 [num_tokens, top_k] (out).
@@ -624,8 +625,9 @@ moeq_status moeq_quantize_fp8_block_weight(const void *w, int64_t num_experts, i
  *               row_scales != 0, one for each row, fp32 [rows] (the operands of
  *               moeq_grouped_matmul_fp8_block and moeq_grouped_matmul_rowwise_fp8).
  *   rstd        fp32 [rows] (out), for the gradient.
- * y, q with scales, and rstd may be NULL, not all of them.  h and y may be x's or the
- * residual's own buffer (the same rows at the same stride); other overlaps are not allowed.
+ * y, q with scales, and rstd may be NULL, not all of them.  h and y, two buffers, may be
+ * x's or the residual's own (the same rows at the same stride); other overlaps are not
+ * allowed.
  * K and the strides are multiples of 8, with q K of 16; K <= 16384 (else
  * MOEQ_ERR_UNSUPPORTED); eps >= 0. */
 moeq_status moeq_add_rms_norm(moeq_dtype dtype, const void *x, int64_t x_stride,
@@ -715,7 +717,8 @@ moeq_status moeq_grouped_matmul_fp8_block_epilogue(
  *   d_bias      fp32 [num_experts, N] (out) or NULL; an expert without rows gets 0.  With
  *               it, workspace: device memory of moeq_grouped_epilogue_grad_workspace(...)
  *               bytes that no other call in flight uses.
- * Rows outside the groups are not written and not summed.  N % 8 == 0, with q N % 16 == 0;
+ * Rows outside the groups are not written and not summed; no output overlaps an input or
+ * another output.  N % 8 == 0, with q N % 16 == 0;
  * num_experts <= 65535 (else MOEQ_ERR_UNSUPPORTED). */
 moeq_status moeq_grouped_epilogue_grad(const void *d_c, int64_t d_c_stride, const void *z,
                                        moeq_activation activation, uint8_t *q, float *scales,

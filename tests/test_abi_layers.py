@@ -52,8 +52,9 @@ def test_binding_refuses_host_tensors():
 
 def test_norm_refusals(lib):  # noqa: F811
     call = _caller(lib.moeq_add_rms_norm, dict(
-        dt=0, x=FAKE, xs=64, r=FAKE, rs=64, R=8, K=64, w=FAKE, eps=1e-6, h=FAKE, y=FAKE, q=FAKE,
+        dt=0, x=FAKE, xs=64, r=FAKE, rs=64, R=8, K=64, w=FAKE, eps=1e-6, h=FAKE, y=0x20000, q=FAKE,
         s=FAKE, by_row=0, u=FAKE, st=None))
+    assert call(y=FAKE) == BAD                             # h itself
     assert call(dt=3) == BAD and call(R=-1) == BAD and call(K=0) == BAD and call(K=68, xs=72, rs=72) == BAD
     assert call(K=56) == BAD                               # codes of a K that is no multiple of 16
     assert call(eps=-1.0) == BAD and call(eps=float("nan")) == BAD
