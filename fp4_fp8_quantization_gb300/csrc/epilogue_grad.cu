@@ -6,15 +6,15 @@
 //   d_bias[e] = sum over the rows of expert e of d_z (fp32, before any rounding)
 //
 // One pass: 4 bytes read and 1 (or 3) written per element.  A CTA takes tiles of
-// 64 to 256 rows of one group by 256 columns, a warp a row at a time, 16 lanes a
+// 64 to 512 rows of one group by 256 columns, a warp a row at a time, 16 lanes a
 // block; each thread sums its 8 columns over its rows, the warps join in shared
 // memory, and a tile leaves one row of partial sums.  A second kernel adds an
 // expert's rows of them in the order of groups and tiles: no atomics, the same
 // bits every time.  Four rows of a warp are worked on together, so that their 8 block
 // scales take one division a lane, and the next four's loads are in flight meanwhile.
 //
-// 32768 x 4096 over 64 experts, silu, even groups: 130 us (0.76 of the copy rate,
-// of it 8 for the bias's second kernel), 0.59 of DRAM's peak and 0.65 of the issue slots
+// 32768 x 4096 over 64 experts, silu, even groups: 127 us (0.78 of the copy rate,
+// of it 6 for the bias's second kernel), 0.59 of DRAM's peak and 0.65 of the issue slots
 // in the profile: instructions and the tiles' beginnings, which nothing overlaps.  4096 x
 // 4096 23, 64 x 4096 7.4 (4.9 without the bias).
 #include <algorithm>

@@ -156,10 +156,14 @@ struct EpilogueGradArgs {
 cudaError_t launch_epilogue_grad(const EpilogueGradArgs &a, cudaStream_t s);
 // Its workspace: a table of tiles for each group, then one row of N sums for each
 // tile of a group's rows: as many rows as leave the machine enough tiles (32768 x 4096,
-// 64 groups: 128 rows 157 us, 256 143).
+// 64 uneven groups: 128 rows 150 us, 256 136, 512 129; 65536 x 1536, 128 groups: 256 112,
+// 512 115).
 inline int64_t epilogue_grad_rows(int64_t rows, int64_t N) {
     const int64_t n = rows * N;
-    return n < (int64_t)1 << 22 ? 64 : n < (int64_t)1 << 25 ? 128 : 256;
+    return n < (int64_t)1 << 22   ? 64
+           : n < (int64_t)1 << 25 ? 128
+           : n < (int64_t)1 << 27 ? 256
+                                  : 512;
 }
 inline int64_t epilogue_grad_tiles(int64_t rows, int64_t N, int64_t groups) {
     return rows && groups ? rows / epilogue_grad_rows(rows, N) + (groups < rows ? groups : rows) : 0;
