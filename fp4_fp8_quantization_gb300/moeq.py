@@ -510,12 +510,14 @@ def _on_current_device(dev):
 
 def _matrix(t, name, dtype=None, shape=None, dev=None):
     """(pointer, row stride, device) of a 2-D CUDA tensor, as _rows_of."""
-    if (isinstance(t, torch.Tensor) and t.is_contiguous() and t.dim() == 2
-            and (t.dtype in DTYPES if dtype is None else t.dtype is dtype)
-            and (shape is None or t.shape == shape)):
-        at = t.get_device()
-        if at >= 0 and (dev is None or at == dev):
-            return t.data_ptr(), t.shape[1], at
+    try:
+        if ((t.dtype in DTYPES if dtype is None else t.dtype is dtype) and t.is_contiguous()
+                and (t.dim() == 2 if shape is None else t.shape == shape)):
+            at = t.get_device()
+            if at >= 0 and (dev is None or at == dev):
+                return t.data_ptr(), t.shape[1], at
+    except AttributeError:
+        pass
     p = _rows_of(t, name, shape, dtype)
     if dev is not None and t.get_device() != dev:
         raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
@@ -523,14 +525,20 @@ def _matrix(t, name, dtype=None, shape=None, dev=None):
 
 
 def _array(t, shape, dtype, dev, name):
-    """Pointer of a contiguous tensor of this shape and dtype (or one of a tuple
-    of dtypes) on device dev."""
-    if (isinstance(t, torch.Tensor) and t.shape == shape and t.get_device() == dev
-            and (t.dtype is dtype or (type(dtype) is tuple and t.dtype in dtype))
-            and t.is_contiguous()):
-        return t.data_ptr()
+    """Pointer of a contiguous tensor of this shape and dtype on device dev."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _shaped(t, shape, dtype, name)
     raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
+
+
+def _array_of(t, shape, dtypes, dev, name):
+    """_array of one of two dtypes."""
+    return _array(t, shape, dtypes[1 if t.dtype is dtypes[1] else 0], dev, name)
 
 
 def _groups(a_offsets, expert_ids, num_active_experts, dev):
@@ -538,7 +546,7 @@ def _groups(a_offsets, expert_ids, num_active_experts, dev):
     G = expert_ids.numel() if num_active_experts is None else num_active_experts
     if expert_ids.numel() < G or a_offsets.numel() < G + 1:
         raise ValueError(f"a_offsets, expert_ids: too short for {G} groups")
-    return (_array(a_offsets, a_offsets.shape, _U32, dev, "a_offsets"),
+    return (_array_of(a_offsets, a_offsets.shape, _U32, dev, "a_offsets"),
             _array(expert_ids, expert_ids.shape, torch.int32, dev, "expert_ids"), G)
 
 
@@ -715,6 +723,7 @@ def _workspace(workspace, need, stream, like, dev):
         if stream is not None:
             raise ValueError("workspace: required with a stream")
         workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        return workspace.data_ptr(), workspace
     if workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace: {need} bytes expected")
     return _array(workspace, workspace.shape, workspace.dtype, dev, "workspace"), workspace
@@ -739,7 +748,7 @@ def add_rms_norm(x, weight, y=None, residual=None, h=None, q=None, scales=None, 
     pw = _array(weight, (k,), dt, dev, "weight")
     ph = None if h is None else _array(h, shape, dt, dev, "h")
     py = None if y is None else _array(y, shape, dt, dev, "y")
-    pq = None if q is None else _array(q, shape, _U8, dev, "q")
+    pq = None if q is None else _array_of(q, shape, _U8, dev, "q")
     by_row, ps = False, None
     if scales is not None:
         by_row = scales.dim() == 1
@@ -820,7 +829,7 @@ def grouped_matmul_fp8_block_epilogue(c, a, b, a_scales, b_scales, a_offsets, ex
         raise ValueError("a: must be contiguous")
     ro, ids, G = _groups(a_offsets, expert_ids, num_active_experts, dev)
     pc = _array(c, out, bf16, dev, "c")
-    pb = _array(b, (E, N, K), _U8, dev, "b")
+    pb = _array_of(b, (E, N, K), _U8, dev, "b")
     kb = _blocks128(K)
     psa = _array(a_scales, (T, kb), f32, dev, "a_scales")
     psb = _array(b_scales, (E, _blocks128(N), kb), f32, dev, "b_scales")
@@ -855,7 +864,7 @@ def grouped_epilogue_grad(d_c, a_offsets, expert_ids, num_experts, z=None, activ
     bf16, f32 = torch.bfloat16, torch.float32
     ro, ids, G = _groups(a_offsets, expert_ids, num_active_experts, dev)
     pz = None if z is None else _array(z, shape, bf16, dev, "z")
-    pq = None if q is None else _array(q, shape, _U8, dev, "q")
+    pq = None if q is None else _array_of(q, shape, _U8, dev, "q")
     ps = None if scales is None else _array(scales, (T, _blocks128(N)), f32, dev, "scales")
     pd = None if d_z is None else _array(d_z, shape, bf16, dev, "d_z")
     pv = ws = None
