@@ -26,12 +26,12 @@
 // are closer than that (about one in a thousand) looks at those again as sums of two
 // floats.
 //
-// Bound by the pipes of integer minima and comparisons and of 2^x and 1 / x: some 385
-// instructions a token of 256 experts, a third of them the lanes' sorts.  65537 x 256,
-// 8 groups of which 4, top-8, sigmoid and bias: forward 49 us fp32, 42 bf16 (10 and 5
-// of memory), gradient 15 (10); 65536 x 128, one group, top-4, 18; 9999 x 160 softmax,
-// 8 groups, top-6, 8.3; 64 x 256 2.9.  A token that is looked at again takes 3 us more
-// (in 64-bit floats 7 to 40), in time with the others'.  More CTAs on an SM by fewer
+// Bound by the pipe of integer minima and comparisons (46 %) and the issue slots (57 %) at
+// four warps a scheduler: some 390 instructions a token of 256 experts.  65537 x 256, 8
+// groups of which 4, top-8, sigmoid and bias: forward 36 us fp32, 33 bf16 (10 and 5 of
+// memory), gradient 15 (10); 65536 x 128, one group, top-4, 18; 9999 x 160 softmax, 8
+// groups, top-6, 7.6; 64 x 256 2.9.  A token that is looked at again takes 3 us more (in
+// 64-bit floats 7 to 40), in time with the others'.  More CTAs on an SM by fewer
 // registers: none faster, 8 of them 15 % slower.
 #include <algorithm>
 
@@ -57,6 +57,7 @@ struct ScoredParams {
     int group_size, lane_shift, per_lane;  // 1 << lane_shift lanes a group, per_lane logits each
     int vec, bias_vec;                     // a lane's logits, biases are aligned vectors
     int staged;                            // and the lanes' are the whole row, in order
+    int halves;                            // a group is a lane, at most half of them are chosen
     float scale;
     int32_t *ids;
     float *weights;
@@ -672,15 +673,11 @@ __global__ void __launch_bounds__(kWarps * 32) gate_scored_kernel(ScoredParams p
                 }
             }
         }
-        if (!in) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) c[i] = -kInf;
-        }
     }
     float top = -kInf;
 #pragma unroll
     for (int i = 0; i < NV; ++i) top = fmaxf(top, c[i]);
-    top = lanes_top<L>(top);
+    top = lanes_top<L>(in ? top : -kInf);
     // without a bias the images of 16-bit logits are whole in the bits above the index
     const bool whole = !BIAS && p.dt != MOEQ_FP32;
     // keys from that of -inf, or of an infinite distance, on stand for no expert
@@ -698,19 +695,47 @@ __global__ void __launch_bounds__(kWarps * 32) gate_scored_kernel(ScoredParams p
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) key[i] = (key[i] & ~kIdx) | (uint32_t)(sub * NV + i);
-    merge_step<NV, 1, 1>(key);
     // a token's best keys, and the one behind them; of a lane's at most as many as that
     // (top_k <= L) and one are looked at
     constexpr int kKeep = NV < L + 2 ? NV : L + 2;
+    constexpr uint32_t kNoKey = 0x7FFFFFFFu;
     __shared__ uint32_t chosen[kWarps][32 / L][L + 1];
     uint32_t *out = chosen[threadIdx.x >> 5][lane / L];
+    if (L < 32 && NV >= 16 && p.halves) {
+        // a lane is a group, and no more than half of them are chosen: each other lane
+        // sorts the second half of a chosen one's keys (65537 x 256 forward 38 us, 36)
+        constexpr int H = NV > 1 ? NV / 2 : 1;
+        constexpr uint32_t kLanes = L < 32 ? (1u << (L % 32)) - 1u : kAll;
+        const uint32_t ins = (__ballot_sync(kAll, in) >> (lane - sub)) & kLanes;
+        const int rank = __popc((in ? ins : ~ins) & ((1u << sub) - 1u));
+        if (in) out[rank] = (uint32_t)sub;
+        __syncwarp();
+        const bool takes = !in && rank < __popc(ins);
+        const int from = takes ? (int)out[rank] : sub;
+        __syncwarp();
+        uint32_t half_keys[H];
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const uint32_t u = __shfl_sync(kAll, key[(H + i) % NV], from, L);
+            half_keys[i] = in ? key[i] : takes ? u : kNoKey;
+        }
+        merge_step<H, 1, 1>(half_keys);
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i) key[i] = i < H ? half_keys[i % H] : kNoKey;
+    } else {
+        merge_step<NV, 1, 1>(key);
+        if (p.groups > 1) {
+#pragma unroll
+            for (int i = 0; i < kKeep; ++i) key[i] = in ? key[i] : kNoKey;
+        }
+    }
     for (int r = 0; r <= p.top_k; ++r) {
         const uint32_t mn = lanes_min<L>(key[0]);
         const bool own = key[0] == mn;
         if (own) out[r] = mn;
 #pragma unroll
         for (int i = 0; i < kKeep; ++i)
-            key[i] = own ? (i + 1 < kKeep ? key[(i + 1) % NV] : 0x7FFFFFFFu) : key[i];
+            key[i] = own ? (i + 1 < kKeep ? key[(i + 1) % NV] : kNoKey) : key[i];
     }
     __syncwarp();
     auto expert_of = [&](uint32_t k) {
@@ -771,7 +796,7 @@ __global__ void __launch_bounds__(kWarps * 32) gate_scored_kernel(ScoredParams p
                 if (own) out[count] = mn;
 #pragma unroll
                 for (int i = 0; i < kKeep; ++i)
-                    key[i] = own ? (i + 1 < kKeep ? key[(i + 1) % NV] : 0x7FFFFFFFu) : key[i];
+                    key[i] = own ? (i + 1 < kKeep ? key[(i + 1) % NV] : kNoKey) : key[i];
             }
             __syncwarp();
             if (sub > p.top_k) candidate();
@@ -956,6 +981,7 @@ int lay_out(ScoredParams &p, int L) {
     const bool whole = p.per_lane == nv;  // lanes begin at multiples of nv in their group
     p.vec = whole && p.stride % bytes == 0 && (p.groups == 1 || p.group_size * size % bytes == 0);
     p.bias_vec = whole && nv % 4 == 0 && (p.groups == 1 || p.group_size % 4 == 0);
+    p.halves = p.groups == L && 2 * p.topk_groups <= L;
     p.staged = p.vec && p.E == L * nv && (p.groups << p.lane_shift) == L;
     return nv;
 }
@@ -963,10 +989,9 @@ int lay_out(ScoredParams &p, int L) {
 cudaError_t run_scored(ScoredParams p, cudaStream_t s) {
     // Many tokens: few lanes each, so that what a token costs whatever its experts is
     // shared by the tokens of a warp.  Forward, sigmoid with bias, bf16, 8 lanes (or 16)
-    // against 32: 65536 tokens x 64 experts, top-8, 14.2 / 36.4 us, x 128, top-4, 17.2 /
-    // 35.5, x 160, 8 groups, 33.3 / 52.6, x 256, 8 groups, 40.2 (45.0) / 51.6, x 512, 16
-    // groups (85.0) / 74.6; 4096 x 64 3.5 / 5.0, x 128 3.8 / 4.5, x 256 6.0 / 6.2; 2048 x
-    // 128 3.2 / 3.4, x 256 4.8 / 4.3
+    // against 32: 65536 tokens x 64 experts, top-8, 17.7 / 37.8 us, x 128, top-4, 18.0 /
+    // 35.7, x 160, 8 groups, 33.8 / 55.3, x 256, 8 groups, 33.4 (46.0) / 51.5, x 512, 16
+    // groups (88) / 79; 4096 x 64 3.8 / 4.9, x 128 4.9 / 4.8, x 256 7.3 / 6.7
     ScoredParams q = p;
     if (p.num_tokens >= 4096) {
         const int nv = lay_out(q, 8);

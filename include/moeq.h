@@ -499,7 +499,8 @@ moeq_status moeq_gate_topk_grad(moeq_dtype dtype, const void *logits, int64_t lo
  *   normalize != 0:  w_r = scale * s_{i_r} / sum over the choices of s  (0 where it is 0)
  * The bias decides the choice and does not enter the weights; without one (NULL) c is
  * ordered as the logits are.  The order is that of c in 64 bits, whatever its fp32
- * rounding (a score below 2^-126 counts as 0); weights are fp32, from s within 4 ulp
+ * rounding (a score below 2^-126 counts as 0; sums that are equal but for the rounding of
+ * 64 bits, as of sigmoid(x) and sigmoid(-x), may fall either way); weights are fp32, from s within 4 ulp
  * (sigmoid) or as in moeq_gate_topk.
  *   logits      dtype [num_tokens, num_experts], row stride logit_stride elements.
  *   bias        fp32 [num_experts] or NULL.
