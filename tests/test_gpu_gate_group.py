@@ -120,7 +120,7 @@ def test_gradient_against_differences(score, normalize):
         assert np.all(np.abs(f64(dx)[:, j] - diff) < 1e-7 + 1e-6 * np.abs(dw).max())
 
 
-@pytest.mark.parametrize("E,G,k", [(256, 8, 8), (128, 1, 8), (1024, 4, 16), (510, 3, 5)])
+@pytest.mark.parametrize("E,G,k", [(256, 8, 8), (128, 1, 8), (1024, 4, 16), (510, 3, 5), (512, 4, 32)])
 def test_order_of_values_that_fp32_does_not_tell_apart(E, G, k):
     """Biases that cancel the scores' differences to a few 2^-26, equal values
     among them: the choice is that of 64 bits."""
