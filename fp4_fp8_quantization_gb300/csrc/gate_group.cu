@@ -28,7 +28,7 @@
 //
 // Bound by the pipe of integer minima and comparisons (46 %) and the issue slots (57 %) at
 // four warps a scheduler: some 390 instructions a token of 256 experts.  65537 x 256, 8
-// groups of which 4, top-8, sigmoid and bias: forward 36 us fp32, 33 bf16 (10 and 5 of
+// groups of which 4, top-8, sigmoid and bias: forward 35 us fp32, 33 bf16 (10 and 5 of
 // memory), gradient 15 (10); 65536 x 128, one group, top-4, 18; 9999 x 160 softmax, 8
 // groups, top-6, 7.6; 64 x 256 2.9.  A token that is looked at again takes 3 us more (in
 // 64-bit floats 7 to 40), in time with the others'.  More CTAs on an SM by fewer
@@ -753,22 +753,23 @@ __global__ void __launch_bounds__(kWarps * 32) gate_scored_kernel(ScoredParams p
             cv = value(v, b);
         }
     };
+    // with a choice in each lane all have the one behind them beside their own
+    const bool full = p.top_k == L;
+    const int behind = full && out[L] < none ? expert_of(out[L]) : -1;
+    float v_behind = 0.0f, b_behind = 0.0f;
+    if (behind >= 0) {
+        v_behind = load_any(row, behind, p.dt);
+        if (BIAS) b_behind = __ldg(p.bias + behind);
+    }
     if (sub <= p.top_k) candidate();
     // two neighbours that are not decided (of the same logit and bias the lower index
-    // is first); lane top_k has the one behind the choices, or, with a choice in each lane,
-    // the last lane looks at it too
+    // is first); lane top_k has the one behind the choices
     float vn = __shfl_down_sync(kAll, v, 1, L), bn = __shfl_down_sync(kAll, b, 1, L);
     float cn = __shfl_down_sync(kAll, cv, 1, L);
-    const bool full = p.top_k == L;
-    int behind = -1;
-    if (full && out[L] < none) behind = expert_of(out[L]);
     if (full && sub == L - 1) {
-        cn = -kInf;
-        if (behind >= 0) {
-            vn = load_any(row, behind, p.dt);
-            if (BIAS) bn = __ldg(p.bias + behind);
-            cn = value(vn, bn);
-        }
+        vn = v_behind;
+        bn = b_behind;
+        cn = behind >= 0 ? value(vn, bn) : -kInf;
     }
     const float near =
         rounded ? __fadd_rn(tol, __fmul_rn(fmaxf(fabsf(cv), fabsf(cn)), 0x1p-22f)) : 0.0f;
@@ -809,15 +810,13 @@ __global__ void __launch_bounds__(kWarps * 32) gate_scored_kernel(ScoredParams p
             // the candidates by their values as pairs; with a choice in each lane the one
             // behind them too, which every lane has
             uint64_t key64 = float_key(v), last = 0u;
-            if (full && behind >= 0) last = float_key(load_any(row, behind, p.dt));
+            if (behind >= 0) last = float_key(v_behind);
             if (BIAS) {
                 Pair sum = {1.0f, 0.0f};
                 if (!SIGMOID) sum = total_pair(p, row, lane, L, m);
                 if (!plain) {
                     key64 = value_key(SIGMOID, v, b, m, sum);
-                    if (full && behind >= 0)
-                        last = value_key(SIGMOID, load_any(row, behind, p.dt),
-                                         __ldg(p.bias + behind), m, sum);
+                    if (behind >= 0) last = value_key(SIGMOID, v_behind, b_behind, m, sum);
                 }
             }
             int rank = behind >= 0 && (last > key64 || (last == key64 && behind < id));
