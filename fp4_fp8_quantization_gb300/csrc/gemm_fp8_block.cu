@@ -108,7 +108,7 @@ struct BlockCfg {
                             32 * SUM_WARP0 * NREG_CTRL + 32 * SUM_WARPS * NREG_SUM <=
                                 THREADS * LAUNCH_REGS),
                   "register split by warpgroups");
-    static_assert(CHUNKS_W % 2 == 0, "the two load buffers alternate across K blocks");
+    static_assert(KSUB * CHUNKS_W % 2 == 0, "the two load buffers alternate across stages");
     static_assert(COLS_W % 32 == 0 && 128 % COLS_W == 0, "a warp's columns share one scale");
 };
 
@@ -871,7 +871,19 @@ cudaError_t launch_gemm_fp8_block(const GemmBlockArgs &a, cudaStream_t s) {
     using Large = BlockCfg<128, 256, 4, 8, false, 1>;
     using Async = BlockCfg<128, 256, 3, 8, true, 1>;
     if (a.bias || a.act != MOEQ_ACT_NONE || a.residual || a.z) {
-        if (tile == kSmallTile) return run_block_gemm<Small, true>(a, s);
+        if (tile == kSmallTile) {
+            // few tiles: what counts is a CTA's walk along K, some 0.17 us for a stage and
+            // 0.12 for each of its blocks (from K 4096 and 16384 with two and four blocks).
+            // So half as wide, with four blocks in a stage, up to one tile an SM.  With bias
+            // and residual, us, this / 64 x 128 / 64 x 64 with two blocks and six stages:
+            // 64 rows, N 4096: K 512 5.0 / 5.8 / 4.9, K 4096 9.9 / 12.0 / 11.3, K 16384
+            // 25.3 / 32.3 / 30.7; 8 rows of 4 experts, N 512, K 7168 12.0 / 15.5 / 14.0;
+            // 64 rows, N 7168, K 2048 7.5 / 8.6 / 8.2; N 9728, K 4096 11.7 / 13.3 / 11.9
+            using Narrow = BlockCfg<64, 64, 3, 8, false, 4>;
+            const int64_t tiles = std::max(g, T / 64 + g / 2) * ((a.N + 127) / 128);
+            return 2 * tiles <= sms ? run_block_gemm<Narrow, true>(a, s)
+                                    : run_block_gemm<Small, true>(a, s);
+        }
 #ifndef MOEQ_FP8_BLOCK_TILE
         // asynchronously with a residual, whose copy it hides, or for very short
         // reductions (against direct stores; 16384 x 4096, K 512: bias 59.5 us / 63.1,
