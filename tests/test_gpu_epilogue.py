@@ -119,6 +119,28 @@ def test_epilogue_is_that_of_the_plain_product(counts, N, K):
     assert torch.equal(c, plain)
 
 
+@pytest.mark.parametrize("K", [16, 128, 144, 256, 384, 400, 512, 528, 1008, 1168, 2176])
+@pytest.mark.parametrize("counts,N", [([1], 8), ([64, 65], 72), ([3, 0, 130], 200), ([64], 9728), ([64], 9736),
+                                      ([70] * 20, 384)])
+def test_every_tail_of_a_reduction_and_the_border_of_the_tiles(counts, N, K):
+    ro, ids, T, E, ins = _case(counts, None, N, K, 0)
+    ins = [t.to(DEV) for t in _scaled(ins, 1.0)]
+    a, b, sa, sb = ins
+    plain = _plain(ins, ro, ids, T, N)
+    res = synth.bf16_normal((T, N), 1.0, seed=5, device=DEV)
+    c, z = torch.full_like(plain, 7.0), torch.full_like(plain, 7.0)
+    moeq.grouped_matmul_fp8_block_epilogue(c, a, b, sa, sb, to_dev_u32(ro), to_dev_i32(ids), z=z, activation="relu",
+                                           residual=res)
+    assert torch.equal(z, plain)
+    # want takes the product rounded to bf16, at most U |product| off, U |plain| (1 + 2 U);
+    # c is the exact product's sum rounded: U |that sum|, itself within the first of want;
+    # 1e-6 for the sum and the product in fp32
+    first = U[BF16] * (1 + 2 * U[BF16]) * np.abs(f64(plain))
+    want = f64(plain).clip(0) + f64(res)
+    tol = first + U[BF16] * (np.abs(want) + first) + 1e-6 * (np.abs(f64(plain)) + np.abs(f64(res)))
+    assert np.all(np.abs(f64(c) - want) <= tol)
+
+
 def test_nonfinite_values_stay_in_their_elements():
     inf, nan = float("inf"), float("nan")
     ro, ids, T, E, ins = _case([40, 30], None, 264, 256, 0)
