@@ -775,12 +775,12 @@ __global__ void __launch_bounds__(kWarps * 32) gate_scored_kernel(ScoredParams p
         rounded ? __fadd_rn(tol, __fmul_rn(fmaxf(fabsf(cv), fabsf(cn)), 0x1p-22f)) : 0.0f;
     bool unsure = !whole && sub < p.top_k && cn > -kInf && (v != vn || b != bn) &&
                   !(__fadd_rn(cv, -cn) > near);
-    // whether what is left may be as good as the last choice: a bound of it is known (an
-    // index took the key's low bits)
+    // whether what is left may be as good as the lane's choice: a bound of it is known (an
+    // index took the key's low bits, so that the last choice need not be the lowest one)
     auto open = [&](uint32_t left) {
         const float bound = __fadd_rn(top, -2.0f * __uint_as_float(left & ~kIdx));
         const float slack = __fmul_rn(__fadd_rn(fabsf(top), fabsf(bound)), 0x1p-22f);
-        return !whole && sub == p.top_k - 1 && id >= 0 && left < none &&
+        return !whole && sub < p.top_k && id >= 0 && left < none &&
                !(__fadd_rn(cv, -bound) > __fadd_rn(near, slack));
     };
     bool all = !whole && top == kInf;
