@@ -633,29 +633,34 @@ __global__ void __launch_bounds__(kWarps * 32) gate_scored_kernel(ScoredParams p
         }
         // (the tokens of a warp may differ in plain: what is between lanes runs for all)
         if (p.topk_groups < p.groups && (p.top2 || BIAS)) {
-            // the border between the last group chosen and the first that is not
+            // The border between the last group chosen and the first that is not.  A group
+            // whose distance from the far side of it is within twice its own error is
+            // not decided.  (Of a chosen and another one in the wrong order, one at least is
+            // that: they lie no further apart than their two errors, and each no further
+            // from the border.  Values that cancel have a larger error than their neighbours.)
             const uint32_t next = lanes_max<L>(key);
-            const uint32_t has = __ballot_sync(kAll, key == next) >> (lane - sub);
-            const int other = __ffs((int)has) - 1;
-            const float size = __fadd_rn(fabsf(g1), two ? fabsf(g2) : 0.0f);
-            const float most =
-                fmaxf(__shfl_sync(kAll, size, at, L), __shfl_sync(kAll, size, other, L));
             const float bound = BIAS || SIGMOID ? tol : 2.0f * kExpTol;
-            const float near = __fadd_rn(2.0f * bound, __fmul_rn(most, 0x1p-20f));
+            const float size = __fadd_rn(fabsf(g1), two ? fabsf(g2) : 0.0f);
+            const float error = v < kInf ? __fmaf_rn(size, 0x1p-21f, bound) : 0.0f;
             const float vb = key_value(border), vn = key_value(next);
-            const bool unsure =
-                (sum || rounded) && next > kNegInfKey && !(__fadd_rn(vb, -vn) > near);
-            if (__any_sync(kAll, unsure)) {
+            const float gap = __fadd_rn(in ? v : vb, in ? -vn : -v);
+            const uint32_t undecided = __ballot_sync(
+                kAll, (sum || rounded) && next > kNegInfKey && v > -kInf && !(gap > 2.0f * error));
+            if (undecided) {
+                const bool unsure = ((undecided >> (lane - sub)) & (kAll >> (32 - L))) != 0u;
+                const uint32_t has = __ballot_sync(kAll, key == next) >> (lane - sub);
+                const int other = __ffs((int)has) - 1;
                 // a third one as near, from either side
                 const int side = a.group == at >> p.lane_shift      ? 1
                                  : a.group == other >> p.lane_shift ? 2
                                                                     : 0;
-                const float wide = __fmaf_rn(size, 0x1p-19f, 2.0f * near);
-                const bool third = side == 0 && a.n > 0 && v > -kInf && unsure &&
-                                   !((in ? v - vn : vb - v) > wide);
-                const bool huge = unsure && !(most < 1e30f);
+                const float most =
+                    fmaxf(__shfl_sync(kAll, error, at, L), __shfl_sync(kAll, error, other, L));
+                const float wide = 2.0f * __fadd_rn(error, most);
+                const bool third = unsure && (side == 0 ? v > -kInf && !(gap > wide)
+                                                        : !(size < 1e30f));
                 const Token token{m, plain, bound};
-                if (__any_sync(kAll, third || huge)) {
+                if (__any_sync(kAll, third)) {
                     in = groups_again(p, row, lane, L, token);
                 } else {
                     uint32_t terms = 0u;

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from fp4_fp8_quantization_gb300 import moeq
+from oracle import layers as L
 from tests._util import need_gpu
 from tests.test_gpu_gate_group import _gate, _want
 
@@ -59,3 +60,38 @@ def test_a_left_over_value_as_good_as_a_choice_that_is_not_the_last():
     x = _logit(value - bias)
     x[:, 0] = 40.0                                         # 1 to the last bit of fp32
     _same_choice(x, k, bias)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("G,size,some", [(3, 2, 1), (8, 2, 4), (8, 4, 3), (16, 2, 5), (5, 3, 2)])
+def test_group_sums_that_cancel(G, size, some, score):
+    """The best two of a group cancel to the rounding of values far larger: it may be
+    better than groups that are not next to it in the order of fp32 sums."""
+    rng = np.random.default_rng(G * size)
+    T, E = 300, G * size
+    large = rng.choice([0.0, 100.0, 1000.0, 10000.0], G)
+    large[:3] = 0.0, 0.0, 1000.0
+    bias = np.full((G, size), -2e4, np.float32)            # what is behind the best two
+    bias[:, 0], bias[:, 1] = large, -large
+    spread = np.where(rng.random(T) < 0.5, 1e-5, 1e-3)[:, None]
+    if score == "sigmoid":
+        x = 0.2 + rng.normal(size=(T, E)) * spread
+    else:
+        x = rng.normal(size=(T, E)) * spread * 10
+    x[0] = 0.0
+    bias[0, 1], bias[1, 1] = 4e-5, 2e-5
+    x[0, 2 * size:2 * size + 2] = 1.1e-4
+    # Where there are more than three groups, the first row's others have the same scores, and
+    # (s + large) + (s - large) is 2 s in the reals for each of them: equal but for the rounding
+    # of 64 bits, which may fall either way.  The row is compared where there are three.
+    x = x[G > 3:].astype(np.float32)
+    for k in (1, min(8, some * size)):
+        _same_choice(x, k, bias.reshape(-1), num_groups=G, topk_groups=some, score=score)
+
+
+def test_the_first_group_of_large_values_in_64_bits():
+    """Sums 1.00004, 1.00002 and 1.000055, the last of 1000.5 and -999.5."""
+    x = np.float32([[0, 0, 0, 0, 1.1e-4, 1.1e-4]])
+    bias = np.float32([0, 4e-5, 0, 2e-5, 1000, -1000])
+    assert L.gate_group_topk(x, 1, bias, groups=3, topk_groups=1)[0].tolist() == [[4]]
+    _same_choice(x, 1, bias, num_groups=3, topk_groups=1)
