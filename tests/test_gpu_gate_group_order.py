@@ -95,3 +95,29 @@ def test_the_first_group_of_large_values_in_64_bits():
     bias = np.float32([0, 4e-5, 0, 2e-5, 1000, -1000])
     assert L.gate_group_topk(x, 1, bias, groups=3, topk_groups=1)[0].tolist() == [[4]]
     _same_choice(x, 1, bias, num_groups=3, topk_groups=1)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_group_sums_past_the_range_of_fp32(score):
+    """Biases of the type's lowest and largest value: -6.8e38 is above a group without an
+    expert, and 6.8e38 above 5e38."""
+    low, inf = float(np.finfo(np.float32).min), float("inf")
+    rng = np.random.default_rng(2)
+    T = 40
+    for values in ([(None, None), (low, low), (0, 0), (None, None)],
+                   [(None, None), (None, low), (low, low), (0, low)],
+                   [(2.5e38, 2.5e38), (-low, -low), (0, 0), (3e38, 1.5e38)],
+                   [(low, low), (low, low), (-low, low), (2.0, -2.0)],
+                   [(inf, 0.0), (-low, -low), (inf, 1.0), (low, low)]):
+        x = rng.normal(size=(T, 4, 3)).astype(np.float32)
+        bias = np.full((4, 3), low, np.float32)
+        x[:, :, 2] = -inf
+        for g, pair in enumerate(values):
+            for j, v in enumerate(pair):
+                if v is None:
+                    x[:, g, j] = -inf
+                else:
+                    bias[g, j] = v
+        for some in (1, 2, 3):
+            for k in (1, 3):
+                _same_choice(x.reshape(T, 12), k, bias.reshape(-1), num_groups=4, topk_groups=some, score=score)
