@@ -91,11 +91,12 @@ __device__ __forceinline__ F2 slope2(F2 z) {
         const F2 zz = mul2(z, z), u = sigma_arg<ACT>(z, zz);
         const F2 e = exp2_2(mul2(abs2(u), f2s(-kLog2e)));
         const F2 r = rcp_2(add2(e, f2s(1.0f))), er = mul2(e, r);
-        // z du / dz
-        F2 zdu = z;
-        if constexpr (ACT == MOEQ_ACT_GELU_TANH)
-            zdu = mul2(z, fma2(zz, f2s(3.0f * kTanhC3), f2s(kTanhC1)));
-        return fma2(zdu, mul2(er, r), by_sign2(u, r, er));
+        const F2 d = mul2(er, r), p = by_sign2(u, r, er);
+        if constexpr (ACT == MOEQ_ACT_SILU) return fma2(z, d, p);
+        // d is 0 from |u| = 88 on; du / dz has to stay finite there (z z is infinite from 2e19
+        // on, z du / dz from 1e13), so that the product is 0 too.  NaN for an infinite or NaN z.
+        const F2 most = f2(fminf(f2_lo(zz), 1e30f), fminf(f2_hi(zz), 1e30f));
+        return fma2(mul2(d, z), fma2(most, f2s(3.0f * kTanhC3), f2s(kTanhC1)), p);
     }
     return f2s(1.0f);
 }
