@@ -62,6 +62,7 @@ __device__ __forceinline__ F2 normal_cdf(F2 z, F2 &e) {
 
 // A NaN stays one.
 __device__ __forceinline__ float relu(float z) { return z <= 0.0f ? 0.0f : z; }
+__device__ __forceinline__ float relu_slope(float z) { return z > 0.0f ? 1.0f : relu(z); }
 
 template <int ACT>
 __device__ __forceinline__ F2 activate2(F2 z) {
@@ -80,8 +81,7 @@ __device__ __forceinline__ F2 activate2(F2 z) {
 // d act / d z
 template <int ACT>
 __device__ __forceinline__ F2 slope2(F2 z) {
-    if constexpr (ACT == MOEQ_ACT_RELU)
-        return f2(f2_lo(z) > 0.0f ? 1.0f : 0.0f, f2_hi(z) > 0.0f ? 1.0f : 0.0f);
+    if constexpr (ACT == MOEQ_ACT_RELU) return f2(relu_slope(f2_lo(z)), relu_slope(f2_hi(z)));
     if constexpr (ACT == MOEQ_ACT_GELU) {
         F2 e;
         const F2 p = normal_cdf(z, e);

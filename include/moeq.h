@@ -718,6 +718,8 @@ moeq_status moeq_grouped_matmul_fp8_block_epilogue(
  *   d_bias      fp32 [num_experts, N] (out) or NULL; an expert without rows gets 0.  With
  *               it, workspace: device memory of moeq_grouped_epilogue_grad_workspace(...)
  *               bytes that no other call in flight uses.
+ * A NaN z makes its d_z NaN, an infinite one too but for relu; an infinity among d_z
+ * gives its block an infinite scale and itself a NaN code.
  * Rows outside the groups are not written and not summed; no output overlaps an input or
  * another output.  N % 8 == 0, with q N % 16 == 0;
  * num_experts <= 65535 (else MOEQ_ERR_UNSUPPORTED). */

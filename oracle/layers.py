@@ -146,7 +146,7 @@ def activate(z, name):
     if name is None:
         return z, one
     if name == "relu":
-        return np.maximum(z, 0.0), (z > 0) * one
+        return np.maximum(z, 0.0), np.where(np.isnan(z), z, (z > 0) * one)
     if name == "silu":
         with np.errstate(over="ignore"):
             p = 1.0 / (1.0 + np.exp(-z))

@@ -83,3 +83,29 @@ def test_activations_of_every_size(act, rows):
             close(c, want, tol)
             if saved:
                 assert torch.equal(z, b.to(BF16).to(DEV).expand(rows, N))
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_gradient_of_nan_and_infinities(act):
+    """A NaN z makes the slope NaN whatever the activation, as it does the activation; an
+    infinite one where the formula has infinity times 0 (all but relu).  A NaN or infinite
+    d_c stays in its element, its column's sum and, as a code, in its element."""
+    inf, nan = float("inf"), float("nan")
+    T, N = 6, 144
+    z = torch.randn(T, N, generator=torch.Generator().manual_seed(1)).to(BF16)
+    dc = torch.randn(T, N, generator=torch.Generator().manual_seed(2)).to(BF16)
+    z[0, 3], z[1, 20], z[2, 37], z[3, 130] = nan, inf, -inf, nan
+    dc[4, 50], dc[4, 60], dc[5, 140] = nan, inf, -inf
+    z[4, 50], z[4, 60], z[5, 140] = 1.0, 2.0, 0.5
+    q, s, dz, db = _grad(dc.to(DEV), z.to(DEV), act)
+    with np.errstate(invalid="ignore"):
+        ref, ref_db, _ = L.epilogue_grad(f64(dc), f64(z) if act else None, act, np.zeros(T, int), 1)
+    got, sums = f64(dz), f64(db)
+    assert np.array_equal(np.isnan(got), np.isnan(ref)) and np.array_equal(np.isinf(got), np.isinf(ref))
+    assert np.array_equal(np.isnan(sums), np.isnan(ref_db)) and np.array_equal(np.isinf(sums), np.isinf(ref_db))
+    if act:
+        assert np.isnan(got[0, 3]) and np.isnan(got[3, 130])
+    fine = np.isfinite(ref)
+    tol = 1.6e-6 * np.abs(f64(dc)[fine]) + (U[BF16] + 2 * EPS) * np.abs(ref[fine])
+    assert np.all(np.abs(got[fine] - ref[fine]) <= tol)
+    assert np.array_equal(np.isnan(F.decode_e4m3(u8(q))), ~fine)   # an infinity's code is NaN
