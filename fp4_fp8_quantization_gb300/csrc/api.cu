@@ -622,7 +622,7 @@ static moeq_status gate_grad_call(moeq_dtype dtype, const void *logits, int64_t 
     if (st != MOEQ_OK) return st;
     if (num_tokens == 0) return MOEQ_OK;
     if (!topk_ids || !d_weights || !d_logits || !aligned16(topk_ids) || !aligned16(d_weights) ||
-        !aligned16(d_logits))
+        !aligned16(d_logits) || (chosen && d_logits == logits))
         return MOEQ_ERR_INVALID_ARG;
     uint32_t *err = device_error_ptr();
     if (!err) return cuda_status(cudaErrorInvalidDevice);

@@ -584,8 +584,8 @@ def gate_group_topk(logits, topk_ids, weights, bias=None, score="sigmoid", num_g
 def gate_group_topk_grad(logits, topk_ids, d_weights, d_logits, score="sigmoid", normalize=True,
                          scale=1.0, stream=None):
     """Gradient of gate_group_topk's weights, the choice taken as fixed: d_logits
-    (out, the logits' dtype, contiguous) from d_weights fp32 [num_tokens, top_k]
-    and the logits and topk_ids of the forward call."""
+    (out, the logits' dtype, contiguous, not over the logits) from d_weights fp32
+    [num_tokens, top_k] and the logits and topk_ids of the forward call."""
     p, stride, dev = _matrix(logits, "logits")
     T, E = logits.shape
     k = _choices(topk_ids, T)

@@ -528,8 +528,9 @@ moeq_status moeq_gate_group_topk(moeq_dtype dtype, const void *logits, int64_t l
  *   sigmoid, normalize == 0:  d_logits_{i_r} = g_r * s (1 - s)
  *   sigmoid, normalize != 0:  d_logits_{i_r} = q_r * (g_r - <q, g>) * (1 - s)
  *   softmax, normalize != 0:  d_logits_{i_r} = q_r * (g_r - <q, g>)
- * and 0 elsewhere: only the chosen logits are read.  Softmax without normalize is
- * moeq_gate_topk_grad.  Arguments as there. */
+ * and 0 elsewhere: only the chosen logits are read, after a row was zeroed, so that
+ * d_logits may not lie over logits.  Softmax without normalize is moeq_gate_topk_grad.
+ * Arguments as there. */
 moeq_status moeq_gate_group_topk_grad(moeq_dtype dtype, const void *logits, int64_t logit_stride,
                                       int64_t num_tokens, int32_t num_experts, moeq_score score,
                                       int32_t top_k, int32_t normalize, float scale,
