@@ -21,13 +21,15 @@
 // bits of max c - c with the lane and index in the low bits (of 16-bit logits without
 // a bias: their whole images): those of the best values, close to the maximum, keep
 // most of their digits, so that a round of the choice is one integer minimum over the
-// lanes.  Scores next to one another are decided as 64 bits would: c in fp32 is off by
+// lanes.  Scores next to one another are decided as the reals would: c in fp32 is off by
 // a bound known beforehand, and a token in which two values that the choice depends on
 // are closer than that (about one in a thousand) looks at those again as sums of two
-// floats.
+// floats (within 2^-44).
 //
-// Bound by the pipe of integer minima and comparisons (46 %) and the issue slots (57 %) at
-// four warps a scheduler: some 390 instructions a token of 256 experts.  65537 x 256, 8
+// Bound by a token's chain of dependent steps: no pipe is full (that of integer minima and
+// comparisons 46 %, the issue slots 57 %) at four warps a scheduler, which a CTA of 16 tokens
+// leaves with its bias, rows and barrier before it to wait for.  Some 390 instructions a
+// token of 256 experts.  65537 x 256, 8
 // groups of which 4, top-8, sigmoid and bias: forward 35 us fp32, 33 bf16 (10 and 5 of
 // memory), gradient 15 (10); 65536 x 128, one group, top-4, 18; 9999 x 160 softmax, 8
 // groups, top-6, 7.6; 64 x 256 2.9.  A token that is looked at again takes 3 us more (in

@@ -878,7 +878,8 @@ cudaError_t launch_gemm_fp8_block(const GemmBlockArgs &a, cudaStream_t s) {
             // and residual, us, this / 64 x 128 / 64 x 64 with two blocks and six stages:
             // 64 rows, N 4096: K 512 5.0 / 5.8 / 4.9, K 4096 9.9 / 12.0 / 11.3, K 16384
             // 25.3 / 32.3 / 30.7; 8 rows of 4 experts, N 512, K 7168 12.0 / 15.5 / 14.0;
-            // 64 rows, N 7168, K 2048 7.5 / 8.6 / 8.2; N 9728, K 4096 11.7 / 13.3 / 11.9
+            // 64 rows, N 7168, K 2048 7.5 / 8.6 / 8.2; N 9728, K 4096 11.7 / 13.3 / 11.9.
+            // (The product without epilogue has no such form yet: 64 rows, N 4096, K 4096 10.5.)
             using Narrow = BlockCfg<64, 64, 3, 8, false, 4>;
             const int64_t tiles = std::max(g, T / 64 + g / 2) * ((a.N + 127) / 128);
             return 2 * tiles <= sms ? run_block_gemm<Narrow, true>(a, s)

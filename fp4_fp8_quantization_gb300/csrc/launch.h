@@ -156,8 +156,9 @@ struct EpilogueGradArgs {
 cudaError_t launch_epilogue_grad(const EpilogueGradArgs &a, cudaStream_t s);
 // Its workspace: a table of tiles for each group, then one row of N sums for each
 // tile of a group's rows: as many rows as leave the machine enough tiles (32768 x 4096,
-// 64 uneven groups: 128 rows 150 us, 256 136, 512 129; 65536 x 1536, 128 groups: 256 112,
-// 512 115).
+// 64 even groups: 256 rows 130 us, 512 127, uneven ones 134, 137; 65536 x 4096, 64 groups:
+// 247, 238; 131072 x 2048, 128 groups: 275, 266; 65536 x 7168: 411, 395; below the border,
+// 65536 x 1536, 128 groups: 112, 115).
 inline int64_t epilogue_grad_rows(int64_t rows, int64_t N) {
     const int64_t n = rows * N;
     return n < (int64_t)1 << 22   ? 64

@@ -498,10 +498,12 @@ moeq_status moeq_gate_topk_grad(moeq_dtype dtype, const void *logits, int64_t lo
  *   normalize == 0:  w_r = scale * s_{i_r}
  *   normalize != 0:  w_r = scale * s_{i_r} / sum over the choices of s  (0 where it is 0)
  * The bias decides the choice and does not enter the weights; without one (NULL) c is
- * ordered as the logits are.  The order is that of c in 64 bits, whatever its fp32
- * rounding (a score below 2^-126 counts as 0; sums that are equal but for the rounding of
- * 64 bits, as of sigmoid(x) and sigmoid(-x), may fall either way); weights are fp32, from s within 4 ulp
- * (sigmoid) or as in moeq_gate_topk.
+ * ordered as the logits are.  The order is that of the real values, whatever their rounding
+ * to fp32, of experts' c and of groups' sums alike, where they are further apart than 2^-42 of
+ * the largest score or bias that is in them; what is closer may fall either way, and
+ * equal logits with equal biases tie (a score below 2^-126 counts as 0).  Weights are
+ * fp32, from s within 4 ulp (sigmoid; a score below 2^-126 has the few bits that fp32 has
+ * there) or as in moeq_gate_topk.
  *   logits      dtype [num_tokens, num_experts], row stride logit_stride elements.
  *   bias        fp32 [num_experts] or NULL.
  *   topk_ids    int32 [num_tokens, top_k] (out);  weights fp32 [num_tokens, top_k] (out).
@@ -619,7 +621,8 @@ moeq_status moeq_quantize_fp8_block_weight(const void *w, int64_t num_experts, i
  *   rstd = 1 / sqrt(mean of h^2 + eps),  v = (h * rstd) * weight
  *   y = v, rounded to the dtype;  q, scales = v in E4M3 by the rule of
  *       moeq_quantize_fp8_block, from fp32 (not from y)
- * fp32 throughout, the squares' sum too (squares past its range give an infinite sum).
+ * fp32 throughout, the squares' sum too (squares past its range give an infinite sum, those
+ * below 2^-126 lose bits).
  *   x, residual dtype [rows, K], row strides x_stride, residual_stride elements.
  *   weight      dtype [K].
  *   h, y        dtype [rows, K] (out); h required with a residual and only then.
