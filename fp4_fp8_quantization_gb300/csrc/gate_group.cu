@@ -27,8 +27,8 @@
 // floats (within 2^-44).
 //
 // Bound by a token's chain of dependent steps: no pipe is full (that of integer minima and
-// comparisons 46 %, the issue slots 57 %) at four warps a scheduler, which a CTA of 16 tokens
-// leaves with its bias, rows and barrier before it to wait for.  Some 390 instructions a
+// comparisons 42 %, the issue slots 58 %) at four warps a scheduler, which a CTA of 16 tokens
+// leaves with its bias, rows and barrier before it to wait for.  Some 370 instructions a
 // token of 256 experts.  65537 x 256, 8
 // groups of which 4, top-8, sigmoid and bias: forward 35 us fp32, 33 bf16 (10 and 5 of
 // memory), gradient 15 (10); 65536 x 128, one group, top-4, 18; 9999 x 160 softmax, 8
